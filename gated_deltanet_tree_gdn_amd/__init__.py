@@ -338,3 +338,8 @@ def verify(q, k, v, g, beta, parent, S0, o=None, stream=None, ctx: Optional[GdnC
     tensors' shapes; returns ``(o, ctx)`` so the caller can commit later."""
     ctx = ctx or GdnContext.for_tensors(q, v, parent)
     return gdn_tree_verify(ctx, q, k, v, g, beta, parent, S0, o=o, stream=stream), ctx
+
+
+# the operators around the tree verify (gdn_layer.h)
+from .layer import (LAYER_EXPORTS, gdn_add_norm, gdn_decode, gdn_gated_norm, gdn_linear,  # noqa: E402
+                    gdn_prefill, gdn_prefill_workspace_bytes)

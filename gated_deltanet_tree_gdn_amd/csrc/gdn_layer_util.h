@@ -1,0 +1,97 @@
+// gdn_layer_util.h -- loads, stores, sums over lanes and gate functions shared
+// by the kernels of gdn_layer.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gdn_layer.h"
+
+namespace gdn {
+
+__host__ __device__ constexpr int dtype_size(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
+
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+
+// Two fp32 values as packed bf16, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    bf16x2 v;
+    v[0] = static_cast<__bf16>(a);
+    v[1] = static_cast<__bf16>(b);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Element i of an array whose dtype is known at run time (uniform over the
+// wavefront, so the branch costs a scalar compare).
+__device__ __forceinline__ float load1(const void* p, int dtype, int64_t i) {
+    if (dtype == GDN_BF16)
+        return __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+    return static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ void store1(void* p, int dtype, int64_t i, float x) {
+    if (dtype == GDN_BF16)
+        static_cast<__bf16*>(p)[i] = static_cast<__bf16>(x);
+    else
+        static_cast<float*>(p)[i] = x;
+}
+
+// Elements i .. i + 7 (i a multiple of 8 elements from a 16-byte boundary).
+__device__ __forceinline__ void load8(const void* p, int dtype, int64_t i, float (&x)[8]) {
+    if (dtype == GDN_BF16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = f[0], b = f[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ void store8(void* p, int dtype, int64_t i, const float (&x)[8]) {
+    if (dtype == GDN_BF16) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        f[0] = make_float4(x[0], x[1], x[2], x[3]);
+        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over aligned groups of W lanes, the result in every lane: exchanges
+// with lanes xor 1 and xor 2 (quad permutes), then mirrored halves and rows
+// of 16, then across rows.
+template <int W>
+__device__ __forceinline__ float lane_sum(float x) {
+    if constexpr (W >= 2) x += dpp<0xB1>(x);
+    if constexpr (W >= 4) x += dpp<0x4E>(x);
+    if constexpr (W >= 8) x += dpp<0x141>(x);
+    if constexpr (W >= 16) x += dpp<0x140>(x);
+    if constexpr (W >= 32) x += __shfl_xor(x, 16);
+    if constexpr (W >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
+__device__ __forceinline__ float sigmoidf(float a) { return 1.0f / (1.0f + __expf(-a)); }
+
+__device__ __forceinline__ float activate(int act, float a) {
+    switch (act) {
+        case GDN_ACT_SILU: return a * sigmoidf(a);
+        case GDN_ACT_GELU: return 0.5f * a * (1.0f + erff(a * 0.70710678118654752f));
+        case GDN_ACT_SIGMOID: return sigmoidf(a);
+        default: return a;
+    }
+}
+
+}  // namespace gdn

@@ -1,0 +1,935 @@
+// gdn_prefill.hip -- the delta rule over packed prompts, in chunks of 64
+// tokens (bf16 q/k/v).
+//
+// Inside a chunk that starts from the state S (d_v x d_k), with
+// G_i = g_1 + .. + g_i, gamma_i = e^{G_i} and u_i = beta_i (v_i - alpha_i S_{i-1} k_i):
+//
+//     (I + A) U = diag(beta) (V - diag(gamma) K S^T),  A_ij = beta_i e^{G_i - G_j} k_i.k_j  (j < i)
+//     O     = diag(gamma) Q S^T + M U,                 M_ij = e^{G_i - G_j} q_i.k_j         (j <= i)
+//     S_new = gamma_64 S + sum_j e^{G_64 - G_j} u_j k_j^T.
+//
+// T = (I + A)^-1 diag(beta) and M do not depend on S, so two kernels run:
+//  1. prep_kernel, parallel over (chunk, key head): T and M as MFMA operands,
+//     and the chunk's scalars, into the workspace;
+//  2. chain_kernel, one workgroup per (sequence, value head, slice of d_v):
+//     the chunks in order with the state in registers.
+// Rows of d_v are independent of each other, so slices need no exchange.
+//
+// Chunk slots: sequence b's chunks are numbered from cu[b] / 64 + b, which
+// leaves every sequence room without a prefix sum over lengths (at most
+// T / 64 + B slots).
+//
+// Precision: q, k and v are exact bf16 operands.  fp32 operands are split
+// into bf16 parts: S, R = V - gamma K S^T, the off-diagonal part of T, and M
+// into two (about 17 bits, relative error below 1e-6 rms), the decayed U that
+// is accumulated into the state into three (24 bits).  The diagonal of T acts
+// in fp32.  Sums, states, T and the decay are fp32, G is fp64 (a difference
+// G_i - G_j stays exact to fp32 however far the chunk has decayed).
+
+#include <type_traits>
+
+#include "gdn_layer_internal.h"
+#include "gdn_layer_util.h"
+#include "gdn_mfma.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kC = 64;  // tokens per chunk
+
+// What prep_kernel hands to chain_kernel, all in the order in which a
+// wavefront's lanes read it (16 bytes per lane, 1 KiB per fragment).  Tokens
+// of a 32-token step sit at k-slot j of lane group g as token
+// 16 (j / 4) + 4 g + j % 4, the order in which accumulators hold rows, so that
+// a product's result is the next product's operand without moving lanes.
+struct PrepLayout {
+    size_t t, m, sc, info, total;
+};
+// T and M: the (row tile, 32-token step) pairs that reach the lower triangle.
+constexpr int kPairs = 6;
+__host__ __device__ constexpr int pair_at(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
+
+__host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
+    const size_t slots = size_t(d.T) / kC + d.B, heads = slots * d.H_v;
+    PrepLayout l;
+    l.t = 0;
+    l.m = l.t + heads * kPairs * 2 * 1024;
+    l.sc = l.m + heads * kPairs * 2 * 1024;
+    l.info = l.sc + heads * kC * sizeof(float4);
+    l.total = (l.info + heads * sizeof(float2) + 255) & ~size_t(255);
+    return l;
+}
+
+struct ChunkArgs {
+    SeqArgs s;
+    uint4* t;
+    uint4* m;
+    float4* sc;    // per token: gamma |k|^-1, beta, scale gamma |q|^-1, e^{G_64 - G} |k|^-1 (norms 1 unless asked for)
+    float2* info;  // gamma_64, first token with a non-finite k, g or beta (kC if none, as int bits)
+    int slots;
+};
+
+struct Range {
+    int64_t start;
+    int len;
+    bool ok;
+};
+__device__ __forceinline__ Range seq_range(const SeqArgs& a, int b) {
+    const int64_t s = a.cu[b], e = a.cu[b + 1];
+    const bool ok = 0 <= s && s <= e && e <= a.d.T;
+    return {ok ? s : 0, ok ? int(e - s) : 0, ok};
+}
+
+__device__ __forceinline__ int slot_base(const SeqArgs& a, int b) {
+    const int s = a.cu[b];
+    return (s < 0 ? 0 : s > a.d.T ? a.d.T : s) / kC + b;
+}
+
+// The sequence that a chunk slot belongs to: the last b with base(b) <= slot,
+// 64 candidates at a time.
+__device__ __forceinline__ int find_seq(const SeqArgs& a, int slot) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.d.B;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int b = lo + lane * step;
+        const bool le = lane * step < n && slot_base(a, b) <= slot;
+        const int last = 63 - __builtin_clzll(__ballot(le) | 1ull);
+        lo += last * step;
+        n = min(step, n - last * step);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void split2(float x, __bf16& hi, __bf16& lo) {
+    hi = static_cast<__bf16>(x);
+    lo = static_cast<__bf16>(x - static_cast<float>(hi));
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+// Orders LDS between the wavefronts of a workgroup without waiting for
+// global loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Orders LDS between the lanes of one wavefront.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// ----------------------------------------------------------------------------
+// 1. per (chunk, key head)
+// ----------------------------------------------------------------------------
+
+constexpr int kGramLd = 68;  // row stride of the Gram matrix in LDS: rows 4 apart fall on different banks
+constexpr int kTriLd = 20;   // row stride of a 16 x 16 block
+
+// e^{x} for a difference of log-decays held times log2(e).
+__device__ __forceinline__ float exp_diff(double hi, double lo) {
+    return __builtin_amdgcn_exp2f(static_cast<float>(hi - lo));
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
+    constexpr int KS = DK / 32;
+    constexpr int kKl = 4 * KS * 64 * 16, kTri = 4 * 4 * 16 * kTriLd * 4;
+    // K rows as fragments [token tile][step][lane]; then per wavefront the
+    // diagonal blocks of A and of T
+    __shared__ __align__(16) char buf[kKl > kTri ? kKl : kTri];
+    __shared__ __align__(16) float gram[kC * kGramLd];  // |k_i|^-1 |k_j|^-1 k_i.k_j, j's tile <= i's
+    __shared__ double gcum[2][kC];                      // G log2(e) of two value heads
+    __shared__ __align__(16) float bet[2][kC];
+    __shared__ __align__(16) float rks[kC], rqs[kC];
+    __shared__ unsigned badk[2];  // tokens whose k is not finite, a bit each
+    const SeqArgs& a = c.s;
+    const gdn_seq_dims& d = a.d;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+    const int slot = blockIdx.x, hk = blockIdx.y;
+    const int b = find_seq(a, slot);
+    const Range seq = seq_range(a, b);
+    const int ch = slot - slot_base(a, b);
+    if (ch < 0 || ch * kC >= seq.len) return;
+    const int64_t t0 = seq.start + int64_t(ch) * kC;
+    const int n = min(kC, seq.len - ch * kC);
+    auto kl = [&](int tile, int step, int l) { return reinterpret_cast<uint4*>(buf) + (tile * KS + step) * 64 + l; };
+
+    // K and Q rows of token tile w: lane (row col, elements 32 s + 8 g ..)
+    const int row = 16 * w + col;
+    const bool in = row < n;
+    const int64_t tr = t0 + (in ? row : 0);
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + tr * d.k_stride + int64_t(hk) * DK + 8 * g;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + tr * d.q_stride + int64_t(hk) * DK + 8 * g;
+    uint4 kf[KS], qf[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        kf[s] = *reinterpret_cast<const uint4*>(kp + 32 * s);
+        qf[s] = *reinterpret_cast<const uint4*>(qp + 32 * s);
+    }
+    // the gates of the first two value heads, a token per lane
+    const int group = d.H_v / d.H_k;
+    const int64_t gi = (t0 + min(lane, n - 1)) * d.H_v + hk * group;
+    float gv = a.g[gi + min(w >> 1, group - 1)], bv = a.beta[gi + min(w >> 1, group - 1)];
+    if (threadIdx.x < 2) badk[threadIdx.x] = 0;
+    float kk = 0.0f, qq = 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const uint32_t ku[4] = {kf[s].x, kf[s].y, kf[s].z, kf[s].w}, qu[4] = {qf[s].x, qf[s].y, qf[s].z, qf[s].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float k0 = bf16_lo(ku[j]), k1 = bf16_hi(ku[j]), q0 = bf16_lo(qu[j]), q1 = bf16_hi(qu[j]);
+            kk += k0 * k0 + k1 * k1;
+            qq += q0 * q0 + q1 * q1;
+        }
+    }
+    kk += __shfl_xor(kk, 16);
+    kk += __shfl_xor(kk, 32);
+    qq += __shfl_xor(qq, 16);
+    qq += __shfl_xor(qq, 32);
+    __syncthreads();
+    // a non-finite k is taken out of the chunk here and its token marked
+    const bool kbad = in && !finite(kk);
+    if (kbad && g == 0) atomicOr(&badk[row >> 5], 1u << (row & 31));
+    if (!in || kbad)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[s] = make_uint4(0, 0, 0, 0);
+    if (!in)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = make_uint4(0, 0, 0, 0);
+    const float rk = d.qk_l2norm ? 1.0f / sqrtf((kbad ? 0.0f : kk) + d.l2_eps) : 1.0f;
+    const float rq = d.q_scale * (d.qk_l2norm ? 1.0f / sqrtf(qq + d.l2_eps) : 1.0f);
+    if (g == 0) {
+        rks[row] = in && !kbad ? rk : 0.0f;
+        rqs[row] = in ? rq : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) *kl(w, s, lane) = kf[s];
+    __syncthreads();
+
+    // Transposed products: accumulators hold column i = 16 w + col, rows
+    // j = 16 jt + 4 g + r.
+    f32x4 qk[4];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+        f32x4 kkt = {0.0f, 0.0f, 0.0f, 0.0f};
+        qk[jt] = kkt;
+        if (jt <= w) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bf16x8 kj = __builtin_bit_cast(bf16x8, *kl(jt, s, lane));
+                kkt = mfma(kj, __builtin_bit_cast(bf16x8, kf[s]), kkt);
+                qk[jt] = mfma(kj, __builtin_bit_cast(bf16x8, qf[s]), qk[jt]);
+            }
+            const float4 rj = *reinterpret_cast<const float4*>(&rks[16 * jt + 4 * g]);
+            const float rr[4] = {rj.x, rj.y, rj.z, rj.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                kkt[r] *= rks[row] * rr[r];
+                qk[jt][r] *= rqs[row] * rr[r];
+            }
+            *reinterpret_cast<f32x4*>(&gram[row * kGramLd + 16 * jt + 4 * g]) = kkt;
+        }
+    }
+
+    // The value heads of this key head, two at a time, two wavefronts each:
+    // both invert the diagonal blocks, the first then forms rows 0 .. 47 of T,
+    // the second rows 48 .. 63.
+    __syncthreads();
+    float(*tri)[16][kTriLd] = reinterpret_cast<float(*)[16][kTriLd]>(buf + w * (kTri / 4));
+    const int hw = w >> 1, part = w & 1;
+    for (int h0 = 0; h0 < group; h0 += 2) {
+        const int nh = min(2, group - h0);
+        if (hw < nh) {
+            const int h = hk * group + h0 + hw;
+            const int64_t sh = int64_t(slot) * d.H_v + h;
+            if (h0 > 0) {
+                gv = a.g[gi + h0 + hw];
+                bv = a.beta[gi + h0 + hw];
+            }
+            // G and the scalars: lane = token
+            if (lane >= n) gv = bv = 0.0f;
+            const bool gbad = !(gv < __builtin_inff()) || !finite(bv);
+            const unsigned long long bad = (static_cast<unsigned long long>(badk[1]) << 32 | badk[0]) | __ballot(gbad);
+            const int first = bad ? __builtin_ctzll(bad) : kC;
+            if (bad >> lane & 1) bv = 0.0f;
+            // exp(g) is zero below -104, so larger decays would only cost precision
+            gv = gbad ? 0.0f : fmaxf(gv, -104.0f);
+            double G = gv * 1.4426950408889634;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const double y = __shfl_up(G, o);
+                if (lane >= o) G += y;
+            }
+            const double G63 = __shfl(G, 63);
+            if (part == 0) {
+                gcum[hw][lane] = G;
+                bet[hw][lane] = bv;
+                const float gam = __builtin_amdgcn_exp2f(static_cast<float>(G));
+                c.sc[sh * kC + lane] =
+                    make_float4(gam * rks[lane], bv, gam * rqs[lane], exp_diff(G63, G) * rks[lane]);
+                if (lane == 0)
+                    c.info[sh] = make_float2(__builtin_amdgcn_exp2f(static_cast<float>(G63)),
+                                             __builtin_bit_cast(float, first));
+            }
+        }
+        __syncthreads();
+        if (hw < nh) {
+            const int64_t sh = int64_t(slot) * d.H_v + hk * group + h0 + hw;
+            const double* G = gcum[hw];
+            const float* be = bet[hw];
+            // diagonal blocks of A: lane group g = block, col = column
+            const double Gc = G[16 * g + col];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = 16 * g + i;
+                tri[g][i][col] = i > col ? be[r] * exp_diff(G[r], Gc) * gram[r * kGramLd + 16 * g + col] : 0.0f;
+            }
+            wave_lds_fence();
+            // their inverses by forward substitution, one column per lane
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == col ? 1.0f : 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int m = 0; m < i; m += 4) {
+                    const float4 am = *reinterpret_cast<const float4*>(&tri[g][i][m]);
+                    s0 -= am.x * x[m];
+                    if (m + 1 < i) s1 -= am.y * x[m + 1];
+                    if (m + 2 < i) s0 -= am.z * x[m + 2];
+                    if (m + 3 < i) s1 -= am.w * x[m + 3];
+                }
+                x[i] = s0 + s1;
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) tri[g][i][col] = x[i];
+            wave_lds_fence();
+            // Row block i of T, transposed: X[j] = T_ij^T = -T_jj^T sum_m A_mj^T T_im^T
+            // as accumulators (column = row of block i, rows = columns of block j);
+            // then T diag(beta) without its diagonal as fragments of tile i's rows.
+            uint4* tp = c.t + sh * kPairs * 2 * 64;
+            auto row_block = [&](auto ii) {
+                constexpr int i = ii.value;
+                f32x4 X[i + 1];
+                X[i] = *reinterpret_cast<const f32x4*>(&tri[i][col][4 * g]);
+#pragma unroll
+                for (int j = i - 1; j >= 0; --j) {
+                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, out = acc;
+                    const double Gj = G[16 * j + col];
+#pragma unroll
+                    for (int m = j + 1; m <= i; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int tm = 16 * m + 4 * g + r;
+                            acc = mfma_f32(be[tm] * exp_diff(G[tm], Gj) * gram[tm * kGramLd + 16 * j + col], X[m][r], acc);
+                        }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) out = mfma_f32(-tri[j][4 * g + r][col], acc[r], out);
+                    X[j] = out;
+                }
+#pragma unroll
+                for (int s = 0; s <= i / 2; ++s) {
+                    bf16x8 hi, lo;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int jt = 2 * s + half;
+                        const f32x4 bj = *reinterpret_cast<const f32x4*>(&be[16 * jt + 4 * g]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            float v = 0.0f;
+                            if (jt < i) v = X[jt < i ? jt : i][r] * bj[r];
+                            if (jt == i) v = 4 * g + r < col ? X[i][r] * bj[r] : 0.0f;
+                            __bf16 h1, l1;
+                            split2(v, h1, l1);
+                            hi[4 * half + r] = h1;
+                            lo[4 * half + r] = l1;
+                        }
+                    }
+                    uint4* p = tp + pair_at(i, s) * 2 * 64 + lane;
+                    p[0] = __builtin_bit_cast(uint4, hi);
+                    p[64] = __builtin_bit_cast(uint4, lo);
+                }
+            };
+            if (part == 0) {
+                row_block(std::integral_constant<int, 0>());
+                row_block(std::integral_constant<int, 1>());
+                row_block(std::integral_constant<int, 2>());
+            } else {
+                row_block(std::integral_constant<int, 3>());
+            }
+        }
+        // M of both heads: rows of token tile w
+        for (int hh = 0; hh < nh; ++hh) {
+            const int64_t sh = int64_t(slot) * d.H_v + hk * group + h0 + hh;
+            const double Gi = gcum[hh][row];
+            uint4* mp = c.m + sh * kPairs * 2 * 64;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (2 * s > w) continue;
+                bf16x8 hi, lo;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int jt = 2 * s + (j >> 2), tok = 16 * jt + 4 * g + (j & 3);
+                    float v = 0.0f;
+                    if (jt <= w && tok <= row) v = exp_diff(Gi, gcum[hh][tok]) * qk[jt][j & 3];
+                    __bf16 h1, l1;
+                    split2(v, h1, l1);
+                    hi[j] = h1;
+                    lo[j] = l1;
+                }
+                uint4* p = mp + pair_at(w, s) * 2 * 64 + lane;
+                p[0] = __builtin_bit_cast(uint4, hi);
+                p[64] = __builtin_bit_cast(uint4, lo);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ----------------------------------------------------------------------------
+// 2. per (sequence, value head, slice of d_v)
+// ----------------------------------------------------------------------------
+
+// NCT adjacent bf16 values.
+template <int NCT>
+struct ValueBits;
+template <>
+struct ValueBits<1> {
+    typedef uint16_t type;
+    static __device__ __forceinline__ float at(type u, int) { return bf16_lo(u); }
+};
+template <>
+struct ValueBits<2> {
+    typedef uint32_t type;
+    static __device__ __forceinline__ float at(type u, int ct) { return ct ? bf16_hi(u) : bf16_lo(u); }
+};
+
+// A load from a uniform base and a lane's 32-bit byte offset.
+template <typename T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t off) {
+    return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+
+// Four 16-bit elements of each lane, transposed over groups of 16 lanes.
+__device__ __forceinline__ uint2 read_tr(const uint2* p) {
+    typedef short s16x4v __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v*)(p)));
+}
+
+// Rows row0 .. row0 + 3 of an output tile: those below n.
+template <typename T, int NCT>
+__device__ __forceinline__ void store_rows(T* base, uint32_t off, uint32_t ld, int left, const f32x4 (&x)[NCT]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (r < left) {
+            T* p = base + (off + r * ld);
+            if constexpr (sizeof(T) == 2) {
+                if constexpr (NCT == 1)
+                    *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(x[0][r]);
+                else
+                    *reinterpret_cast<uint32_t*>(p) = pack_bf16(x[0][r], x[1][r]);
+            } else {
+                if constexpr (NCT == 1)
+                    *p = x[0][r];
+                else
+                    *reinterpret_cast<float2*>(p) = make_float2(x[0][r], x[1][r]);
+            }
+        }
+}
+
+// Rows of K and Q are loaded in the order of memory (a wavefront's load covers
+// whole rows; loading the MFMA layout directly would touch 16 rows per 256
+// bytes) and turned into operands in LDS.  The 16-byte pieces of a row are
+// permuted so that both reads below use all banks: a fragment (piece p of 16
+// rows) and a transposing read (4 adjacent pieces of 4 adjacent rows).
+template <int DK>
+__device__ __forceinline__ int piece_at(int row, int p) {
+    constexpr int P = DK / 8;
+    const int f = P == 16 ? ((row >> 2) & 3) | (row & 3) << 2 : ((row >> 2) & 3) | (row >> 1 & 1) << 2;
+    return row * P + (p ^ f);
+}
+
+// The 16 rows of one token tile: load number j of lane l is piece l % P of row
+// j 64 / P + l / P.
+template <int DK>
+struct TileRows {
+    static constexpr int P = DK / 8, L = DK / 32, RPL = 64 / P;  // pieces per row, loads, rows per load
+    uint4 x[L];
+    __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int last, int tile, int lane) {
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const uint32_t row = min(16 * tile + j * RPL + lane / P, last);
+            x[j] = load_at<uint4>(base, (row * uint32_t(stride) + 8 * (lane % P)) * 2);
+        }
+    }
+    __device__ __forceinline__ void put(uint4* tile_lds, int lane) const {
+#pragma unroll
+        for (int j = 0; j < L; ++j) tile_lds[piece_at<DK>(j * RPL + lane / P, lane % P)] = x[j];
+    }
+};
+
+// LDS of one chain workgroup: operands of the products over the state and over
+// tokens as [step][part][column tile][lane].
+template <int DK, int NCT>
+struct ChainLds {
+    uint4 K[4][16 * DK / 8];       // rows of K by token tile, pieces permuted
+    uint4 Q[4][16 * DK / 8];       // rows of Q, each tile read by its own wavefront only
+    uint4 S[DK / 32][2][NCT][64];  // state: hi, lo
+    uint4 R[2][2][NCT][64];        // R: hi, lo
+    uint4 D[2][3][NCT][64];        // decayed U: three parts
+    f32x4 U[4][NCT][64];           // U in fp32, rows of token tile [i] as accumulated
+    int4 marks;                    // wavefront i's R has a value that is not finite
+    uint8_t badrow[4][NCT][64];    // its rows, where marked
+};
+
+// The first row of each of the lane's columns that is not finite; kC if none.
+template <int DK, int NCT>
+__device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int chunk_first, int col, int (&first)[NCT]) {
+    const int marks[4] = {l.marks.x, l.marks.y, l.marks.z, l.marks.w};
+    for (int ct = 0; ct < NCT; ++ct) {
+        first[ct] = chunk_first;
+        for (int w = 0; w < 4; ++w)
+            if (marks[w])
+                for (int g = 0; g < 4; ++g) {
+                    const unsigned m = l.badrow[w][ct][16 * g + col];
+                    if (m) first[ct] = min(first[ct], 16 * w + 4 * g + __builtin_ctz(m));
+                }
+    }
+}
+
+// Eight wavefronts: 0 .. 3 carry the state from chunk to chunk, 4 .. 7 form
+// the outputs beside them.  Three barriers per chunk:
+//   chain:  state operands | K S^T, R      | U, K^T operands    | state update, next K
+//   output:                | Q S^T, store  | next Q             | M U
+// Wavefront i of either kind owns token tile i (16 rows of the chunk); chain
+// wavefront i also owns d_k / 4 elements of the state's rows.
+//
+// NCT column tiles of 16 values per workgroup: lane column `col` of tile ct is
+// value NCT col + ct of the slice, so a lane's NCT values are adjacent.
+template <int DK, int NCT>
+__global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
+    constexpr int KS = DK / 32, TPW = DK / 64;
+    __shared__ ChainLds<DK, NCT> l;
+    const SeqArgs& a = c.s;
+    const gdn_seq_dims& d = a.d;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
+    // Workgroups go to the 8 XCDs in turn: the slices and value heads of one
+    // (sequence, key head) are numbered onto one XCD, whose L2 then serves
+    // their common K, Q, K^T, T and M.
+    const int group = d.H_v / d.H_k, slices = d.d_v / (16 * NCT), per = group * slices;
+    const int j8 = blockIdx.x >> 3, item = (blockIdx.x & 7) + 8 * (j8 / per), part = j8 % per;
+    if (item >= d.B * d.H_k) return;
+    const int b = item / d.H_k, hk = item % d.H_k, h = hk * group + part / slices, v0 = (part % slices) * 16 * NCT;
+
+    const Range seq = seq_range(a, b);
+    const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
+    const int64_t sh0 = int64_t(base) * d.H_v + h;
+    const float2* info_p = c.info + sh0;
+
+    if (wave >= 4) {
+        // ---- outputs ----
+        if (chunks == 0) return;
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq.start * d.q_stride + int64_t(hk) * DK;
+        const uint4* mp = c.m + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
+        const float4* sp = c.sc + sh0 * kC + 16 * w;
+        const int64_t m_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC;
+        const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + 4 * g) * ld + NCT * col;
+        const int64_t o0 = (seq.start * d.H_v + h) * d.d_v + v0;
+        uint4 mf[2][2];
+        TileRows<DK> qr;
+        float cq[4];
+        auto load_q = [&](int ch) { qr.load(qp + ch * (kC * d.q_stride), d.q_stride, seq.len - ch * kC - 1, w, lane); };
+        auto load_c = [&](int ch) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                cq[r] = load_at<float>(reinterpret_cast<const float*>(sp + ch * s_step + r) + 2, g * 64);
+        };
+        auto load_m = [&](int ch) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)  // tiles 0 and 1 have one step: read again rather than branch
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    mf[s][p] = load_at<uint4>(mp + ch * m_step + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+        };
+        load_q(0);
+        qr.put(l.Q[w], lane);
+        load_c(0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_q(min(1, chunks - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        load_m(0);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 O[NCT];
+        int first[NCT];
+        bool poisoned = false;
+        auto store = [&](int ch) {
+            if (poisoned)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * w + 4 * g + r >= first[ct]) O[ct][r] = __builtin_nanf("");
+            const int64_t at = o0 + int64_t(ch) * kC * ld;
+            const int left = seq.len - ch * kC - (16 * w + 4 * g);
+            if (d.o_dtype == GDN_BF16)
+                store_rows<uint16_t, NCT>(static_cast<uint16_t*>(a.o) + at, o_off, ld, left, O);
+            else
+                store_rows<float, NCT>(static_cast<float*>(a.o) + at, o_off, ld, left, O);
+        };
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int next = min(ch + 1, chunks - 1);
+            lds_barrier();  // state operands written
+            f32x4 Qh[NCT], Ql[NCT];
+            uint4 qf[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                bf16x8 sh[KS], sl[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
+                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
+                }
+                Qh[ct] = Ql[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Qh[ct] = mfma(__builtin_bit_cast(bf16x8, qf[s]), sh[s], Qh[ct]);
+                    Ql[ct] = mfma(__builtin_bit_cast(bf16x8, qf[s]), sl[s], Ql[ct]);
+                }
+            }
+            if (ch > 0) store(ch - 1);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) O[ct][r] = cq[r] * (Qh[ct][r] + Ql[ct][r]);
+            load_c(next);
+            lds_barrier();  // R written
+            wave_lds_fence();
+            qr.put(l.Q[w], lane);
+            load_q(min(ch + 2, chunks - 1));
+            const int chunk_first = __builtin_bit_cast(int, info_p[int64_t(ch) * d.H_v].y);
+            lds_barrier();  // U written
+            const int4 marks = l.marks;
+            poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0 || chunk_first < kC) != 0;
+            if (poisoned) first_bad(l, chunk_first, col, first);
+            auto add = [&](auto steps) {
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int s = 0; s < steps.value; ++s) {
+                        const f32x4 x0 = l.U[2 * s][ct][lane], x1 = l.U[2 * s + 1][ct][lane];
+                        const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+                        bf16x8 uh, ul;
+                        split8(x, uh, ul);
+                        const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
+                        O[ct] = mfma(mh, uh, O[ct]);
+                        O[ct] = mfma(mh, ul, O[ct]);
+                        O[ct] = mfma(ml, uh, O[ct]);
+                    }
+            };
+            if (w < 2)
+                add(std::integral_constant<int, 1>());
+            else
+                add(std::integral_constant<int, 2>());
+            load_m(next);
+        }
+        store(chunks - 1);
+        return;
+    }
+
+    // ---- the state ----
+    if (a.seq_status && threadIdx.x == 0 && h == 0 && v0 == 0) a.seq_status[b] = seq.ok ? GDN_OK : GDN_ERR_SHAPE;
+    const int pool = a.slot ? a.slot[b] : b;
+    const bool keep = pool >= 0 && pool < d.n_slots;
+    const bool resume = keep && (!a.has_state || a.has_state[b] != 0);
+    // state rows (elements of d_k) 32 (tau / 2) + 8 g + 4 (tau % 2) + r of tile tau
+    float* Sp = keep ? a.S + ((int64_t(pool) * d.H_v + h) * d.d_v + v0 + NCT * col) * DK + 8 * g : nullptr;
+    f32x4 S[TPW][NCT];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            const int tau = w * TPW + i;
+            S[i][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (resume) S[i][ct] = *reinterpret_cast<const f32x4*>(Sp + ct * DK + 32 * (tau >> 1) + 4 * (tau & 1));
+        }
+    if (chunks > 0) {
+        const uint16_t* kp = static_cast<const uint16_t*>(a.k) + seq.start * d.k_stride + int64_t(hk) * DK;
+        const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
+        const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
+        const float4* sp = c.sc + sh0 * kC + 16 * w;
+        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        const int64_t s_step = int64_t(d.H_v) * kC;
+        // Each group of inputs is loaded for the next chunk as soon as this chunk
+        // has used it, so one set of registers covers a chunk's latency.
+        uint4 tf[2][2];
+        TileRows<DK> kr;
+        float4 sc[4];  // scalars of tokens 16 w + 4 g + r
+        typename ValueBits<NCT>::type v[4];  // as loaded: converting at the load would wait for it
+        float2 info;
+        auto load_k = [&](int ch) { kr.load(kp + ch * (kC * d.k_stride), d.k_stride, seq.len - ch * kC - 1, w, lane); };
+        auto load_v = [&](int ch) {
+            const int last = seq.len - ch * kC - 1;
+            const uint16_t* pv = vp + ch * (kC * d.v_stride);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] = load_at<typename ValueBits<NCT>::type>(
+                    pv, (uint32_t(min(16 * w + 4 * g + r, last)) * uint32_t(d.v_stride) + NCT * col) * 2);
+        };
+        auto load_t = [&](int ch) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    tf[s][p] = load_at<uint4>(tp + ch * t_step + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[r] = load_at<float4>(sp + ch * s_step + r, g * 64);
+        };
+        // issued in the order of the loop: a wait for one group then lets the
+        // groups behind it stay in flight
+        load_k(0);
+        kr.put(l.K[w], lane);
+        load_v(0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_t(0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(min(1, chunks - 1));
+        info = info_p[0];
+        __builtin_amdgcn_sched_barrier(0);
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int n = seq.len - ch * kC;  // 64 or more but for the last
+            const int next = min(ch + 1, chunks - 1);
+
+            // the state as operands
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < TPW; ++i) {
+                    const int tau = w * TPW + i;
+                    __bf16 hi[4], lo[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) split2(S[i][ct][r], hi[r], lo[r]);
+                    reinterpret_cast<uint2*>(&l.S[tau >> 1][0][ct][lane])[tau & 1] = __builtin_bit_cast(uint2, hi);
+                    reinterpret_cast<uint2*>(&l.S[tau >> 1][1][ct][lane])[tau & 1] = __builtin_bit_cast(uint2, lo);
+                }
+            lds_barrier();
+
+            // K S^T of token tile w, then R = V - gamma K S^T
+            f32x4 R[NCT];
+            float check = 0.0f;
+            uint4 kf[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                bf16x8 sh[KS], sl[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
+                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
+                }
+                f32x4 Ph = {0.0f, 0.0f, 0.0f, 0.0f}, Pl = Ph;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Ph = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph);
+                    Pl = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[r].x * (Ph[r] + Pl[r]);
+            }
+            if (n < kC)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * w + 4 * g + r >= n) R[ct][r] = 0.0f;
+            // A value that is not finite must not reach earlier tokens through a
+            // product with a masked zero: it is taken out here, its row is marked,
+            // and rows from the first marked one on come out as NaN.
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) check = fmaf(R[ct][r], 0.0f, check);
+            const bool marked = __ballot(!(check == 0.0f)) != 0;
+            if (marked)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    unsigned m = 0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!finite(R[ct][r])) {
+                            m |= 1u << r;
+                            R[ct][r] = 0.0f;
+                        }
+                    l.badrow[w][ct][lane] = m;
+                }
+            if (lane == 0) (&l.marks.x)[w] = marked;
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                __bf16 hi[4], lo[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) split2(R[ct][r], hi[r], lo[r]);
+                reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, hi);
+                reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, lo);
+            }
+            load_v(next);
+            lds_barrier();
+
+            // U = beta R + T R below the diagonal
+            f32x4 u0[NCT], u1[NCT];
+            auto solve = [&](auto steps) {
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    bf16x8 rh[2], rl[2];
+#pragma unroll
+                    for (int s = 0; s < steps.value; ++s) {
+                        rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][ct][lane]);
+                        rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][ct][lane]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) u0[ct][r] = sc[r].y * R[ct][r];
+                    u1[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < steps.value; ++s) {
+                        const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
+                        u1[ct] = mfma(tl, rh[s], u1[ct]);
+                        u0[ct] = mfma(th, rh[s], u0[ct]);
+                        u1[ct] = mfma(th, rl[s], u1[ct]);
+                    }
+                }
+            };
+            const int4 marks = l.marks;
+            if (w < 2)
+                solve(std::integral_constant<int, 1>());
+            else
+                solve(std::integral_constant<int, 2>());
+            // K^T of the wavefront's state rows: accumulator row rho of tile tau is
+            // element 32 (tau / 2) + 8 (rho / 4) + 4 (tau % 2) + rho % 4.  In a
+            // transposing read lane i of 16 names 4 elements of row i / 4 and gets
+            // element i of the 4 rows.
+            uint4 ktf[TPW][2];
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int tau = w * TPW + i;
+                    uint2 x[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4* p = &l.K[2 * s + half][piece_at<DK>(4 * g + (col >> 2), 4 * (tau >> 1) + (col & 3))];
+                        x[half] = read_tr(reinterpret_cast<const uint2*>(p) + (tau & 1));
+                    }
+                    ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
+                }
+            const int chunk_first = __builtin_bit_cast(int, info.y);
+            float e[NCT][4];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u0[ct] += u1[ct];
+                l.U[w][ct][lane] = u0[ct];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) e[ct][r] = u0[ct][r] * sc[r].w;
+            }
+            if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0 || chunk_first < kC)) {
+                int first[NCT];
+                first_bad(l, chunk_first, col, first);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * w + 4 * g + r == first[ct]) e[ct][r] = __builtin_nanf("");
+            }
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                __bf16 dh[4], dm[4], dl[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dh[r] = static_cast<__bf16>(e[ct][r]);
+                    split2(e[ct][r] - static_cast<float>(dh[r]), dm[r], dl[r]);
+                }
+                reinterpret_cast<uint2*>(&l.D[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dh);
+                reinterpret_cast<uint2*>(&l.D[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dm);
+                reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dl);
+            }
+            load_t(next);
+            lds_barrier();
+
+            // S <- gamma_64 S + K^T diag(decay) U
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                bf16x8 du[2][3];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][ct][lane]);
+#pragma unroll
+                for (int i = 0; i < TPW; ++i) S[i][ct] *= info.x;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+#pragma unroll
+                        for (int i = 0; i < TPW; ++i)
+                            S[i][ct] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i][ct]);
+            }
+            kr.put(l.K[w], lane);
+            load_k(min(ch + 2, chunks - 1));
+            info = info_p[int64_t(next) * d.H_v];
+        }
+    }
+    if (keep)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const int tau = w * TPW + i;
+                *reinterpret_cast<f32x4*>(Sp + ct * DK + 32 * (tau >> 1) + 4 * (tau & 1)) = S[i][ct];
+            }
+}
+
+template <int DK>
+hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
+    const gdn_seq_dims& d = c.s.d;
+    prep_kernel<DK><<<dim3(c.slots, d.H_k), 256, 0, stream>>>(c);
+    const int items8 = (d.B * d.H_k + 7) / 8 * 8, per16 = d.H_v / d.H_k * (d.d_v / 16);
+    const int64_t wgs = int64_t(d.B) * d.H_v * (d.d_v / 16);
+    if (wgs > 512)
+        chain_kernel<DK, 2><<<items8 * per16 / 2, 512, 0, stream>>>(c);
+    else
+        chain_kernel<DK, 1><<<items8 * per16, 512, 0, stream>>>(c);
+    return hipGetLastError();
+}
+
+bool use_chunks(const gdn_seq_dims& d) { return d.qkv_dtype == GDN_BF16 && d.T > 0; }
+
+}  // namespace
+
+size_t prefill_ws_bytes(const gdn_seq_dims& d) { return use_chunks(d) ? prep_layout(d).total : 0; }
+
+hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream) {
+    if (!use_chunks(a.d)) return launch_prefill_walk(a, stream);
+    const PrepLayout l = prep_layout(a.d);
+    unsigned char* p = static_cast<unsigned char*>(a.ws);
+    ChunkArgs c{a,
+                reinterpret_cast<uint4*>(p + l.t),
+                reinterpret_cast<uint4*>(p + l.m),
+                reinterpret_cast<float4*>(p + l.sc),
+                reinterpret_cast<float2*>(p + l.info),
+                a.d.T / kC + a.d.B};
+    return a.d.d_k == 128 ? launch_chunks<128>(c, stream) : launch_chunks<64>(c, stream);
+}
+
+}  // namespace gdn
