@@ -83,7 +83,8 @@ __device__ __forceinline__ float lane_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ float sigmoidf(float a) { return 1.0f / (1.0f + __expf(-a)); }
+// 1 / (1 + e^-a) with the hardware's exponential and reciprocal (1 ulp each).
+__device__ __forceinline__ float sigmoidf(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
 __device__ __forceinline__ float activate(int act, float a) {
     switch (act) {
