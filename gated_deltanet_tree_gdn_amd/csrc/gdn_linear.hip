@@ -3,6 +3,7 @@
 // Products run as w x^T: a lane's accumulators are then 4 adjacent outputs of
 // one row of y.
 //
+//  - thin_kernel (M <= 64): the weights straight from memory into operands;
 //  - tile_kernel: BM x BN outputs per workgroup, K in steps of 64 through two
 //    LDS buffers filled by direct loads while the other one is multiplied.
 
@@ -15,43 +16,43 @@ namespace {
 
 constexpr int kBK = 64;  // elements of K per step of the tile kernel: 8 pieces of 16 bytes per row
 
-// Outputs n .. n + 7 of row m: bias, activation, scale and residual in fp32,
-// rounded once.  VEC: all 8 exist and rows of y and residual are 16-byte
-// aligned.
-template <bool VEC>
-__device__ __forceinline__ void put8(const LinearArgs& a, int64_t m, int n, float (&v)[8]) {
+// Outputs n .. n + E - 1 of row m: bias, activation, scale and residual in
+// fp32, rounded once.  VEC (E = 8): all of them exist and rows of y and
+// residual are 16-byte aligned.
+template <int E, bool VEC>
+__device__ __forceinline__ void put(const LinearArgs& a, int64_t m, int n, float (&v)[E]) {
+    static_assert(!VEC || E == 8, "");
     const gdn_linear_dims& d = a.d;
-    const int have = VEC ? 8 : min(8, d.N - n);
-    float b[8] = {}, r[8] = {};
+    float b[E] = {}, r[E] = {};
     if constexpr (VEC) {
         if (a.bias) load8(a.bias, GDN_F32, n, b);
         if (a.res) load8(a.res, d.res_dtype, m * d.res_stride + n, r);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < have) {
+        for (int e = 0; e < E; ++e)
+            if (n + e < d.N) {
                 if (a.bias) b[e] = a.bias[n + e];
                 if (a.res) r[e] = load1(a.res, d.res_dtype, m * d.res_stride + n + e);
             }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += b[e];
+    for (int e = 0; e < E; ++e) v[e] += b[e];
     if (d.act == GDN_ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = activate(GDN_ACT_GELU, v[e]);
+        for (int e = 0; e < E; ++e) v[e] = activate(GDN_ACT_GELU, v[e]);
     } else if (d.act != GDN_ACT_NONE) {
         const bool silu = d.act == GDN_ACT_SILU;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (silu ? v[e] : 1.0f) * sigmoidf(v[e]);
+        for (int e = 0; e < E; ++e) v[e] = (silu ? v[e] : 1.0f) * sigmoidf(v[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = a.res ? r[e] + d.scale * v[e] : d.scale * v[e];
+    for (int e = 0; e < E; ++e) v[e] = a.res ? r[e] + d.scale * v[e] : d.scale * v[e];
     if constexpr (VEC) {
         store8(a.y, d.y_dtype, m * d.y_stride + n, v);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < have) store1(a.y, d.y_dtype, m * d.y_stride + n + e, v[e]);
+        for (int e = 0; e < E; ++e)
+            if (n + e < d.N) store1(a.y, d.y_dtype, m * d.y_stride + n + e, v[e]);
     }
 }
 
@@ -208,12 +209,79 @@ __global__ void __launch_bounds__(64 * WM * WN) tile_kernel(LinearArgs a, int ve
             load8(out, GDN_F32, r * kOutLd + c, v);
             if (m < d.M && n < d.N) {
                 if (vec_out)
-                    put8<true>(a, m, n, v);
+                    put<8, true>(a, m, n, v);
                 else
-                    put8<false>(a, m, n, v);
+                    put<8, false>(a, m, n, v);
             }
         }
     }
+}
+
+// Few rows (M <= 16 MT): the weights are read once, straight into MFMA
+// operands, and that read is what bounds it.  A workgroup owns 16 outputs; its
+// NW wavefronts take turns at blocks of 128 elements of K and add their sums
+// in LDS, in a fixed order.
+constexpr int kThinBlock = 128;
+
+template <int MT, int NW, bool VEC>
+__global__ void __launch_bounds__(64 * NW) thin_kernel(LinearArgs a) {
+    constexpr int L = kThinBlock / 32;
+    __shared__ f32x4 part[NW][MT][64];
+    const gdn_linear_dims& d = a.d;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int64_t n0 = int64_t(blockIdx.x) * 16;
+    const uint16_t* wp = static_cast<const uint16_t*>(a.w) + min(n0 + col, int64_t(d.N) - 1) * d.w_stride + 8 * g;
+    const uint16_t* xp[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        xp[i] = static_cast<const uint16_t*>(a.x) + min(16 * i + col, d.M - 1) * d.x_stride + 8 * g;
+    uint4 wf[L], xf[MT][L];
+    auto load = [&](int k) {
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            if constexpr (VEC) {
+                const bool in = k + 32 * j + 8 * g < d.K;
+                wf[j] = in ? *reinterpret_cast<const uint4*>(wp + k + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    xf[i][j] = in ? *reinterpret_cast<const uint4*>(xp[i] + k + 32 * j) : make_uint4(0, 0, 0, 0);
+            } else {
+                wf[j] = load_k8(wp, k + 32 * j, d.K - 8 * g);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) xf[i][j] = load_k8(xp[i], k + 32 * j, d.K - 8 * g);
+            }
+        }
+    };
+    f32x4 acc[MT] = {};
+    for (int k = wave * kThinBlock; k < d.K; k += NW * kThinBlock) {
+        load(k);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                acc[i] = mfma(__builtin_bit_cast(bf16x8, wf[j]), __builtin_bit_cast(bf16x8, xf[i][j]), acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < MT; i += NW) {
+        f32x4 s = part[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += part[w][i][lane];
+        const int m = 16 * i + col;
+        float v[4] = {s[0], s[1], s[2], s[3]};
+        if (m < d.M) put<4, false>(a, m, n0 + 4 * g, v);
+    }
+}
+
+template <int MT>
+void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
+    const int grid = (a.d.N + 15) / 16;
+    if (vec)
+        thin_kernel<MT, 8, true><<<grid, 512, 0, stream>>>(a);
+    else
+        thin_kernel<MT, 8, false><<<grid, 512, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -227,7 +295,13 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
                         d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
     const bool vec_out = d.N % 8 == 0 && (d.M <= 1 || (d.y_stride % 8 == 0 && (!a.res || d.res_stride % 8 == 0)));
     auto tiles = [&](int bm, int bn) { return ((d.M + bm - 1) / bm) * ((d.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= 256 && direct)
+    if (d.M <= 16)
+        launch_thin<1>(a, direct, stream);
+    else if (d.M <= 32)
+        launch_thin<2>(a, direct, stream);
+    else if (d.M <= 64)
+        launch_thin<4>(a, direct, stream);
+    else if (tiles(256, 256) >= 256 && direct)
         tile_kernel<256, 256, 2, 4, true><<<tiles(256, 256), 512, 0, stream>>>(a, vec_out);
     else if (tiles(128, 128) >= 128 && direct)
         tile_kernel<128, 128, 2, 2, true><<<tiles(128, 128), 256, 0, stream>>>(a, vec_out);

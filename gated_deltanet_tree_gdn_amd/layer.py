@@ -44,12 +44,13 @@ class LinearDims(ctypes.Structure):
 
 _lib = None
 _torch = None
+_Tensor = _raw_stream = _current_device = None  # from torch, bound on first use
 _codes = {}  # torch dtype -> gdn_dtype
 
 
 def layer_library():
     """The HIP library with this header's entry points declared."""
-    global _lib, _torch
+    global _lib, _torch, _Tensor, _raw_stream, _current_device
     if _lib is None:
         lib = load_library()
         import torch
@@ -67,107 +68,108 @@ def layer_library():
         for name in ("gdn_prefill", "gdn_decode", "gdn_add_norm", "gdn_gated_norm", "gdn_linear"):
             getattr(lib, name).restype = ctypes.c_int
         _codes.update({torch.bfloat16: GDN_BF16, torch.float32: GDN_F32})
-        _torch = torch
+        _torch, _Tensor = torch, torch.Tensor
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         _lib = lib
     return _lib
 
 
 def _code(dtype, name):
-    try:
-        return _codes[dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}") from None
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return code
 
 
-def _rows(t, name, shape, device, dtype=None):
+def _device(t, name):
+    """The index of the device that the call runs on."""
+    if _lib is None:
+        layer_library()
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return index
+
+
+def _rows(t, name, shape, index, dtype=None):
     """Checks a tensor [rows][...] whose rows are dense; returns the stride
-    between rows (0 where there is one row)."""
-    if not isinstance(t, _torch.Tensor):
+    between rows."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}, got {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.is_contiguous():
-        return t.numel() // shape[0] if shape[0] > 0 else 0
-    stride, want = t.stride(), 1
-    for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
-        if n != 1 and s != want:
-            raise ValueError(f"{name}: the elements of a row must be dense")
-        want *= n
-    return stride[0] if shape[0] > 1 else 0
+    stride = t.stride()
+    if not t.is_contiguous():
+        want = 1
+        for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
+            if n != 1 and s != want:
+                raise ValueError(f"{name}: the elements of a row must be dense")
+            want *= n
+    return stride[0]
 
 
-def _dense(t, name, shape, device, dtype):
+def _dense(t, name, shape, index, dtype):
+    """The address of a contiguous tensor, None for None."""
     if t is None:
         return None
-    _rows(t, name, shape, device, dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index or t.dtype != dtype or not t.is_contiguous():
+        raise (TypeError if t.dtype != dtype else ValueError)(f"{name} must be a contiguous {dtype} tensor on device {index}")
     return t.data_ptr()
 
 
-def _on_device(t, name):
-    layer_library()
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    return t.device
+def _stream(stream, index):
+    """The raw handle of the call's stream."""
+    if stream is None:
+        return _raw_stream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-class _Launch:
-    """The call's device and stream.  Memory allocated here for work on a
-    stream other than the current one is marked as used there."""
-
-    def __init__(self, device, stream):
-        self.device, self.current = device, _torch.cuda.current_stream(device)
-        self.other = None
-        if stream is None:
-            self.raw = self.current.cuda_stream
-        else:
-            self.raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            if self.raw != self.current.cuda_stream:
-                self.other = _torch.cuda.ExternalStream(self.raw, device=device)
-
-    def empty(self, shape, dtype):
-        t = _torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
-
-    def run(self, fn, *args):
-        if _torch.cuda.current_device() != self.device.index:
-            with _torch.cuda.device(self.device):
-                code = fn(*args, self.raw)
-        else:
-            code = fn(*args, self.raw)
-        if code != 0:
-            raise GdnError(code, _lib.gdn_last_error().decode())
+def _empty(like, shape, dtype, index, raw):
+    """Memory for an output.  The allocator hands it out for the current
+    stream; where the call runs on another, it is marked as used there."""
+    t = like.new_empty(shape, dtype=dtype)
+    if raw != _raw_stream(index):
+        t.record_stream(_torch.cuda.ExternalStream(raw, device=index))
+    return t
 
 
-def _seq_dims(q, k, v, g, beta, S, slot, n, device, q_scale, qk_l2norm, l2_eps, o_dtype):
+def _run(index, fn, *args):
+    if _current_device() == index:
+        code = fn(*args)
+    else:
+        with _torch.cuda.device(index):
+            code = fn(*args)
+    if code != 0:
+        raise GdnError(code, _lib.gdn_last_error().decode())
+
+
+def _seq_dims(q, k, v, g, beta, S, n, index, q_scale, qk_l2norm, l2_eps, o_dtype):
     if q.dim() != 3 or v.dim() != 3 or S.dim() != 4:
         raise ValueError("q, k and v must have 3 dimensions, S 4")
-    rows, Hk, dk = q.shape
+    rows, Hk, dk = shape = q.shape
     Hv, dv = v.shape[1:]
-    if n is None:
-        n = rows
-    qs = _rows(q, "q", (rows, Hk, dk), device)
-    ks = _rows(k, "k", (rows, Hk, dk), device, q.dtype)
-    vs = _rows(v, "v", (rows, Hv, dv), device, q.dtype)
-    _dense(g, "g", (rows, Hv), device, _torch.float32)
-    _dense(beta, "beta", (rows, Hv), device, _torch.float32)
-    _dense(S, "S", (S.shape[0], Hv, dv, dk), device, _torch.float32)
-    _dense(slot, "slot", (n,), device, _torch.int32)
-    return SeqDims(n, rows, Hk, Hv, dk, dv, _code(q.dtype, "q"), _code(o_dtype, "o_dtype"), S.shape[0],
-                   int(bool(qk_l2norm)), q_scale, l2_eps, qs, ks, vs)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    dtype = q.dtype
+    qs = _rows(q, "q", shape, index)
+    ks = _rows(k, "k", shape, index, dtype)
+    vs = _rows(v, "v", (rows, Hv, dv), index, dtype)
+    if rows <= 1:  # one row has no stride
+        qs = ks = vs = 0
+    f32 = _torch.float32
+    slots = S.shape[0]
+    ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dense(g, "g", (rows, Hv), index, f32),
+            _dense(beta, "beta", (rows, Hv), index, f32), _dense(S, "S", (slots, Hv, dv, dk), index, f32))
+    return SeqDims(rows if n is None else n, rows, Hk, Hv, dk, dv, _code(dtype, "q"), _code(o_dtype, "o_dtype"), slots,
+                   bool(qk_l2norm), q_scale, l2_eps, qs, ks, vs), ptrs
 
 
 def gdn_prefill(q, k, v, g, beta, cu_seqlens, S, slot=None, has_state=None, q_scale=1.0, qk_l2norm=False, l2_eps=1e-6,
@@ -179,24 +181,26 @@ def gdn_prefill(q, k, v, g, beta, cu_seqlens, S, slot=None, has_state=None, q_sc
     [T][H_v][d_v] (q's dtype unless ``o`` or ``o_dtype`` says otherwise).
     ``workspace``: a uint8 device tensor of at least
     :func:`gdn_prefill_workspace_bytes` bytes to allocate nothing here."""
-    device = _on_device(q, "q")
+    index = _device(q, "q")
     n = cu_seqlens.shape[0] - 1
     o_dtype = o.dtype if o is not None else o_dtype or q.dtype
-    dims = _seq_dims(q, k, v, g, beta, S, slot, n, device, q_scale, qk_l2norm, l2_eps, o_dtype)
-    _dense(cu_seqlens, "cu_seqlens", (n + 1,), device, _torch.int32)
-    _dense(has_state, "has_state", (n,), device, _torch.int32)
-    _dense(seq_status, "seq_status", (n,), device, _torch.int32)
-    at = _Launch(device, stream)
+    dims, (qp, kp, vp, gp, bp, sp) = _seq_dims(q, k, v, g, beta, S, n, index, q_scale, qk_l2norm, l2_eps, o_dtype)
+    i32 = _torch.int32
+    cu = _dense(cu_seqlens, "cu_seqlens", (n + 1,), index, i32)
+    slot = _dense(slot, "slot", (n,), index, i32)
+    has_state = _dense(has_state, "has_state", (n,), index, i32)
+    seq_status = _dense(seq_status, "seq_status", (n,), index, i32)
+    raw = _stream(stream, index)
     if o is None:
-        o = at.empty(v.shape, o_dtype)
+        o = _empty(q, v.shape, o_dtype, index, raw)
+        op = o.data_ptr()
     else:
-        _dense(o, "o", v.shape, device, o_dtype)
-    need = _lib.gdn_prefill_workspace_bytes(dims)
-    if workspace is None and need:
-        workspace = at.empty((need,), _torch.uint8)
-    at.run(_lib.gdn_prefill, dims, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-           cu_seqlens.data_ptr(), _ptr(slot), _ptr(has_state), S.data_ptr(), o.data_ptr(), _ptr(seq_status),
-           _ptr(workspace), 0 if workspace is None else workspace.numel())
+        op = _dense(o, "o", v.shape, index, o_dtype)
+    if workspace is None:
+        need = _lib.gdn_prefill_workspace_bytes(dims)
+        workspace = _empty(q, (need,), _torch.uint8, index, raw)
+    _run(index, _lib.gdn_prefill, dims, qp, kp, vp, gp, bp, cu, slot, has_state, sp, op, seq_status,
+         workspace.data_ptr(), workspace.numel(), raw)
     return o
 
 
@@ -213,16 +217,17 @@ def gdn_decode(q, k, v, g, beta, S, slot=None, q_scale=1.0, qk_l2norm=False, l2_
     """One token per sequence: q, k [B][H_k][d_k], v [B][H_v][d_v], g and beta
     [B][H_v]; the states in the pool S are updated in place.  A row whose
     slot is outside the pool is idle (o = 0).  Returns o [B][H_v][d_v]."""
-    device = _on_device(q, "q")
+    index = _device(q, "q")
     o_dtype = o.dtype if o is not None else o_dtype or q.dtype
-    dims = _seq_dims(q, k, v, g, beta, S, slot, None, device, q_scale, qk_l2norm, l2_eps, o_dtype)
-    at = _Launch(device, stream)
+    dims, (qp, kp, vp, gp, bp, sp) = _seq_dims(q, k, v, g, beta, S, None, index, q_scale, qk_l2norm, l2_eps, o_dtype)
+    slot = _dense(slot, "slot", (q.shape[0],), index, _torch.int32)
+    raw = _stream(stream, index)
     if o is None:
-        o = at.empty(v.shape, o_dtype)
+        o = _empty(q, v.shape, o_dtype, index, raw)
+        op = o.data_ptr()
     else:
-        _dense(o, "o", v.shape, device, o_dtype)
-    at.run(_lib.gdn_decode, dims, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(slot),
-           S.data_ptr(), o.data_ptr())
+        op = _dense(o, "o", v.shape, index, o_dtype)
+    _run(index, _lib.gdn_decode, dims, qp, kp, vp, gp, bp, slot, sp, op, raw)
     return o
 
 
@@ -231,54 +236,56 @@ def gdn_add_norm(x, residual, weight, scale=1.0, chan_scale=None, post_weight=No
     """(y, h): the residual sum h = residual + scale * p and its RMS norm y,
     where p is x, or with ``post_weight`` x's own RMS norm, times
     ``chan_scale`` if given.  x [T][D]; h has the residual's dtype (x's where
-    there is no residual) and may be the residual itself."""
-    device = _on_device(x, "x")
+    there is no residual) and may be the residual itself; y is bfloat16
+    unless ``y`` or ``y_dtype`` says otherwise."""
+    index = _device(x, "x")
     if x.dim() != 2:
         raise ValueError("x must have 2 dimensions")
     T, D = shape = x.shape
-    xs = _rows(x, "x", shape, device)
-    rs = 0 if residual is None else _rows(residual, "residual", shape, device)
-    h_dtype = x.dtype if residual is None else residual.dtype
+    xs = _rows(x, "x", shape, index)
+    if residual is None:
+        rs, rp, h_dtype = 0, None, x.dtype
+    else:
+        rs, rp, h_dtype = _rows(residual, "residual", shape, index), residual.data_ptr(), residual.dtype
     f32 = _torch.float32
-    _dense(weight, "weight", (D,), device, f32)
-    _dense(chan_scale, "chan_scale", (D,), device, f32)
-    _dense(post_weight, "post_weight", (D,), device, f32)
-    at = _Launch(device, stream)
+    raw = _stream(stream, index)
     if h is None:
-        h, hs = at.empty(shape, h_dtype), D
+        h, hs = _empty(x, shape, h_dtype, index, raw), D
     else:
-        hs = _rows(h, "h", shape, device, h_dtype)
+        hs = _rows(h, "h", shape, index, h_dtype)
     if y is None:
-        y, ys = at.empty(shape, y_dtype or _torch.bfloat16), D
+        y, ys = _empty(x, shape, y_dtype or _torch.bfloat16, index, raw), D
     else:
-        ys = _rows(y, "y", shape, device, y_dtype)
+        ys = _rows(y, "y", shape, index, y_dtype)
     dims = AddNormDims(T, D, _code(x.dtype, "x"), _code(h_dtype, "residual"), _code(y.dtype, "y"), scale, eps,
                        weight_offset, xs, rs, hs, ys)
-    at.run(_lib.gdn_add_norm, dims, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(post_weight),
-           _ptr(chan_scale), h.data_ptr(), y.data_ptr())
+    _run(index, _lib.gdn_add_norm, dims, x.data_ptr(), rp, _dense(weight, "weight", (D,), index, f32),
+         _dense(post_weight, "post_weight", (D,), index, f32), _dense(chan_scale, "chan_scale", (D,), index, f32),
+         h.data_ptr(), y.data_ptr(), raw)
     return y, h
 
 
 def gdn_gated_norm(o, z, weight, eps=1e-6, gate="silu", y=None, y_dtype=None, stream=None):
     """y = rms(o) * weight * gate(z) over each head of o and z [T][H][d];
-    ``gate`` is "silu" or "sigmoid"."""
-    device = _on_device(o, "o")
+    ``gate`` is "silu" or "sigmoid"; y is bfloat16 unless ``y`` or
+    ``y_dtype`` says otherwise, and may be o or z itself."""
+    index = _device(o, "o")
     if o.dim() != 3:
         raise ValueError("o must have 3 dimensions")
     T, H, d = shape = o.shape
-    os_ = _rows(o, "o", shape, device)
-    zs = _rows(z, "z", shape, device)
-    _dense(weight, "weight", (d,), device, _torch.float32)
-    at = _Launch(device, stream)
+    os_ = _rows(o, "o", shape, index)
+    zs = _rows(z, "z", shape, index)
+    raw = _stream(stream, index)
     if y is None:
-        y, ys = at.empty(shape, y_dtype or _torch.bfloat16), H * d
+        y, ys = _empty(o, shape, y_dtype or _torch.bfloat16, index, raw), H * d
     else:
-        ys = _rows(y, "y", shape, device, y_dtype)
+        ys = _rows(y, "y", shape, index, y_dtype)
     if gate not in ("silu", "sigmoid"):
         raise ValueError('gate must be "silu" or "sigmoid"')
     dims = GatedNormDims(T, H, d, _code(o.dtype, "o"), _code(z.dtype, "z"), _code(y.dtype, "y"), ACTS[gate], eps, os_,
                          zs, ys)
-    at.run(_lib.gdn_gated_norm, dims, o.data_ptr(), z.data_ptr(), weight.data_ptr(), y.data_ptr())
+    _run(index, _lib.gdn_gated_norm, dims, o.data_ptr(), z.data_ptr(),
+         _dense(weight, "weight", (d,), index, _torch.float32), y.data_ptr(), raw)
     return y
 
 
@@ -286,29 +293,34 @@ def gdn_linear(x, w, bias=None, act="none", residual=None, scale=1.0, y=None, y_
                stream=None):
     """y = residual + scale * act(x w^T + bias): x [M][K] and w [N][K]
     bfloat16, bias [N] float32, residual and y [M][N]; ``act`` is "none",
-    "silu", "gelu" or "sigmoid".  ``y`` may be the residual itself."""
-    device = _on_device(x, "x")
+    "silu", "gelu" or "sigmoid"; y is bfloat16 unless ``y`` or ``y_dtype``
+    says otherwise, and may be the residual itself."""
+    index = _device(x, "x")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must have 2 dimensions")
     M, K = x.shape
     N = w.shape[0]
     bf16 = _torch.bfloat16
-    xs = _rows(x, "x", (M, K), device, bf16)
-    ws = _rows(w, "w", (N, K), device, bf16)
-    _dense(bias, "bias", (N,), device, _torch.float32)
-    rs = 0 if residual is None else _rows(residual, "residual", (M, N), device)
-    at = _Launch(device, stream)
-    if y is None:
-        y, ys = at.empty((M, N), y_dtype or bf16), N
+    xs = _rows(x, "x", (M, K), index, bf16)
+    ws = _rows(w, "w", (N, K), index, bf16)
+    if residual is None:
+        rs, rp, r_code = 0, None, GDN_BF16
     else:
-        ys = _rows(y, "y", (M, N), device, y_dtype)
-    if act not in ACTS:
+        rs, rp, r_code = _rows(residual, "residual", (M, N), index), residual.data_ptr(), _code(residual.dtype, "residual")
+    raw = _stream(stream, index)
+    if y is None:
+        y, ys = _empty(x, (M, N), y_dtype or bf16, index, raw), N
+    else:
+        ys = _rows(y, "y", (M, N), index, y_dtype)
+    act_code = ACTS.get(act)
+    if act_code is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    dims = LinearDims(M, N, K, GDN_BF16 if residual is None else _code(residual.dtype, "residual"),
-                      _code(y.dtype, "y"), ACTS[act], scale, xs, ws, rs, ys)
-    need = _lib.gdn_linear_workspace_bytes(dims)
-    if workspace is None and need:
-        workspace = at.empty((need,), _torch.uint8)
-    at.run(_lib.gdn_linear, dims, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
-           _ptr(workspace), 0 if workspace is None else workspace.numel())
+    dims = LinearDims(M, N, K, r_code, _code(y.dtype, "y"), act_code, scale, xs, ws, rs, ys)
+    if workspace is None:
+        need = _lib.gdn_linear_workspace_bytes(dims)
+        if need:
+            workspace = _empty(x, (need,), _torch.uint8, index, raw)
+    wp, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _run(index, _lib.gdn_linear, dims, x.data_ptr(), w.data_ptr(), _dense(bias, "bias", (N,), index, _torch.float32), rp,
+         y.data_ptr(), wp, nbytes, raw)
     return y
