@@ -95,4 +95,12 @@ __device__ __forceinline__ float activate(int act, float a) {
     }
 }
 
+// Orders LDS between the wavefronts of a workgroup without waiting for
+// global loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 }  // namespace gdn

@@ -3,9 +3,13 @@
 // Products run as w x^T: a lane's accumulators are then 4 adjacent outputs of
 // one row of y.
 //
-//  - thin_kernel (M <= 64): the weights straight from memory into operands;
-//  - tile_kernel: BM x BN outputs per workgroup, K in steps of 64 through two
-//    LDS buffers filled by direct loads while the other one is multiplied.
+//  - thin_kernel (at most 16 rows, few outputs): the weights straight from
+//    memory into operands;
+//  - tile_kernel: BM x BN outputs per workgroup, K in steps of 64 through LDS
+//    buffers filled by direct loads while others are multiplied.
+
+#include <algorithm>
+#include <cmath>
 
 #include "gdn_layer_internal.h"
 #include "gdn_layer_util.h"
@@ -14,7 +18,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kBK = 64;  // elements of K per step of the tile kernel: 8 pieces of 16 bytes per row
+constexpr int kBK = 64;  // elements of K per step of the tile kernel
+
 
 // Outputs n .. n + E - 1 of row m: bias, activation, scale and residual in
 // fp32, rounded once.  VEC (E = 8): all of them exist and rows of y and
@@ -69,7 +74,6 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& t
 }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // 8 elements k .. k + 7 of a row of K, zeros past its end; rows of any alignment.
 __device__ __forceinline__ uint4 load_k8(const uint16_t* row, int k, int K) {
@@ -81,19 +85,19 @@ __device__ __forceinline__ uint4 load_k8(const uint16_t* row, int k, int K) {
     return make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
 }
 
-// ROWS rows of x or w by 64 elements of K in LDS: row r's piece p (16 bytes)
-// at position p ^ (r & 7), which spreads the 16 rows of a fragment read over
-// the banks.  One direct load of a wavefront fills 8 rows (LDS addresses run
-// with the lanes), so the permutation is made in the global address.
+// Direct loads of ROWS rows of x or w by kBK elements of K into LDS.  Piece p
+// (16 bytes) of row r sits at position p ^ (r & 7) of its row, which spreads
+// the rows of a fragment read over the banks.  One load of a wavefront fills
+// 8 rows (LDS addresses run with the lanes), so the permutation is made in the
+// global address.
 template <int ROWS, int WAVES>
 struct Stage {
     static constexpr int L = ROWS / 8 / WAVES;  // loads per wavefront
-    rsrc_t rsrc;
+    const uint16_t* base;  // of the first row
     uint32_t off[L];
-    __device__ __forceinline__ void init(const uint16_t* base, int64_t stride, int64_t row0, int64_t rows, int wave,
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t stride, int64_t row0, int64_t rows, int wave,
                                          int lane) {
-        const uint16_t* p = base + row0 * stride;
-        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, 0x7fffffff, 0x00027000);
+        base = p + row0 * stride;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const int r = (wave * L + i) * 8 + (lane >> 3);
@@ -102,9 +106,12 @@ struct Stage {
         }
     }
     __device__ __forceinline__ void load(uint4* lds, int k, int wave) const {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass rejects the 16-byte form
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, 0x7fffffff, 0x00027000);
 #pragma unroll
         for (int i = 0; i < L; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(lds + (wave * L + i) * 64), 16, off[i], k * 2, 0, 0);
+#endif
     }
 };
 
@@ -124,18 +131,35 @@ __device__ __forceinline__ void stage_any(uint4* lds, const uint16_t* base, int6
     for (int i = 0; i < L; ++i) lds[(wave * L + i) * 64 + lane] = x[i];
 }
 
-// WM x WN wavefronts, each (BM / WM) x (BN / WN) outputs.
-template <int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ void __launch_bounds__(64 * WM * WN) tile_kernel(LinearArgs a, int vec_out) {
+// Waits until at most N of the wavefront's direct loads are outstanding (and, if
+// READS, until its LDS reads are done), then meets the workgroup.  A fence would wait for every
+// direct load (they count as LDS writes); what has to have arrived is exactly
+// what the count says.
+template <int N, bool READS = true>
+__device__ __forceinline__ void loads_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (READS ? 0 : 15) << 8 | (N >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// KG groups of WM x WN wavefronts; a wavefront has (BM / WM) x (BN / WN)
+// outputs.  The groups take turns at the steps of K, each through its own NB
+// LDS buffers, and add their sums at the end in a fixed order: with few tiles
+// that keeps KG times as many loads in flight on a CU.
+template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
+__global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a, int vec_out) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kOutRows = TM > 4 ? 64 : TM * 16, kOutLd = TN * 16 + 4;  // epilogue: rows of a wavefront at a time
-    constexpr int kStageBytes = (BM + BN) * 8 * 16 * 2, kOutBytes = W * kOutRows * kOutLd * 4;
-    __shared__ __align__(16) char lds[kStageBytes > kOutBytes ? kStageBytes : kOutBytes];
-    auto xs = [&](int p) { return reinterpret_cast<uint4*>(lds) + p * BM * 8; };
-    auto ws = [&](int p) { return reinterpret_cast<uint4*>(lds) + (2 * BM + p * BN) * 8; };
+    constexpr int kGroupPieces = (BM + BN) * 8 * NB, kOutBytes = W * kOutRows * kOutLd * 4;
+    constexpr int kSumBytes = (KG - 1) * W * TM * TN * 1024, kStageBytes = KG * kGroupPieces * 16;
+    constexpr int kMax1 = kStageBytes > kOutBytes ? kStageBytes : kOutBytes;
+    __shared__ __align__(16) char lds[kMax1 > kSumBytes ? kMax1 : kSumBytes];
     const gdn_linear_dims& d = a.d;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = all % W, grp = all / W, col = lane & 15, g = lane >> 4;
+    auto xs = [&](int p) { return reinterpret_cast<uint4*>(lds) + grp * kGroupPieces + p * BM * 8; };
+    auto ws = [&](int p) { return reinterpret_cast<uint4*>(lds) + grp * kGroupPieces + (NB * BM + p * BN) * 8; };
     int tm, tn;
     tile_of(blockIdx.x, (d.M + BM - 1) / BM, (d.N + BN - 1) / BN, tm, tn);
     const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
@@ -143,26 +167,33 @@ __global__ void __launch_bounds__(64 * WM * WN) tile_kernel(LinearArgs a, int ve
     const uint16_t* xp = static_cast<const uint16_t*>(a.x);
     const uint16_t* wp = static_cast<const uint16_t*>(a.w);
     f32x4 acc[TN][TM] = {};
-    auto multiply = [&](const uint4* x, const uint4* w) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 xf[TM], wf[TN];
-            const int at = (4 * s + g) ^ (col & 7);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) xf[i] = __builtin_bit_cast(bf16x8, x[((wm * TM + i) * 16 + col) * 8 + at]);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) wf[j] = __builtin_bit_cast(bf16x8, w[((wn * TN + j) * 16 + col) * 8 + at]);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int i = 0; i < TM; ++i) acc[j][i] = mfma(wf[j], xf[i], acc[j][i]);
-        }
+    struct Frags {
+        bf16x8 x[TM], w[TN];
     };
-    auto any_step = [&](int k) {
+    auto read = [&](Frags& f, int p, int s) {  // 32 elements of K of buffer p
+        const uint4 *x = xs(p), *w = ws(p);
+        const int at = (4 * s + g) ^ (col & 7);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) f.x[i] = __builtin_bit_cast(bf16x8, x[((wm * TM + i) * 16 + col) * 8 + at]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) f.w[j] = __builtin_bit_cast(bf16x8, w[((wn * TN + j) * 16 + col) * 8 + at]);
+    };
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) acc[j][i] = mfma(f.w[j], f.x[i], acc[j][i]);
+    };
+    auto any_step = [&](int k) {  // all groups stage, one multiplies the end of K
         stage_any<BM, W>(xs(0), xp, d.x_stride, m0, d.M, k, d.K, wave, lane);
         stage_any<BN, W>(ws(0), wp, d.w_stride, n0, d.N, k, d.K, wave, lane);
         __syncthreads();
-        multiply(xs(0), ws(0));
+        Frags f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            read(f, 0, s);
+            multiply(f);
+        }
         __syncthreads();
     };
     if constexpr (DIRECT) {
@@ -172,22 +203,88 @@ __global__ void __launch_bounds__(64 * WM * WN) tile_kernel(LinearArgs a, int ve
             Stage<BN, W> sw;
             sx.init(xp, d.x_stride, m0, d.M, wave, lane);
             sw.init(wp, d.w_stride, n0, d.N, wave, lane);
-            sx.load(xs(0), 0, wave);
-            sw.load(ws(0), 0, wave);
-            __syncthreads();
-            for (int t = 0; t < steps; ++t) {
-                const int p = t & 1;
-                if (t + 1 < steps) {
-                    sx.load(xs(p ^ 1), (t + 1) * kBK, wave);
-                    sw.load(ws(p ^ 1), (t + 1) * kBK, wave);
+            // This group's steps are grp, grp + KG, ..; every group goes through as
+            // many rounds.  Loads run NB - 1 rounds ahead.
+            const int rounds = (steps + KG - 1) / KG;
+            auto load = [&](int round) {
+                const int t = round * KG + grp, p = round % NB;
+                if (t < steps) {
+                    sx.load(xs(p), t * kBK, wave);
+                    sw.load(ws(p), t * kBK, wave);
                 }
-                multiply(xs(p), ws(p));
-                __syncthreads();
+            };
+#pragma unroll
+            for (int r = 0; r < NB - 1; ++r) load(r);
+            loads_barrier<0>();
+            constexpr int L = Stage<BM, W>::L + Stage<BN, W>::L;
+            if constexpr (NB == 2) {
+                for (int r = 0; r < rounds; ++r) {
+                    load(r + 1);
+                    if (KG == 1 || r * KG + grp < steps) {
+                        Frags f;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            read(f, r & 1, s);
+                            multiply(f);
+                        }
+                    }
+                    loads_barrier<0>();
+                }
+            } else {
+                // Operands are read half a step ahead, the first of a round before
+                // the barrier that ends the round before it: at that barrier the
+                // round after next has arrived, that is, only the NB - 3 rounds
+                // behind it are outstanding (as long as they were issued by all
+                // groups: grp < KG loaded step (r + NB - 1) KG + grp if
+                // (r + NB) KG <= steps).  A group whose last round has no step
+                // multiplies what is left in its buffer into nothing.
+                Frags f0, f1;
+                read(f0, 0, 0);
+                for (int r = 0, p = 0; r < rounds; ++r) {
+                    const int next = p + 1 == NB ? 0 : p + 1;
+                    const bool mine = KG == 1 || r * KG + grp < steps;
+                    load(r + NB - 1);
+                    read(f1, p, 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (mine) multiply(f0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    read(f0, next, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (mine) multiply(f1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if ((r + NB) * KG <= steps)
+                        loads_barrier<(NB - 3) * L, false>();
+                    else
+                        loads_barrier<0, false>();
+                    p = next;
+                }
+                loads_barrier<0>();
             }
         }
-        if (d.K % kBK) any_step(d.K / kBK * kBK);
+        // the end of K: past it both operands are staged as zeros, so every
+        // group but the first adds nothing
+        if (d.K % kBK) any_step(grp == 0 ? d.K / kBK * kBK : d.K);
     } else {
-        for (int k = 0; k < d.K; k += kBK) any_step(k);
+        for (int k = 0; k < d.K; k += kBK * KG) any_step(k + grp * kBK);
+    }
+    if constexpr (KG > 1) {
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);
+        if (grp > 0)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    sums[(((grp - 1) * W + wave) * TN * TM + j * TM + i) * 64 + lane] = acc[j][i];
+        __syncthreads();
+        if (grp == 0)
+#pragma unroll
+            for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) acc[j][i] += sums[((q * W + wave) * TN * TM + j * TM + i) * 64 + lane];
+        __syncthreads();
+        if (grp > 0) return;
     }
     // Rows through LDS, so that a lane stores 8 adjacent outputs and the
     // activation's code is not repeated for every register.
@@ -217,98 +314,151 @@ __global__ void __launch_bounds__(64 * WM * WN) tile_kernel(LinearArgs a, int ve
     }
 }
 
-// Few rows (M <= 16 MT): the weights are read once, straight into MFMA
-// operands, and that read is what bounds it.  A workgroup owns 16 outputs; its
-// NW wavefronts take turns at blocks of 128 elements of K and add their sums
-// in LDS, in a fixed order.
-constexpr int kThinBlock = 128;
+// At most 16 rows: the weights are read once, straight into MFMA operands, and
+// that read is what bounds it.  A workgroup owns 16 outputs; its wavefronts take
+// turns at blocks of 128 elements of K and add their sums in LDS, in a fixed
+// order.
+constexpr int kThinBlock = 128, kThinWaves = 8;
 
-template <int MT, int NW, bool VEC>
-__global__ void __launch_bounds__(64 * NW) thin_kernel(LinearArgs a) {
+template <bool VEC>
+__global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(LinearArgs a) {
     constexpr int L = kThinBlock / 32;
-    __shared__ f32x4 part[NW][MT][64];
+    __shared__ f32x4 part[kThinWaves][64];
     const gdn_linear_dims& d = a.d;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int64_t n0 = int64_t(blockIdx.x) * 16;
     const uint16_t* wp = static_cast<const uint16_t*>(a.w) + min(n0 + col, int64_t(d.N) - 1) * d.w_stride + 8 * g;
-    const uint16_t* xp[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-        xp[i] = static_cast<const uint16_t*>(a.x) + min(16 * i + col, d.M - 1) * d.x_stride + 8 * g;
-    uint4 wf[L], xf[MT][L];
-    auto load = [&](int k) {
+    const uint16_t* xp = static_cast<const uint16_t*>(a.x) + int64_t(min(col, d.M - 1)) * d.x_stride + 8 * g;
+    f32x4 acc = {};
+    for (int k = wave * kThinBlock; k < d.K; k += kThinWaves * kThinBlock) {
+        uint4 wf[L], xf[L];
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             if constexpr (VEC) {
                 const bool in = k + 32 * j + 8 * g < d.K;
                 wf[j] = in ? *reinterpret_cast<const uint4*>(wp + k + 32 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    xf[i][j] = in ? *reinterpret_cast<const uint4*>(xp[i] + k + 32 * j) : make_uint4(0, 0, 0, 0);
+                xf[j] = in ? *reinterpret_cast<const uint4*>(xp + k + 32 * j) : make_uint4(0, 0, 0, 0);
             } else {
                 wf[j] = load_k8(wp, k + 32 * j, d.K - 8 * g);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) xf[i][j] = load_k8(xp[i], k + 32 * j, d.K - 8 * g);
+                xf[j] = load_k8(xp, k + 32 * j, d.K - 8 * g);
             }
         }
-    };
-    f32x4 acc[MT] = {};
-    for (int k = wave * kThinBlock; k < d.K; k += NW * kThinBlock) {
-        load(k);
 #pragma unroll
         for (int j = 0; j < L; ++j)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                acc[i] = mfma(__builtin_bit_cast(bf16x8, wf[j]), __builtin_bit_cast(bf16x8, xf[i][j]), acc[i]);
+            acc = mfma(__builtin_bit_cast(bf16x8, wf[j]), __builtin_bit_cast(bf16x8, xf[j]), acc);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    part[wave][lane] = acc;
     __syncthreads();
-    for (int i = wave; i < MT; i += NW) {
-        f32x4 s = part[0][i][lane];
+    if (wave == 0 && col < d.M) {
 #pragma unroll
-        for (int w = 1; w < NW; ++w) s += part[w][i][lane];
-        const int m = 16 * i + col;
-        float v[4] = {s[0], s[1], s[2], s[3]};
-        if (m < d.M) put<4, false>(a, m, n0 + 4 * g, v);
+        for (int w = 1; w < kThinWaves; ++w) acc += part[w][lane];
+        float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+        put<4, false>(a, col, n0 + 4 * g, v);
     }
 }
 
-template <int MT>
 void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
     const int grid = (a.d.N + 15) / 16;
     if (vec)
-        thin_kernel<MT, 8, true><<<grid, 512, 0, stream>>>(a);
+        thin_kernel<true><<<grid, 64 * kThinWaves, 0, stream>>>(a);
     else
-        thin_kernel<MT, 8, false><<<grid, 512, 0, stream>>>(a);
+        thin_kernel<false><<<grid, 64 * kThinWaves, 0, stream>>>(a);
+}
+
+template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
+void launch_tile(const LinearArgs& a, bool vec_out, hipStream_t stream) {
+    const int tiles = ((a.d.M + BM - 1) / BM) * ((a.d.N + BN - 1) / BN);
+    tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT><<<tiles, 64 * WM * WN * KG, 0, stream>>>(a, vec_out);
+}
+
+// Rows of any alignment to rows of 16-byte pieces.
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t stride, int64_t rows, int K, uint4* dst) {
+    const int per = (K + 7) / 8;
+    const int64_t n = rows * per, step = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
+        const int64_t r = i / per;
+        const int k = int(i - r * per) * 8;
+        dst[i] = load_k8(src + r * stride, k, K);
+    }
+}
+
+// Which operand rows do not start on 16 bytes, and whether copying those pays:
+// the tile kernel on such rows stages them through registers at 8.8e-9 us per
+// multiply-add (8192 x 8192 x 4095: 2411 us) instead of 1.6e-9, a copy costs
+// 0.9e-6 us per element, so it pays where M N / (M + N) exceeds about 125.
+struct Packing {
+    bool x, w;  // not aligned
+    bool copy;
+};
+Packing packing(const gdn_linear_dims& d) {
+    Packing p;
+    p.x = d.M > 1 && d.x_stride % 8 != 0;
+    p.w = d.N > 1 && d.w_stride % 8 != 0;
+    p.copy = (p.x || p.w) && d.K > 0 && double(d.M) * d.N > 125.0 * (double(d.M) + d.N);
+    return p;
+}
+size_t packed_bytes(int64_t rows, int K) { return (size_t(rows) * ((size_t(K) + 7) / 8) * 16 + 255) & ~size_t(255); }
+
+void launch_pack(const void* src, int64_t stride, int64_t rows, int K, void* dst, hipStream_t stream) {
+    const int64_t blocks = (rows * ((K + 7) / 8) + 255) / 256;
+    pack_kernel<<<static_cast<unsigned>(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(
+        static_cast<const uint16_t*>(src), stride, rows, K, static_cast<uint4*>(dst));
 }
 
 }  // namespace
 
-size_t linear_ws_bytes(const gdn_linear_dims&) { return 0; }
+size_t linear_ws_bytes(const gdn_linear_dims& d) {
+    const Packing p = packing(d);
+    return p.copy ? (p.x ? packed_bytes(d.M, d.K) : 0) + (p.w ? packed_bytes(d.N, d.K) : 0) : 0;
+}
 
-hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
-    const gdn_linear_dims& d = a.d;
-    // a tile's rows lie within 2^31 bytes of its first
-    const bool direct = d.K % 8 == 0 && (d.M <= 1 || d.x_stride % 8 == 0) && (d.N <= 1 || d.w_stride % 8 == 0) &&
-                        d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
+hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
+    LinearArgs a = args;
+    gdn_linear_dims& d = a.d;
+    const Packing p = packing(d);
+    if (p.copy) {
+        char* ws = static_cast<char*>(a.ws);
+        if (p.x) {
+            launch_pack(a.x, d.x_stride, d.M, d.K, ws, stream);
+            a.x = ws;
+            d.x_stride = (int64_t(d.K) + 7) / 8 * 8;
+            ws += packed_bytes(d.M, d.K);
+        }
+        if (p.w) {
+            launch_pack(a.w, d.w_stride, d.N, d.K, ws, stream);
+            a.w = ws;
+            d.w_stride = (int64_t(d.K) + 7) / 8 * 8;
+        }
+    }
+    const bool aligned = p.copy || !(p.x || p.w);
+    // direct loads: a tile's rows lie within 2^31 bytes of its first
+    const bool direct = aligned && d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
     const bool vec_out = d.N % 8 == 0 && (d.M <= 1 || (d.y_stride % 8 == 0 && (!a.res || d.res_stride % 8 == 0)));
-    auto tiles = [&](int bm, int bn) { return ((d.M + bm - 1) / bm) * ((d.N + bn - 1) / bn); };
-    if (d.M <= 16)
-        launch_thin<1>(a, direct, stream);
-    else if (d.M <= 32)
-        launch_thin<2>(a, direct, stream);
-    else if (d.M <= 64)
-        launch_thin<4>(a, direct, stream);
-    else if (tiles(256, 256) >= 256 && direct)
-        tile_kernel<256, 256, 2, 4, true><<<tiles(256, 256), 512, 0, stream>>>(a, vec_out);
-    else if (tiles(128, 128) >= 128 && direct)
-        tile_kernel<128, 128, 2, 2, true><<<tiles(128, 128), 256, 0, stream>>>(a, vec_out);
-    else if (direct)
-        tile_kernel<64, 64, 2, 2, true><<<tiles(64, 64), 256, 0, stream>>>(a, vec_out);
+    auto tiles = [&](int64_t t) { return double((d.M + t - 1) / t) * double((d.N + t - 1) / t); };
+    // What each kernel takes at K = 4096 in us (measured over M = 64 .. 8192,
+    // N = 4096 .. 12352); the ratios hold for other K.
+    const double t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
+    const double k64two = 16.0 * std::ceil(t64 / 256);   // 256 KiB of loads in flight per CU: few tiles
+    const double k64 = std::max(20.0, 0.05 * t64);       // two workgroups per CU
+    const double k128two = t128 <= 256 ? 36.0 : 1e30;    // one round of tiles, two groups per CU
+    const double k128 = std::max(43.0, 0.133 * t128);    // two workgroups per CU
+    const double k256 = 108.0 * std::ceil(t256 / 256);   // fewest bytes through LDS per product
+    const double best = std::min({k64two, k64, k128two, k128, k256});
+    if (d.M <= 16 && d.N <= 8192)
+        launch_thin(a, aligned && d.K % 8 == 0, stream);
+    else if (!direct)
+        launch_tile<64, 64, 2, 2, 4, 2, false>(a, vec_out, stream);
+    else if (best == k64two)
+        launch_tile<64, 64, 2, 2, 2, 4, true>(a, vec_out, stream);
+    else if (best == k64)
+        launch_tile<64, 64, 2, 2, 1, 4, true>(a, vec_out, stream);
+    else if (best == k128two)
+        launch_tile<128, 128, 2, 2, 2, 2, true>(a, vec_out, stream);
+    else if (best == k128)
+        launch_tile<128, 128, 2, 4, 1, 2, true>(a, vec_out, stream);
     else
-        tile_kernel<64, 64, 2, 2, false><<<tiles(64, 64), 256, 0, stream>>>(a, vec_out);
+        launch_tile<256, 256, 2, 4, 1, 2, true>(a, vec_out, stream);
     return hipGetLastError();
 }
 

@@ -112,14 +112,6 @@ __device__ __forceinline__ void split2(float x, __bf16& hi, __bf16& lo) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
-// Orders LDS between the wavefronts of a workgroup without waiting for
-// global loads and stores in flight.
-__device__ __forceinline__ void lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Orders LDS between the lanes of one wavefront.
 __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
