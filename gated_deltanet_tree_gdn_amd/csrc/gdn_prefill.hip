@@ -43,20 +43,21 @@ constexpr int kC = 64;  // tokens per chunk
 // 16 (j / 4) + 4 g + j % 4, the order in which accumulators hold rows, so that
 // a product's result is the next product's operand without moving lanes.
 struct PrepLayout {
-    size_t t, m, sc, info, total;
+    size_t t, m, sc, gam, total;
 };
 // T and M: the (row tile, 32-token step) pairs that reach the lower triangle.
 constexpr int kPairs = 6;
 __host__ __device__ constexpr int pair_at(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
 
 __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
-    const size_t slots = size_t(d.T) / kC + d.B, heads = slots * d.H_v;
+    // one slot more than can be used: the chain loads a chunk ahead
+    const size_t slots = size_t(d.T) / kC + d.B + 1, heads = slots * d.H_v;
     PrepLayout l;
     l.t = 0;
     l.m = l.t + heads * kPairs * 2 * 1024;
     l.sc = l.m + heads * kPairs * 2 * 1024;
-    l.info = l.sc + heads * kC * sizeof(float4);
-    l.total = (l.info + heads * sizeof(float2) + 255) & ~size_t(255);
+    l.gam = l.sc + heads * kC * sizeof(float4);
+    l.total = (l.gam + heads * sizeof(float) + 255) & ~size_t(255);
     return l;
 }
 
@@ -64,8 +65,9 @@ struct ChunkArgs {
     SeqArgs s;
     uint4* t;
     uint4* m;
-    float4* sc;    // per token: gamma |k|^-1, beta, scale gamma |q|^-1, e^{G_64 - G} |k|^-1 (norms 1 unless asked for)
-    float2* info;  // gamma_64, first token with a non-finite k, g or beta (kC if none, as int bits)
+    float4* sc;    // per token: gamma |k|^-1, beta, scale gamma |q|^-1, e^{G_64 - G} |k|^-1 (norms 1 unless
+                   // asked for); the first is NaN where k, g or beta is not finite
+    float* gam;    // gamma_64
     int slots;
 };
 
@@ -251,7 +253,6 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
             if (lane >= n) gv = bv = 0.0f;
             const bool gbad = !(gv < __builtin_inff()) || !finite(bv);
             const unsigned long long bad = (static_cast<unsigned long long>(badk[1]) << 32 | badk[0]) | __ballot(gbad);
-            const int first = bad ? __builtin_ctzll(bad) : kC;
             if (bad >> lane & 1) bv = 0.0f;
             // exp(g) is zero below -104, so larger decays would only cost precision
             gv = gbad ? 0.0f : fmaxf(gv, -104.0f);
@@ -267,10 +268,9 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
                 bet[hw][lane] = bv;
                 const float gam = __builtin_amdgcn_exp2f(static_cast<float>(G));
                 c.sc[sh * kC + lane] =
-                    make_float4(gam * rks[lane], bv, gam * rqs[lane], exp_diff(G63, G) * rks[lane]);
-                if (lane == 0)
-                    c.info[sh] = make_float2(__builtin_amdgcn_exp2f(static_cast<float>(G63)),
-                                             __builtin_bit_cast(float, first));
+                    make_float4(bad >> lane & 1 ? __builtin_nanf("") : gam * rks[lane], bv, gam * rqs[lane],
+                                exp_diff(G63, G) * rks[lane]);
+                if (lane == 0) c.gam[sh] = __builtin_amdgcn_exp2f(static_cast<float>(G63));
             }
         }
         __syncthreads();
@@ -457,12 +457,16 @@ template <int DK>
 struct TileRows {
     static constexpr int P = DK / 8, L = DK / 32, RPL = 64 / P;  // pieces per row, loads, rows per load
     uint4 x[L];
-    __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int last, int tile, int lane) {
+    uint32_t off[L];  // bytes, the lane's piece of each load's row
+    // `left` > 0 rows exist from the chunk's first on; further ones repeat the last.
+    __device__ __forceinline__ void rows(int64_t stride, int left, int tile, int lane) {
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const uint32_t row = min(16 * tile + j * RPL + lane / P, last);
-            x[j] = load_at<uint4>(base, (row * uint32_t(stride) + 8 * (lane % P)) * 2);
-        }
+        for (int j = 0; j < L; ++j)
+            off[j] = (uint32_t(min(16 * tile + j * RPL + lane / P, left - 1)) * uint32_t(stride) + 8 * (lane % P)) * 2;
+    }
+    __device__ __forceinline__ void load(const uint16_t* base) {
+#pragma unroll
+        for (int j = 0; j < L; ++j) x[j] = load_at<uint4>(base, off[j]);
     }
     __device__ __forceinline__ void put(uint4* tile_lds, int lane) const {
 #pragma unroll
@@ -480,16 +484,16 @@ struct ChainLds {
     uint4 R[2][2][NCT][64];        // R: hi, lo
     uint4 D[2][3][NCT][64];        // decayed U: three parts
     f32x4 U[4][NCT][64];           // U in fp32, rows of token tile [i] as accumulated
-    int4 marks;                    // wavefront i's R has a value that is not finite
+    int4 marks;                    // whether wavefront i's R has a value that is not finite
     uint8_t badrow[4][NCT][64];    // its rows, where marked
 };
 
 // The first row of each of the lane's columns that is not finite; kC if none.
 template <int DK, int NCT>
-__device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int chunk_first, int col, int (&first)[NCT]) {
+__device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int col, int (&first)[NCT]) {
     const int marks[4] = {l.marks.x, l.marks.y, l.marks.z, l.marks.w};
     for (int ct = 0; ct < NCT; ++ct) {
-        first[ct] = chunk_first;
+        first[ct] = kC;
         for (int w = 0; w < 4; ++w)
             if (marks[w])
                 for (int g = 0; g < 4; ++g) {
@@ -501,8 +505,11 @@ __device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int chunk_
 
 // Eight wavefronts: 0 .. 3 carry the state from chunk to chunk, 4 .. 7 form
 // the outputs beside them.  Three barriers per chunk:
-//   chain:  state operands | K S^T, R      | U, K^T operands    | state update, next K
-//   output:                | Q S^T, store  | next Q             | M U
+//   chain:  state operands | K S^T, R, K^T operands | U, next K | state update
+//   output:                | next Q, store          | Q S^T     | M U
+// LDS bandwidth is what the phases compete for: the outputs read the state
+// operands a phase after the chain does, and operands that do not depend on the
+// chain are read outside its critical phases.
 // Wavefront i of either kind owns token tile i (16 rows of the chunk); chain
 // wavefront i also owns d_k / 4 elements of the state's rows.
 //
@@ -527,65 +534,78 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     const Range seq = seq_range(a, b);
     const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
     const int64_t sh0 = int64_t(base) * d.H_v + h;
-    const float2* info_p = c.info + sh0;
+    if (lane == 0 && wave < 4) (&l.marks.x)[w] = 0;
 
     if (wave >= 4) {
         // ---- outputs ----
         if (chunks == 0) return;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq.start * d.q_stride + int64_t(hk) * DK;
         const uint4* mp = c.m + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const float4* sp = c.sc + sh0 * kC + 16 * w;
-        const int64_t m_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC;
+        const float* sp = reinterpret_cast<const float*>(c.sc + sh0 * kC + 16 * w) + 2;
+        const int64_t q_step = kC * d.q_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC * 4;
         const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + 4 * g) * ld + NCT * col;
-        const int64_t o0 = (seq.start * d.H_v + h) * d.d_v + v0;
-        uint4 mf[2][2];
+        int64_t o_at = (seq.start * d.H_v + h) * d.d_v + v0;
+        uint4 mf[2][2], qf[KS];
         TileRows<DK> qr;
         float cq[4];
-        auto load_q = [&](int ch) { qr.load(qp + ch * (kC * d.q_stride), d.q_stride, seq.len - ch * kC - 1, w, lane); };
-        auto load_c = [&](int ch) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                cq[r] = load_at<float>(reinterpret_cast<const float*>(sp + ch * s_step + r) + 2, g * 64);
+        qr.rows(d.q_stride, seq.len, w, lane);
+        // The chunk that `left` tokens are left from on.  The loads are not behind
+        // a branch (whose end would wait for them): past the sequence the last
+        // chunk is loaded again.
+        auto load_q = [&](int left) {
+            if (left < kC && left > 0) qr.rows(d.q_stride, left, w, lane);
+            qp += left > 0 ? q_step : 0;
+            qr.load(qp - q_step);
         };
-        auto load_m = [&](int ch) {
+        auto load_c = [&]() {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) cq[r] = load_at<float>(sp + 4 * r, g * 64);
+            sp += s_step;
+        };
+        auto load_m = [&]() {
 #pragma unroll
             for (int s = 0; s < 2; ++s)  // tiles 0 and 1 have one step: read again rather than branch
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    mf[s][p] = load_at<uint4>(mp + ch * m_step + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+                for (int p = 0; p < 2; ++p) mf[s][p] = load_at<uint4>(mp + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+            mp += m_step;
         };
-        load_q(0);
-        qr.put(l.Q[w], lane);
-        load_c(0);
+        auto turn_q = [&]() {  // rows to operands
+            wave_lds_fence();
+            qr.put(l.Q[w], lane);
+            wave_lds_fence();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
+        };
+        load_q(seq.len);
         __builtin_amdgcn_sched_barrier(0);
-        load_q(min(1, chunks - 1));
+        load_c();
         __builtin_amdgcn_sched_barrier(0);
-        load_m(0);
+        load_m();
         __builtin_amdgcn_sched_barrier(0);
         f32x4 O[NCT];
         int first[NCT];
         bool poisoned = false;
-        auto store = [&](int ch) {
+        auto store = [&](int n) {
             if (poisoned)
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (16 * w + 4 * g + r >= first[ct]) O[ct][r] = __builtin_nanf("");
-            const int64_t at = o0 + int64_t(ch) * kC * ld;
-            const int left = seq.len - ch * kC - (16 * w + 4 * g);
+            const int left = n < kC ? n - (16 * w + 4 * g) : 4;
             if (d.o_dtype == GDN_BF16)
-                store_rows<uint16_t, NCT>(static_cast<uint16_t*>(a.o) + at, o_off, ld, left, O);
+                store_rows<uint16_t, NCT>(static_cast<uint16_t*>(a.o) + o_at, o_off, ld, left, O);
             else
-                store_rows<float, NCT>(static_cast<float*>(a.o) + at, o_off, ld, left, O);
+                store_rows<float, NCT>(static_cast<float*>(a.o) + o_at, o_off, ld, left, O);
+            o_at += int64_t(kC) * ld;
         };
         for (int ch = 0; ch < chunks; ++ch) {
-            const int next = min(ch + 1, chunks - 1);
             lds_barrier();  // state operands written
+            turn_q();
+            load_q(seq.len - (ch + 1) * kC);
+            if (ch > 0) store(kC);
+            lds_barrier();  // R written
             f32x4 Qh[NCT], Ql[NCT];
-            uint4 qf[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 bf16x8 sh[KS], sl[KS];
@@ -601,28 +621,23 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     Ql[ct] = mfma(__builtin_bit_cast(bf16x8, qf[s]), sl[s], Ql[ct]);
                 }
             }
-            if (ch > 0) store(ch - 1);
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) O[ct][r] = cq[r] * (Qh[ct][r] + Ql[ct][r]);
-            load_c(next);
-            lds_barrier();  // R written
-            wave_lds_fence();
-            qr.put(l.Q[w], lane);
-            load_q(min(ch + 2, chunks - 1));
-            const int chunk_first = __builtin_bit_cast(int, info_p[int64_t(ch) * d.H_v].y);
+            load_c();
             lds_barrier();  // U written
             const int4 marks = l.marks;
-            poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0 || chunk_first < kC) != 0;
-            if (poisoned) first_bad(l, chunk_first, col, first);
             auto add = [&](auto steps) {
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
+                for (int ct = 0; ct < NCT; ++ct) {
+                    f32x4 u[4];
+#pragma unroll
+                    for (int i = 0; i < 2 * steps.value; ++i) u[i] = l.U[i][ct][lane];
 #pragma unroll
                     for (int s = 0; s < steps.value; ++s) {
-                        const f32x4 x0 = l.U[2 * s][ct][lane], x1 = l.U[2 * s + 1][ct][lane];
-                        const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+                        const float x[8] = {u[2 * s][0],     u[2 * s][1],     u[2 * s][2],     u[2 * s][3],
+                                            u[2 * s + 1][0], u[2 * s + 1][1], u[2 * s + 1][2], u[2 * s + 1][3]};
                         bf16x8 uh, ul;
                         split8(x, uh, ul);
                         const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
@@ -630,18 +645,22 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         O[ct] = mfma(mh, ul, O[ct]);
                         O[ct] = mfma(ml, uh, O[ct]);
                     }
+                }
             };
             if (w < 2)
                 add(std::integral_constant<int, 1>());
             else
                 add(std::integral_constant<int, 2>());
-            load_m(next);
+            poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0) != 0;
+            if (poisoned) first_bad(l, col, first);
+            load_m();
         }
-        store(chunks - 1);
+        store(seq.len - (chunks - 1) * kC);
         return;
     }
 
     // ---- the state ----
+    __builtin_amdgcn_s_setprio(3);  // the outputs only fill what the chain leaves
     if (a.seq_status && threadIdx.x == 0 && h == 0 && v0 == 0) a.seq_status[b] = seq.ok ? GDN_OK : GDN_ERR_SHAPE;
     const int pool = a.slot ? a.slot[b] : b;
     const bool keep = pool >= 0 && pool < d.n_slots;
@@ -662,47 +681,66 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
         const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
         const float4* sp = c.sc + sh0 * kC + 16 * w;
-        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64;
-        const int64_t s_step = int64_t(d.H_v) * kC;
+        const int64_t k_step = kC * d.k_stride, v_step = kC * d.v_stride;
+        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC;
         // Each group of inputs is loaded for the next chunk as soon as this chunk
         // has used it, so one set of registers covers a chunk's latency.
-        uint4 tf[2][2];
+        const float* gp = c.gam + sh0;
+        uint4 tf[2][2], kf[KS];
         TileRows<DK> kr;
         float4 sc[4];  // scalars of tokens 16 w + 4 g + r
         typename ValueBits<NCT>::type v[4];  // as loaded: converting at the load would wait for it
-        float2 info;
-        auto load_k = [&](int ch) { kr.load(kp + ch * (kC * d.k_stride), d.k_stride, seq.len - ch * kC - 1, w, lane); };
-        auto load_v = [&](int ch) {
-            const int last = seq.len - ch * kC - 1;
-            const uint16_t* pv = vp + ch * (kC * d.v_stride);
+        float gam;
+        uint32_t v_off[4];
+        auto v_rows = [&](int left) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                v[r] = load_at<typename ValueBits<NCT>::type>(
-                    pv, (uint32_t(min(16 * w + 4 * g + r, last)) * uint32_t(d.v_stride) + NCT * col) * 2);
+                v_off[r] = (uint32_t(min(16 * w + 4 * g + r, left - 1)) * uint32_t(d.v_stride) + NCT * col) * 2;
         };
-        auto load_t = [&](int ch) {
+        kr.rows(d.k_stride, seq.len, w, lane);
+        v_rows(seq.len);
+        // As for the outputs, no load is behind a branch.
+        auto load_k = [&](int left) {
+            if (left < kC && left > 0) kr.rows(d.k_stride, left, w, lane);
+            kp += left > 0 ? k_step : 0;
+            kr.load(kp - k_step);
+        };
+        auto turn_k = [&]() {  // rows to operands; the other wavefronts read them after the next barrier
+            kr.put(l.K[w], lane);
+            wave_lds_fence();
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
+        };
+        auto load_v = [&](int left) {
+            if (left < kC && left > 0) v_rows(left);
+            vp += left > 0 ? v_step : 0;
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    tf[s][p] = load_at<uint4>(tp + ch * t_step + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+            for (int r = 0; r < 4; ++r) v[r] = load_at<typename ValueBits<NCT>::type>(vp - v_step, v_off[r]);
+        };
+        auto load_t = [&]() {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[r] = load_at<float4>(sp + ch * s_step + r, g * 64);
+            for (int s = 0; s < 2; ++s)  // tiles 0 and 1 have one step: read again rather than branch
+#pragma unroll
+                for (int p = 0; p < 2; ++p) tf[s][p] = load_at<uint4>(tp + (2 * min(s, w >> 1) + p) * 64, lane * 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[r] = load_at<float4>(sp + r, g * 64);
+            tp += t_step;
+            sp += s_step;
         };
         // issued in the order of the loop: a wait for one group then lets the
         // groups behind it stay in flight
-        load_k(0);
-        kr.put(l.K[w], lane);
-        load_v(0);
+        load_k(seq.len);
+        turn_k();
+        load_v(seq.len);
         __builtin_amdgcn_sched_barrier(0);
-        load_t(0);
+        load_t();
         __builtin_amdgcn_sched_barrier(0);
-        load_k(min(1, chunks - 1));
-        info = info_p[0];
+        load_k(seq.len - kC);
+        gam = *gp;
         __builtin_amdgcn_sched_barrier(0);
+        bool was_marked = false;
         for (int ch = 0; ch < chunks; ++ch) {
             const int n = seq.len - ch * kC;  // 64 or more but for the last
-            const int next = min(ch + 1, chunks - 1);
 
             // the state as operands
 #pragma unroll
@@ -719,11 +757,8 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             lds_barrier();
 
             // K S^T of token tile w, then R = V - gamma K S^T
-            f32x4 R[NCT];
+            f32x4 R[NCT], Ph[NCT], Pl[NCT];
             float check = 0.0f;
-            uint4 kf[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 bf16x8 sh[KS], sl[KS];
@@ -732,16 +767,36 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
                     sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
                 }
-                f32x4 Ph = {0.0f, 0.0f, 0.0f, 0.0f}, Pl = Ph;
+                Ph[ct] = Pl[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    Ph = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph);
-                    Pl = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl);
+                    Ph[ct] = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph[ct]);
+                    Pl[ct] = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl[ct]);
+                }
+            }
+            // K^T of the wavefront's state rows: accumulator row rho of tile tau is
+            // element 32 (tau / 2) + 8 (rho / 4) + 4 (tau % 2) + rho % 4.  In a
+            // transposing read lane i of 16 names 4 elements of row i / 4 and gets
+            // element i of the 4 rows.
+            uint4 ktf[TPW][2];
+#pragma unroll
+            for (int i = 0; i < TPW; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int tau = w * TPW + i;
+                    uint2 x[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4* p = &l.K[2 * s + half][piece_at<DK>(4 * g + (col >> 2), 4 * (tau >> 1) + (col & 3))];
+                        x[half] = read_tr(reinterpret_cast<const uint2*>(p) + (tau & 1));
+                    }
+                    ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
                 }
 #pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[r].x * (Ph[r] + Pl[r]);
-            }
+                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[r].x * (Ph[ct][r] + Pl[ct][r]);
             if (n < kC)
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
@@ -756,7 +811,9 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) check = fmaf(R[ct][r], 0.0f, check);
             const bool marked = __ballot(!(check == 0.0f)) != 0;
-            if (marked)
+            if (marked || was_marked) {
+                if (lane == 0) (&l.marks.x)[w] = marked;
+                was_marked = marked;
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
                     unsigned m = 0;
@@ -768,7 +825,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         }
                     l.badrow[w][ct][lane] = m;
                 }
-            if (lane == 0) (&l.marks.x)[w] = marked;
+            }
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 __bf16 hi[4], lo[4];
@@ -777,7 +834,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, hi);
                 reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, lo);
             }
-            load_v(next);
+            load_v(n - kC);
             lds_barrier();
 
             // U = beta R + T R below the diagonal
@@ -808,36 +865,18 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 solve(std::integral_constant<int, 1>());
             else
                 solve(std::integral_constant<int, 2>());
-            // K^T of the wavefront's state rows: accumulator row rho of tile tau is
-            // element 32 (tau / 2) + 8 (rho / 4) + 4 (tau % 2) + rho % 4.  In a
-            // transposing read lane i of 16 names 4 elements of row i / 4 and gets
-            // element i of the 4 rows.
-            uint4 ktf[TPW][2];
-#pragma unroll
-            for (int i = 0; i < TPW; ++i)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int tau = w * TPW + i;
-                    uint2 x[2];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint4* p = &l.K[2 * s + half][piece_at<DK>(4 * g + (col >> 2), 4 * (tau >> 1) + (col & 3))];
-                        x[half] = read_tr(reinterpret_cast<const uint2*>(p) + (tau & 1));
-                    }
-                    ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
-                }
-            const int chunk_first = __builtin_bit_cast(int, info.y);
+            turn_k();
+            load_k(n - 2 * kC);
             float e[NCT][4];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 u0[ct] += u1[ct];
-                l.U[w][ct][lane] = u0[ct];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) e[ct][r] = u0[ct][r] * sc[r].w;
             }
-            if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0 || chunk_first < kC)) {
+            if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0)) {
                 int first[NCT];
-                first_bad(l, chunk_first, col, first);
+                first_bad(l, col, first);
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -855,8 +894,9 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 reinterpret_cast<uint2*>(&l.D[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dh);
                 reinterpret_cast<uint2*>(&l.D[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dm);
                 reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dl);
+                l.U[w][ct][lane] = u0[ct];
             }
-            load_t(next);
+            load_t();
             lds_barrier();
 
             // S <- gamma_64 S + K^T diag(decay) U
@@ -868,7 +908,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
                     for (int p = 0; p < 3; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][ct][lane]);
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) S[i][ct] *= info.x;
+                for (int i = 0; i < TPW; ++i) S[i][ct] *= gam;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -877,9 +917,8 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         for (int i = 0; i < TPW; ++i)
                             S[i][ct] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i][ct]);
             }
-            kr.put(l.K[w], lane);
-            load_k(min(ch + 2, chunks - 1));
-            info = info_p[int64_t(next) * d.H_v];
+            gp += d.H_v;
+            gam = *gp;
         }
     }
     if (keep)
@@ -919,7 +958,7 @@ hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream) {
                 reinterpret_cast<uint4*>(p + l.t),
                 reinterpret_cast<uint4*>(p + l.m),
                 reinterpret_cast<float4*>(p + l.sc),
-                reinterpret_cast<float2*>(p + l.info),
+                reinterpret_cast<float*>(p + l.gam),
                 a.d.T / kC + a.d.B};
     return a.d.d_k == 128 ? launch_chunks<128>(c, stream) : launch_chunks<64>(c, stream);
 }
