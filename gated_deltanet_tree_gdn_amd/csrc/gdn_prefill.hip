@@ -107,9 +107,20 @@ __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ void split2(float x, __bf16& hi, __bf16& lo) {
-    hi = static_cast<__bf16>(x);
-    lo = static_cast<__bf16>(x - static_cast<float>(hi));
+// Four accumulators as packed bf16 parts, x = hi + lo or hi + mid + lo, each
+// rounded to nearest; in pairs, as the conversions come.
+__device__ __forceinline__ uint2 take4(f32x4& x) {  // the leading part; x keeps the rest
+    const uint2 part = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    x -= f32x4{bf16_lo(part.x), bf16_hi(part.x), bf16_lo(part.y), bf16_hi(part.y)};
+    return part;
+}
+__device__ __forceinline__ void split4(f32x4 x, uint2& hi, uint2& lo) {
+    hi = take4(x);
+    lo = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+}
+__device__ __forceinline__ void split4(f32x4 x, uint2& hi, uint2& mid, uint2& lo) {
+    hi = take4(x);
+    split4(x, mid, lo);
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
@@ -330,25 +341,21 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
                 }
 #pragma unroll
                 for (int s = 0; s <= i / 2; ++s) {
-                    bf16x8 hi, lo;
+                    uint2 hi[2], lo[2];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int jt = 2 * s + half;
                         const f32x4 bj = *reinterpret_cast<const f32x4*>(&be[16 * jt + 4 * g]);
+                        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (jt < i) v = X[jt < i ? jt : i] * bj;
+                        if (jt == i)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            float v = 0.0f;
-                            if (jt < i) v = X[jt < i ? jt : i][r] * bj[r];
-                            if (jt == i) v = 4 * g + r < col ? X[i][r] * bj[r] : 0.0f;
-                            __bf16 h1, l1;
-                            split2(v, h1, l1);
-                            hi[4 * half + r] = h1;
-                            lo[4 * half + r] = l1;
-                        }
+                            for (int r = 0; r < 4; ++r) v[r] = 4 * g + r < col ? X[i][r] * bj[r] : 0.0f;
+                        split4(v, hi[half], lo[half]);
                     }
                     uint4* p = tp + pair_at(i, s) * 2 * 64 + lane;
-                    p[0] = __builtin_bit_cast(uint4, hi);
-                    p[64] = __builtin_bit_cast(uint4, lo);
+                    p[0] = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+                    p[64] = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
                 }
             };
             if (part == 0) {
@@ -367,20 +374,21 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (2 * s > w) continue;
-                bf16x8 hi, lo;
+                uint2 hi[2], lo[2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int jt = 2 * s + (j >> 2), tok = 16 * jt + 4 * g + (j & 3);
-                    float v = 0.0f;
-                    if (jt <= w && tok <= row) v = exp_diff(Gi, gcum[hh][tok]) * qk[jt][j & 3];
-                    __bf16 h1, l1;
-                    split2(v, h1, l1);
-                    hi[j] = h1;
-                    lo[j] = l1;
+                for (int half = 0; half < 2; ++half) {
+                    const int jt = 2 * s + half;
+                    f32x4 v;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int tok = 16 * jt + 4 * g + r;
+                        v[r] = tok <= row ? exp_diff(Gi, gcum[hh][tok]) * qk[jt][r] : 0.0f;
+                    }
+                    split4(v, hi[half], lo[half]);
                 }
                 uint4* p = mp + pair_at(w, s) * 2 * 64 + lane;
-                p[0] = __builtin_bit_cast(uint4, hi);
-                p[64] = __builtin_bit_cast(uint4, lo);
+                p[0] = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+                p[64] = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
             }
         }
         __syncthreads();
@@ -636,10 +644,11 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     for (int i = 0; i < 2 * steps.value; ++i) u[i] = l.U[i][ct][lane];
 #pragma unroll
                     for (int s = 0; s < steps.value; ++s) {
-                        const float x[8] = {u[2 * s][0],     u[2 * s][1],     u[2 * s][2],     u[2 * s][3],
-                                            u[2 * s + 1][0], u[2 * s + 1][1], u[2 * s + 1][2], u[2 * s + 1][3]};
-                        bf16x8 uh, ul;
-                        split8(x, uh, ul);
+                        uint2 h0, l0, h1, l1;
+                        split4(u[2 * s], h0, l0);
+                        split4(u[2 * s + 1], h1, l1);
+                        const bf16x8 uh = __builtin_bit_cast(bf16x8, make_uint4(h0.x, h0.y, h1.x, h1.y));
+                        const bf16x8 ul = __builtin_bit_cast(bf16x8, make_uint4(l0.x, l0.y, l1.x, l1.y));
                         const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
                         O[ct] = mfma(mh, uh, O[ct]);
                         O[ct] = mfma(mh, ul, O[ct]);
@@ -748,11 +757,10 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
                 for (int i = 0; i < TPW; ++i) {
                     const int tau = w * TPW + i;
-                    __bf16 hi[4], lo[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) split2(S[i][ct][r], hi[r], lo[r]);
-                    reinterpret_cast<uint2*>(&l.S[tau >> 1][0][ct][lane])[tau & 1] = __builtin_bit_cast(uint2, hi);
-                    reinterpret_cast<uint2*>(&l.S[tau >> 1][1][ct][lane])[tau & 1] = __builtin_bit_cast(uint2, lo);
+                    uint2 hi, lo;
+                    split4(S[i][ct], hi, lo);
+                    reinterpret_cast<uint2*>(&l.S[tau >> 1][0][ct][lane])[tau & 1] = hi;
+                    reinterpret_cast<uint2*>(&l.S[tau >> 1][1][ct][lane])[tau & 1] = lo;
                 }
             lds_barrier();
 
@@ -828,11 +836,10 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             }
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                __bf16 hi[4], lo[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) split2(R[ct][r], hi[r], lo[r]);
-                reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, hi);
-                reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, lo);
+                uint2 hi, lo;
+                split4(R[ct], hi, lo);
+                reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = hi;
+                reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = lo;
             }
             load_v(n - kC);
             lds_barrier();
@@ -867,7 +874,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 solve(std::integral_constant<int, 2>());
             turn_k();
             load_k(n - 2 * kC);
-            float e[NCT][4];
+            f32x4 e[NCT];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 u0[ct] += u1[ct];
@@ -885,15 +892,11 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             }
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                __bf16 dh[4], dm[4], dl[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dh[r] = static_cast<__bf16>(e[ct][r]);
-                    split2(e[ct][r] - static_cast<float>(dh[r]), dm[r], dl[r]);
-                }
-                reinterpret_cast<uint2*>(&l.D[w >> 1][0][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dh);
-                reinterpret_cast<uint2*>(&l.D[w >> 1][1][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dm);
-                reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = __builtin_bit_cast(uint2, dl);
+                uint2 hi, mid, lo;
+                split4(e[ct], hi, mid, lo);
+                reinterpret_cast<uint2*>(&l.D[w >> 1][0][ct][lane])[w & 1] = hi;
+                reinterpret_cast<uint2*>(&l.D[w >> 1][1][ct][lane])[w & 1] = mid;
+                reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = lo;
                 l.U[w][ct][lane] = u0[ct];
             }
             load_t();
