@@ -56,7 +56,7 @@ __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
     l.t = 0;
     l.m = l.t + heads * kPairs * 2 * 1024;
     l.sc = l.m + heads * kPairs * 2 * 1024;
-    l.gam = l.sc + heads * kC * sizeof(float4);
+    l.gam = l.sc + heads * 4 * kC * sizeof(float);
     l.total = (l.gam + heads * sizeof(float) + 255) & ~size_t(255);
     return l;
 }
@@ -65,8 +65,8 @@ struct ChunkArgs {
     SeqArgs s;
     uint4* t;
     uint4* m;
-    float4* sc;    // per token: gamma |k|^-1, beta, scale gamma |q|^-1, e^{G_64 - G} |k|^-1 (norms 1 unless
-                   // asked for); the first is NaN where k, g or beta is not finite
+    float* sc;     // 4 x 64: gamma |k|^-1, beta, e^{G_64 - G} |k|^-1 and scale gamma |q|^-1 of every token (norms
+                   // 1 unless asked for); the first is NaN where k, g or beta is not finite
     float* gam;    // gamma_64
     int slots;
 };
@@ -101,6 +101,23 @@ __device__ __forceinline__ int find_seq(const SeqArgs& a, int slot) {
         n = min(step, n - last * step);
     }
     return lo;
+}
+
+// The sequence with the r-th most tokens of up to 64 (the lower index first
+// among equals): workgroups start in order of their number, and a long
+// sequence that starts late is what the others wait for.  More sequences than
+// that are taken as they come.
+__device__ __forceinline__ int longest_seq(const SeqArgs& a, int r) {
+    const int B = a.d.B;
+    if (B > 64) return r;
+    const int lane = threadIdx.x & 63;
+    const int len = lane < B ? seq_range(a, lane).len : -1;
+    int rank = 0;
+    for (int j = 0; j < B; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < B && rank == r));
 }
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4& c) {
@@ -278,9 +295,11 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
                 gcum[hw][lane] = G;
                 bet[hw][lane] = bv;
                 const float gam = __builtin_amdgcn_exp2f(static_cast<float>(G));
-                c.sc[sh * kC + lane] =
-                    make_float4(bad >> lane & 1 ? __builtin_nanf("") : gam * rks[lane], bv, gam * rqs[lane],
-                                exp_diff(G63, G) * rks[lane]);
+                float* sc = c.sc + sh * 4 * kC + lane;
+                sc[0] = bad >> lane & 1 ? __builtin_nanf("") : gam * rks[lane];
+                sc[kC] = bv;
+                sc[2 * kC] = exp_diff(G63, G) * rks[lane];
+                sc[3 * kC] = gam * rqs[lane];
                 if (lane == 0) c.gam[sh] = __builtin_amdgcn_exp2f(static_cast<float>(G63));
             }
         }
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     const int group = d.H_v / d.H_k, slices = d.d_v / (16 * NCT), per = group * slices;
     const int j8 = blockIdx.x >> 3, item = (blockIdx.x & 7) + 8 * (j8 / per), part = j8 % per;
     if (item >= d.B * d.H_k) return;
-    const int b = item / d.H_k, hk = item % d.H_k, h = hk * group + part / slices, v0 = (part % slices) * 16 * NCT;
+    const int b = longest_seq(a, item / d.H_k), hk = item % d.H_k, h = hk * group + part / slices, v0 = (part % slices) * 16 * NCT;
 
     const Range seq = seq_range(a, b);
     const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
@@ -549,13 +568,13 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         if (chunks == 0) return;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq.start * d.q_stride + int64_t(hk) * DK;
         const uint4* mp = c.m + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const float* sp = reinterpret_cast<const float*>(c.sc + sh0 * kC + 16 * w) + 2;
+        const float* sp = c.sc + sh0 * 4 * kC + 3 * kC + 16 * w;
         const int64_t q_step = kC * d.q_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC * 4;
         const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + 4 * g) * ld + NCT * col;
         int64_t o_at = (seq.start * d.H_v + h) * d.d_v + v0;
         uint4 mf[2][2], qf[KS];
         TileRows<DK> qr;
-        float cq[4];
+        f32x4 cq;
         qr.rows(d.q_stride, seq.len, w, lane);
         // The chunk that `left` tokens are left from on.  The loads are not behind
         // a branch (whose end would wait for them): past the sequence the last
@@ -566,8 +585,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             qr.load(qp - q_step);
         };
         auto load_c = [&]() {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) cq[r] = load_at<float>(sp + 4 * r, g * 64);
+            cq = load_at<f32x4>(sp, g * 16);
             sp += s_step;
         };
         auto load_m = [&]() {
@@ -689,15 +707,15 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         const uint16_t* kp = static_cast<const uint16_t*>(a.k) + seq.start * d.k_stride + int64_t(hk) * DK;
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
         const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const float4* sp = c.sc + sh0 * kC + 16 * w;
+        const float* sp = c.sc + sh0 * 4 * kC + 16 * w;
         const int64_t k_step = kC * d.k_stride, v_step = kC * d.v_stride;
-        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC;
+        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC * 4;
         // Each group of inputs is loaded for the next chunk as soon as this chunk
         // has used it, so one set of registers covers a chunk's latency.
         const float* gp = c.gam + sh0;
-        uint4 tf[2][2], kf[KS];
+        uint4 tf[2][2];
         TileRows<DK> kr;
-        float4 sc[4];  // scalars of tokens 16 w + 4 g + r
+        f32x4 sc[3];  // scalars of tokens 16 w + 4 g + r
         typename ValueBits<NCT>::type v[4];  // as loaded: converting at the load would wait for it
         float gam;
         uint32_t v_off[4];
@@ -714,12 +732,6 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             kp += left > 0 ? k_step : 0;
             kr.load(kp - k_step);
         };
-        auto turn_k = [&]() {  // rows to operands; the other wavefronts read them after the next barrier
-            kr.put(l.K[w], lane);
-            wave_lds_fence();
-#pragma unroll
-            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
-        };
         auto load_v = [&](int left) {
             if (left < kC && left > 0) v_rows(left);
             vp += left > 0 ? v_step : 0;
@@ -732,14 +744,14 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) tf[s][p] = load_at<uint4>(tp + (2 * min(s, w >> 1) + p) * 64, lane * 16);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[r] = load_at<float4>(sp + r, g * 64);
+            for (int r = 0; r < 3; ++r) sc[r] = load_at<f32x4>(sp + r * kC, g * 16);
             tp += t_step;
             sp += s_step;
         };
         // issued in the order of the loop: a wait for one group then lets the
         // groups behind it stay in flight
         load_k(seq.len);
-        turn_k();
+        kr.put(l.K[w], lane);
         load_v(seq.len);
         __builtin_amdgcn_sched_barrier(0);
         load_t();
@@ -766,6 +778,9 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 
             // K S^T of token tile w, then R = V - gamma K S^T
             f32x4 R[NCT], Ph[NCT], Pl[NCT];
+            uint4 kf[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
             float check = 0.0f;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
@@ -804,7 +819,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[r].x * (Ph[ct][r] + Pl[ct][r]);
+                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[0][r] * (Ph[ct][r] + Pl[ct][r]);
             if (n < kC)
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
@@ -856,7 +871,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][ct][lane]);
                     }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) u0[ct][r] = sc[r].y * R[ct][r];
+                    for (int r = 0; r < 4; ++r) u0[ct][r] = sc[1][r] * R[ct][r];
                     u1[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int s = 0; s < steps.value; ++s) {
@@ -872,14 +887,14 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 solve(std::integral_constant<int, 1>());
             else
                 solve(std::integral_constant<int, 2>());
-            turn_k();
+            kr.put(l.K[w], lane);
             load_k(n - 2 * kC);
             f32x4 e[NCT];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 u0[ct] += u1[ct];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) e[ct][r] = u0[ct][r] * sc[r].w;
+                for (int r = 0; r < 4; ++r) e[ct][r] = u0[ct][r] * sc[2][r];
             }
             if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0)) {
                 int first[NCT];
@@ -960,7 +975,7 @@ hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream) {
     ChunkArgs c{a,
                 reinterpret_cast<uint4*>(p + l.t),
                 reinterpret_cast<uint4*>(p + l.m),
-                reinterpret_cast<float4*>(p + l.sc),
+                reinterpret_cast<float*>(p + l.sc),
                 reinterpret_cast<float*>(p + l.gam),
                 a.d.T / kC + a.d.B};
     return a.d.d_k == 128 ? launch_chunks<128>(c, stream) : launch_chunks<64>(c, stream);
