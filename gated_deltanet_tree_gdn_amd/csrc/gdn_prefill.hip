@@ -43,8 +43,9 @@ constexpr int kC = 64;  // tokens per chunk
 // 16 (j / 4) + 4 g + j % 4, the order in which accumulators hold rows, so that
 // a product's result is the next product's operand without moving lanes.
 struct PrepLayout {
-    size_t t, m, sc, gam, total;
+    size_t t, m, sc, total;
 };
+constexpr int kScalars = 4 * kC + 4;  // floats per (slot, head), whole 16-byte pieces
 // T and M: the (row tile, 32-token step) pairs that reach the lower triangle.
 constexpr int kPairs = 6;
 __host__ __device__ constexpr int pair_at(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
@@ -56,8 +57,7 @@ __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
     l.t = 0;
     l.m = l.t + heads * kPairs * 2 * 1024;
     l.sc = l.m + heads * kPairs * 2 * 1024;
-    l.gam = l.sc + heads * 4 * kC * sizeof(float);
-    l.total = (l.gam + heads * sizeof(float) + 255) & ~size_t(255);
+    l.total = (l.sc + heads * kScalars * sizeof(float) + 255) & ~size_t(255);
     return l;
 }
 
@@ -66,8 +66,7 @@ struct ChunkArgs {
     uint4* t;
     uint4* m;
     float* sc;     // 4 x 64: gamma |k|^-1, beta, e^{G_64 - G} |k|^-1 and scale gamma |q|^-1 of every token (norms
-                   // 1 unless asked for); the first is NaN where k, g or beta is not finite
-    float* gam;    // gamma_64
+                   // 1 unless asked for), the first NaN where k, g or beta is not finite; then gamma_64
     int slots;
 };
 
@@ -295,12 +294,12 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
                 gcum[hw][lane] = G;
                 bet[hw][lane] = bv;
                 const float gam = __builtin_amdgcn_exp2f(static_cast<float>(G));
-                float* sc = c.sc + sh * 4 * kC + lane;
+                float* sc = c.sc + sh * kScalars + lane;
                 sc[0] = bad >> lane & 1 ? __builtin_nanf("") : gam * rks[lane];
                 sc[kC] = bv;
                 sc[2 * kC] = exp_diff(G63, G) * rks[lane];
                 sc[3 * kC] = gam * rqs[lane];
-                if (lane == 0) c.gam[sh] = __builtin_amdgcn_exp2f(static_cast<float>(G63));
+                if (lane == 0) sc[4 * kC] = __builtin_amdgcn_exp2f(static_cast<float>(G63));
             }
         }
         __syncthreads();
@@ -418,20 +417,6 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
 // 2. per (sequence, value head, slice of d_v)
 // ----------------------------------------------------------------------------
 
-// NCT adjacent bf16 values.
-template <int NCT>
-struct ValueBits;
-template <>
-struct ValueBits<1> {
-    typedef uint16_t type;
-    static __device__ __forceinline__ float at(type u, int) { return bf16_lo(u); }
-};
-template <>
-struct ValueBits<2> {
-    typedef uint32_t type;
-    static __device__ __forceinline__ float at(type u, int ct) { return ct ? bf16_hi(u) : bf16_lo(u); }
-};
-
 // A load from a uniform base and a lane's 32-bit byte offset.
 template <typename T>
 __device__ __forceinline__ T load_at(const void* base, uint32_t off) {
@@ -443,27 +428,6 @@ __device__ __forceinline__ uint2 read_tr(const uint2* p) {
     typedef short s16x4v __attribute__((ext_vector_type(4)));
     return __builtin_bit_cast(
         uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v*)(p)));
-}
-
-// Rows row0 .. row0 + 3 of an output tile: those below n.
-template <typename T, int NCT>
-__device__ __forceinline__ void store_rows(T* base, uint32_t off, uint32_t ld, int left, const f32x4 (&x)[NCT]) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (r < left) {
-            T* p = base + (off + r * ld);
-            if constexpr (sizeof(T) == 2) {
-                if constexpr (NCT == 1)
-                    *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(x[0][r]);
-                else
-                    *reinterpret_cast<uint32_t*>(p) = pack_bf16(x[0][r], x[1][r]);
-            } else {
-                if constexpr (NCT == 1)
-                    *p = x[0][r];
-                else
-                    *reinterpret_cast<float2*>(p) = make_float2(x[0][r], x[1][r]);
-            }
-        }
 }
 
 // Rows of K and Q are loaded in the order of memory (a wavefront's load covers
@@ -511,6 +475,8 @@ struct ChainLds {
     uint4 R[2][2][NCT][64];        // R: hi, lo
     uint4 D[2][3][NCT][64];        // decayed U: three parts
     f32x4 U[4][NCT][64];           // U in fp32, rows of token tile [i] as accumulated
+    uint4 V[kC * 2 * NCT];         // the chunk's rows of the slice's values
+    float sc[kScalars];            // its scalars
     int4 marks;                    // whether wavefront i's R has a value that is not finite
     uint8_t badrow[4][NCT][64];    // its rows, where marked
 };
@@ -540,8 +506,11 @@ __device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int col, i
 // Wavefront i of either kind owns token tile i (16 rows of the chunk); chain
 // wavefront i also owns d_k / 4 elements of the state's rows.
 //
-// NCT column tiles of 16 values per workgroup: lane column `col` of tile ct is
-// value NCT col + ct of the slice, so a lane's NCT values are adjacent.
+// Vector memory instructions are dear too (16 clocks each for 1 KiB or less), so
+// values and scalars go through LDS rather than to each lane from memory, and
+// outputs are formed transposed: a lane then stores 4 adjacent values.
+//
+// NCT column tiles of 16 values per workgroup.
 template <int DK, int NCT>
 __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     constexpr int KS = DK / 32, TPW = DK / 64;
@@ -568,121 +537,113 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         if (chunks == 0) return;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq.start * d.q_stride + int64_t(hk) * DK;
         const uint4* mp = c.m + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const float* sp = c.sc + sh0 * 4 * kC + 3 * kC + 16 * w;
-        const int64_t q_step = kC * d.q_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC * 4;
-        const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + 4 * g) * ld + NCT * col;
+        const int64_t q_step = kC * d.q_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + col) * ld + 4 * g;
         int64_t o_at = (seq.start * d.H_v + h) * d.d_v + v0;
-        uint4 mf[2][2], qf[KS];
-        TileRows<DK> qr;
-        f32x4 cq;
-        qr.rows(d.q_stride, seq.len, w, lane);
-        // The chunk that `left` tokens are left from on.  The loads are not behind
-        // a branch (whose end would wait for them): past the sequence the last
-        // chunk is loaded again.
-        auto load_q = [&](int left) {
-            if (left < kC && left > 0) qr.rows(d.q_stride, left, w, lane);
-            qp += left > 0 ? q_step : 0;
-            qr.load(qp - q_step);
-        };
-        auto load_c = [&]() {
-            cq = load_at<f32x4>(sp, g * 16);
-            sp += s_step;
-        };
-        auto load_m = [&]() {
+        auto run = [&](auto steps_of_tile) {
+            constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
+            uint4 mf[kSteps][2], qf[KS];
+            TileRows<DK> qr;
+            qr.rows(d.q_stride, seq.len, w, lane);
+            // The chunk that `left` tokens are left from on.  The loads are not behind
+            // a branch (whose end would wait for them): past the sequence the last
+            // chunk is loaded again.
+            auto load_q = [&](int left) {
+                if (left < kC && left > 0) qr.rows(d.q_stride, left, w, lane);
+                qp += left > 0 ? q_step : 0;
+                qr.load(qp - q_step);
+            };
+            auto load_m = [&]() {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)  // tiles 0 and 1 have one step: read again rather than branch
+                for (int i = 0; i < 2 * kSteps; ++i) mf[i >> 1][i & 1] = load_at<uint4>(mp + i * 64, lane * 16);
+                mp += m_step;
+            };
+            auto turn_q = [&]() {  // rows to operands
+                wave_lds_fence();
+                qr.put(l.Q[w], lane);
+                wave_lds_fence();
 #pragma unroll
-                for (int p = 0; p < 2; ++p) mf[s][p] = load_at<uint4>(mp + (2 * min(s, w >> 1) + p) * 64, lane * 16);
-            mp += m_step;
-        };
-        auto turn_q = [&]() {  // rows to operands
-            wave_lds_fence();
-            qr.put(l.Q[w], lane);
-            wave_lds_fence();
+                for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
+            };
+            load_q(seq.len);
+            __builtin_amdgcn_sched_barrier(0);
+            load_m();
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 O[NCT];  // transposed: column = token 16 w + col, rows = values 16 ct + 4 g + r
+            int first[NCT];
+            bool poisoned = false;
+            auto store = [&](int n) {
+                if (poisoned)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
-        };
-        load_q(seq.len);
-        __builtin_amdgcn_sched_barrier(0);
-        load_c();
-        __builtin_amdgcn_sched_barrier(0);
-        load_m();
-        __builtin_amdgcn_sched_barrier(0);
-        f32x4 O[NCT];
-        int first[NCT];
-        bool poisoned = false;
-        auto store = [&](int n) {
-            if (poisoned)
+                    for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
+                        for (int r = 0; r < 4; ++r)
+                            if (16 * w + col >= __shfl(first[ct], 4 * g + r)) O[ct][r] = __builtin_nanf("");
+                if (16 * w + col < n)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * w + 4 * g + r >= first[ct]) O[ct][r] = __builtin_nanf("");
-            const int left = n < kC ? n - (16 * w + 4 * g) : 4;
-            if (d.o_dtype == GDN_BF16)
-                store_rows<uint16_t, NCT>(static_cast<uint16_t*>(a.o) + o_at, o_off, ld, left, O);
-            else
-                store_rows<float, NCT>(static_cast<float*>(a.o) + o_at, o_off, ld, left, O);
-            o_at += int64_t(kC) * ld;
-        };
-        for (int ch = 0; ch < chunks; ++ch) {
-            lds_barrier();  // state operands written
-            turn_q();
-            load_q(seq.len - (ch + 1) * kC);
-            if (ch > 0) store(kC);
-            lds_barrier();  // R written
-            f32x4 Qh[NCT], Ql[NCT];
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                bf16x8 sh[KS], sl[KS];
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
-                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
-                }
-                Qh[ct] = Ql[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    Qh[ct] = mfma(__builtin_bit_cast(bf16x8, qf[s]), sh[s], Qh[ct]);
-                    Ql[ct] = mfma(__builtin_bit_cast(bf16x8, qf[s]), sl[s], Ql[ct]);
-                }
-            }
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) O[ct][r] = cq[r] * (Qh[ct][r] + Ql[ct][r]);
-            load_c();
-            lds_barrier();  // U written
-            const int4 marks = l.marks;
-            auto add = [&](auto steps) {
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        const int64_t at = o_at + 16 * ct + o_off;
+                        if (d.o_dtype == GDN_BF16)
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + at) =
+                                make_uint2(pack_bf16(O[ct][0], O[ct][1]), pack_bf16(O[ct][2], O[ct][3]));
+                        else
+                            *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + at) = O[ct];
+                    }
+                o_at += int64_t(kC) * ld;
+            };
+            for (int ch = 0; ch < chunks; ++ch) {
+                lds_barrier();  // state operands, values and scalars written
+                turn_q();
+                load_q(seq.len - (ch + 1) * kC);
+                if (ch > 0) store(kC);
+                lds_barrier();  // R written
+                const float cq = l.sc[3 * kC + 16 * w + col];
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
-                    f32x4 u[4];
+                    bf16x8 sh[KS], sl[KS];
 #pragma unroll
-                    for (int i = 0; i < 2 * steps.value; ++i) u[i] = l.U[i][ct][lane];
+                    for (int s = 0; s < KS; ++s) {
+                        sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
+                        sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
+                    }
+                    f32x4 Qh = {0.0f, 0.0f, 0.0f, 0.0f}, Ql = Qh;
 #pragma unroll
-                    for (int s = 0; s < steps.value; ++s) {
+                    for (int s = 0; s < KS; ++s) {
+                        Qh = mfma(sh[s], __builtin_bit_cast(bf16x8, qf[s]), Qh);
+                        Ql = mfma(sl[s], __builtin_bit_cast(bf16x8, qf[s]), Ql);
+                    }
+                    O[ct] = cq * (Qh + Ql);
+                }
+                lds_barrier();  // U written
+                const int4 marks = l.marks;
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    f32x4 u[2 * kSteps];
+#pragma unroll
+                    for (int i = 0; i < 2 * kSteps; ++i) u[i] = l.U[i][ct][lane];
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
                         uint2 h0, l0, h1, l1;
                         split4(u[2 * s], h0, l0);
                         split4(u[2 * s + 1], h1, l1);
                         const bf16x8 uh = __builtin_bit_cast(bf16x8, make_uint4(h0.x, h0.y, h1.x, h1.y));
                         const bf16x8 ul = __builtin_bit_cast(bf16x8, make_uint4(l0.x, l0.y, l1.x, l1.y));
                         const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
-                        O[ct] = mfma(mh, uh, O[ct]);
-                        O[ct] = mfma(mh, ul, O[ct]);
-                        O[ct] = mfma(ml, uh, O[ct]);
+                        O[ct] = mfma(uh, mh, O[ct]);
+                        O[ct] = mfma(ul, mh, O[ct]);
+                        O[ct] = mfma(uh, ml, O[ct]);
                     }
                 }
-            };
-            if (w < 2)
-                add(std::integral_constant<int, 1>());
-            else
-                add(std::integral_constant<int, 2>());
-            poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0) != 0;
-            if (poisoned) first_bad(l, col, first);
-            load_m();
-        }
-        store(seq.len - (chunks - 1) * kC);
+                poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0) != 0;
+                if (poisoned) first_bad(l, col, first);
+                load_m();
+            }
+            store(seq.len - (chunks - 1) * kC);
+        };
+        if (w < 2)
+            run(std::integral_constant<int, 1>());
+        else
+            run(std::integral_constant<int, 2>());
         return;
     }
 
@@ -693,7 +654,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     const bool keep = pool >= 0 && pool < d.n_slots;
     const bool resume = keep && (!a.has_state || a.has_state[b] != 0);
     // state rows (elements of d_k) 32 (tau / 2) + 8 g + 4 (tau % 2) + r of tile tau
-    float* Sp = keep ? a.S + ((int64_t(pool) * d.H_v + h) * d.d_v + v0 + NCT * col) * DK + 8 * g : nullptr;
+    float* Sp = keep ? a.S + ((int64_t(pool) * d.H_v + h) * d.d_v + v0 + col) * DK + 8 * g : nullptr;
     f32x4 S[TPW][NCT];
 #pragma unroll
     for (int i = 0; i < TPW; ++i)
@@ -701,63 +662,70 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         for (int ct = 0; ct < NCT; ++ct) {
             const int tau = w * TPW + i;
             S[i][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (resume) S[i][ct] = *reinterpret_cast<const f32x4*>(Sp + ct * DK + 32 * (tau >> 1) + 4 * (tau & 1));
+            if (resume) S[i][ct] = *reinterpret_cast<const f32x4*>(Sp + ct * 16 * DK + 32 * (tau >> 1) + 4 * (tau & 1));
         }
-    if (chunks > 0) {
+    auto run = [&](auto steps_of_tile) {
+        constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
         const uint16_t* kp = static_cast<const uint16_t*>(a.k) + seq.start * d.k_stride + int64_t(hk) * DK;
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
         const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const float* sp = c.sc + sh0 * 4 * kC + 16 * w;
-        const int64_t k_step = kC * d.k_stride, v_step = kC * d.v_stride;
-        const int64_t t_step = int64_t(d.H_v) * kPairs * 2 * 64, s_step = int64_t(d.H_v) * kC * 4;
-        // Each group of inputs is loaded for the next chunk as soon as this chunk
-        // has used it, so one set of registers covers a chunk's latency.
-        const float* gp = c.gam + sh0;
-        uint4 tf[2][2];
+        const int64_t k_step = kC * d.k_stride, v_step = kC * d.v_stride, t_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        // wavefront 2 loads the scalars of every token, wavefront 3 gamma_64
+        const float* xp = c.sc + sh0 * kScalars;
+        const uint32_t x_off = (w == 3 ? kC : lane) * 16;
+        const int64_t x_step = int64_t(d.H_v) * kScalars;
+        // Each group of inputs is loaded for the next chunk (or the one after) as
+        // soon as this chunk has used it, so one set of registers covers a chunk's
+        // latency.  As for the outputs, no load is behind a branch.
+        uint4 tf[kSteps][2], vr, xr;
         TileRows<DK> kr;
-        f32x4 sc[3];  // scalars of tokens 16 w + 4 g + r
-        typename ValueBits<NCT>::type v[4];  // as loaded: converting at the load would wait for it
-        float gam;
-        uint32_t v_off[4];
-        auto v_rows = [&](int left) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v_off[r] = (uint32_t(min(16 * w + 4 * g + r, left - 1)) * uint32_t(d.v_stride) + NCT * col) * 2;
-        };
         kr.rows(d.k_stride, seq.len, w, lane);
+        // V: a row of the slice is 2 NCT pieces; the lane's piece
+        const int vi = (w * 64 + lane) % (kC * 2 * NCT);
+        uint32_t v_off;
+        auto v_rows = [&](int left) {
+            v_off = (uint32_t(min(vi / (2 * NCT), left - 1)) * uint32_t(d.v_stride) + 8 * (vi % (2 * NCT))) * 2;
+        };
         v_rows(seq.len);
-        // As for the outputs, no load is behind a branch.
         auto load_k = [&](int left) {
             if (left < kC && left > 0) kr.rows(d.k_stride, left, w, lane);
             kp += left > 0 ? k_step : 0;
             kr.load(kp - k_step);
         };
         auto load_v = [&](int left) {
-            if (left < kC && left > 0) v_rows(left);
-            vp += left > 0 ? v_step : 0;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = load_at<typename ValueBits<NCT>::type>(vp - v_step, v_off[r]);
+            if (NCT > 1 || kSteps == 1) {  // one tile: wavefronts 0 and 1 hold all pieces
+                if (left < kC && left > 0) v_rows(left);
+                vp += left > 0 ? v_step : 0;
+                vr = load_at<uint4>(vp - v_step, v_off);
+            }
+            if (kSteps == 2) {
+                xp += left > 0 ? x_step : 0;
+                xr = load_at<uint4>(xp - x_step, x_off);
+            }
+        };
+        auto put_v = [&]() {
+            if (NCT > 1 || kSteps == 1) l.V[vi] = vr;
+            if (kSteps == 2) {
+                if (w == 2 || lane == 0) *reinterpret_cast<uint4*>(&l.sc[x_off / 4]) = xr;
+            }
         };
         auto load_t = [&]() {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)  // tiles 0 and 1 have one step: read again rather than branch
-#pragma unroll
-                for (int p = 0; p < 2; ++p) tf[s][p] = load_at<uint4>(tp + (2 * min(s, w >> 1) + p) * 64, lane * 16);
-#pragma unroll
-            for (int r = 0; r < 3; ++r) sc[r] = load_at<f32x4>(sp + r * kC, g * 16);
+            for (int i = 0; i < 2 * kSteps; ++i) tf[i >> 1][i & 1] = load_at<uint4>(tp + i * 64, lane * 16);
             tp += t_step;
-            sp += s_step;
         };
         // issued in the order of the loop: a wait for one group then lets the
         // groups behind it stay in flight
         load_k(seq.len);
-        kr.put(l.K[w], lane);
         load_v(seq.len);
+        kr.put(l.K[w], lane);
+        put_v();
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(seq.len - kC);
         __builtin_amdgcn_sched_barrier(0);
         load_t();
         __builtin_amdgcn_sched_barrier(0);
-        load_k(seq.len - kC);
-        gam = *gp;
+        load_v(seq.len - kC);
         __builtin_amdgcn_sched_barrier(0);
         bool was_marked = false;
         for (int ch = 0; ch < chunks; ++ch) {
@@ -815,11 +783,15 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     }
                     ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
                 }
+            const f32x4 cp = *reinterpret_cast<const f32x4*>(&l.sc[16 * w + 4 * g]);
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    R[ct][r] = ValueBits<NCT>::at(v[r], ct) - sc[0][r] * (Ph[ct][r] + Pl[ct][r]);
+            for (int ct = 0; ct < NCT; ++ct) {
+                // the lane's column of rows 16 w + 4 g + r
+                const uint2 v = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * (4 * NCT) +
+                                        4 * ct + (col & 3));
+                const f32x4 vv = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+                R[ct] = vv - cp * (Ph[ct] + Pl[ct]);
+            }
             if (n < kC)
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
@@ -856,45 +828,39 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = hi;
                 reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = lo;
             }
-            load_v(n - kC);
             lds_barrier();
 
             // U = beta R + T R below the diagonal
             f32x4 u0[NCT], u1[NCT];
-            auto solve = [&](auto steps) {
+            const f32x4 be = *reinterpret_cast<const f32x4*>(&l.sc[kC + 16 * w + 4 * g]);
+            const f32x4 cu = *reinterpret_cast<const f32x4*>(&l.sc[2 * kC + 16 * w + 4 * g]);
+            const float gam = l.sc[4 * kC];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    bf16x8 rh[2], rl[2];
+            for (int ct = 0; ct < NCT; ++ct) {
+                bf16x8 rh[kSteps], rl[kSteps];
 #pragma unroll
-                    for (int s = 0; s < steps.value; ++s) {
-                        rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][ct][lane]);
-                        rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][ct][lane]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) u0[ct][r] = sc[1][r] * R[ct][r];
-                    u1[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int s = 0; s < steps.value; ++s) {
-                        const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
-                        u1[ct] = mfma(tl, rh[s], u1[ct]);
-                        u0[ct] = mfma(th, rh[s], u0[ct]);
-                        u1[ct] = mfma(th, rl[s], u1[ct]);
-                    }
+                for (int s = 0; s < kSteps; ++s) {
+                    rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][ct][lane]);
+                    rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][ct][lane]);
                 }
-            };
+                u0[ct] = be * R[ct];
+                u1[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
+                    u1[ct] = mfma(tl, rh[s], u1[ct]);
+                    u0[ct] = mfma(th, rh[s], u0[ct]);
+                    u1[ct] = mfma(th, rl[s], u1[ct]);
+                }
+            }
             const int4 marks = l.marks;
-            if (w < 2)
-                solve(std::integral_constant<int, 1>());
-            else
-                solve(std::integral_constant<int, 2>());
             kr.put(l.K[w], lane);
             load_k(n - 2 * kC);
             f32x4 e[NCT];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 u0[ct] += u1[ct];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) e[ct][r] = u0[ct][r] * sc[2][r];
+                e[ct] = u0[ct] * cu;
             }
             if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0)) {
                 int first[NCT];
@@ -935,9 +901,15 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         for (int i = 0; i < TPW; ++i)
                             S[i][ct] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i][ct]);
             }
-            gp += d.H_v;
-            gam = *gp;
+            put_v();
+            load_v(n - 2 * kC);
         }
+    };
+    if (chunks > 0) {
+        if (w < 2)
+            run(std::integral_constant<int, 1>());
+        else
+            run(std::integral_constant<int, 2>());
     }
     if (keep)
 #pragma unroll
@@ -945,7 +917,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 const int tau = w * TPW + i;
-                *reinterpret_cast<f32x4*>(Sp + ct * DK + 32 * (tau >> 1) + 4 * (tau & 1)) = S[i][ct];
+                *reinterpret_cast<f32x4*>(Sp + ct * 16 * DK + 32 * (tau >> 1) + 4 * (tau & 1)) = S[i][ct];
             }
 }
 
@@ -976,7 +948,6 @@ hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream) {
                 reinterpret_cast<uint4*>(p + l.t),
                 reinterpret_cast<uint4*>(p + l.m),
                 reinterpret_cast<float*>(p + l.sc),
-                reinterpret_cast<float*>(p + l.gam),
                 a.d.T / kC + a.d.B};
     return a.d.d_k == 128 ? launch_chunks<128>(c, stream) : launch_chunks<64>(c, stream);
 }
