@@ -10,34 +10,56 @@
 
 #include "gdn_layer_internal.h"
 #include "gdn_layer_util.h"
+#include "gdn_mfma.h"
 
 namespace gdn {
 namespace {
 
+// Four adjacent elements as loaded.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* x) {
-    if constexpr (sizeof(T) == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    } else {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+struct Four;
+template <>
+struct Four<uint16_t> {
+    uint2 u;
+    __device__ __forceinline__ float at(int i) const {
+        const uint32_t w = i < 2 ? u.x : u.y;
+        return i & 1 ? bf16_hi(w) : bf16_lo(w);
     }
-}
+};
+template <>
+struct Four<float> {
+    f32x4 u;
+    __device__ __forceinline__ float at(int i) const { return u[i]; }
+};
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-    if constexpr (sizeof(T) == 2)
-        return __builtin_bit_cast(float, static_cast<uint32_t>(x) << 16);
-    else
-        return x;
-}
+__device__ __forceinline__ float to_float(uint16_t x) { return bf16_lo(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
 
 // The lane's E = d_k / 8 elements of a row: pieces of 4, 32 apart.
 template <int E, typename T>
-__device__ __forceinline__ void load_row(const T* row, int l8, float (&x)[E]) {
+__device__ __forceinline__ void load_pieces(const T* row, int l8, Four<T> (&x)[E / 4]) {
 #pragma unroll
-    for (int j = 0; j < E / 4; ++j) load4(row + 32 * j + 4 * l8, x + 4 * j);
+    for (int j = 0; j < E / 4; ++j) x[j] = *reinterpret_cast<const Four<T>*>(row + 32 * j + 4 * l8);
+}
+
+template <int E, typename T>
+__device__ __forceinline__ void unpack(const Four<T> (&x)[E / 4], float (&y)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = x[j / 4].at(j % 4);
+}
+
+template <int E, typename T>
+__device__ __forceinline__ void load_row(const T* row, int l8, float (&y)[E]) {
+    Four<T> x[E / 4];
+    load_pieces<E>(row, l8, x);
+    unpack<E>(x, y);
+}
+
+template <int E>
+__device__ __forceinline__ void store_row(float* row, int l8, const float (&x)[E]) {
+#pragma unroll
+    for (int j = 0; j < E / 4; ++j)
+        *reinterpret_cast<f32x4*>(row + 32 * j + 4 * l8) = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
 }
 
 template <int E>
@@ -76,45 +98,45 @@ __device__ __forceinline__ float scale_qk(const gdn_seq_dims& d, float (&q)[E], 
     return lane_sum<8>(dot(k, q));
 }
 
-// Grid (d_v / (32 R), H_v, B): a wavefront takes R groups of 8 state rows.
-template <typename T, int DK, int R>
+// Grid (d_v / 32, H_v, B): a wavefront takes 8 state rows.
+template <typename T, int DK>
 __global__ void __launch_bounds__(256) decode_kernel(SeqArgs a) {
     constexpr int E = DK / 8;
     const gdn_seq_dims& d = a.d;
     const int b = blockIdx.z, h = blockIdx.y, hk = h / (d.H_v / d.H_k);
     const int lane = threadIdx.x & 63, l8 = lane & 7;
-    const int row0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 * R + (lane >> 3);
+    const int row = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 + (lane >> 3);
     const int slot = a.slot ? a.slot[b] : b;
     const int64_t bh = int64_t(b) * d.H_v + h;
     if (slot < 0 || slot >= d.n_slots) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (l8 == 0) store1(a.o, d.o_dtype, bh * d.d_v + row0 + 8 * r, 0.0f);
+        if (l8 == 0) store1(a.o, d.o_dtype, bh * d.d_v + row, 0.0f);
         return;
     }
-    float* S = a.S + ((int64_t(slot) * d.H_v + h) * d.d_v + row0) * DK;
-    float s[R][E];
-#pragma unroll
-    for (int r = 0; r < R; ++r) load_row<E>(S + int64_t(8 * r) * DK, l8, s[r]);
-    float q[E], k[E];
+    float* S = a.S + ((int64_t(slot) * d.H_v + h) * d.d_v + row) * DK;
+    float s[E], q[E], k[E];
+    load_row<E>(S, l8, s);
     load_row<E>(static_cast<const T*>(a.q) + b * d.q_stride + int64_t(hk) * DK, l8, q);
     load_row<E>(static_cast<const T*>(a.k) + b * d.k_stride + int64_t(hk) * DK, l8, k);
+    const float v = to_float(static_cast<const T*>(a.v)[b * d.v_stride + int64_t(h) * d.d_v + row]);
     const float kq = scale_qk<E>(d, q, k);
-    const T* v = static_cast<const T*>(a.v) + b * d.v_stride + int64_t(h) * d.d_v + row0;
-    const float alpha = expf(a.g[bh]), beta = a.beta[bh];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float o = delta_step<E>(s[r], k, q, alpha, beta, to_float(v[8 * r]), kq);
-#pragma unroll
-        for (int j = 0; j < E / 4; ++j)
-            *reinterpret_cast<float4*>(S + int64_t(8 * r) * DK + 32 * j + 4 * l8) =
-                make_float4(s[r][4 * j], s[r][4 * j + 1], s[r][4 * j + 2], s[r][4 * j + 3]);
-        if (l8 == 0) store1(a.o, d.o_dtype, bh * d.d_v + row0 + 8 * r, o);
-    }
+    const float o = delta_step<E>(s, k, q, expf(a.g[bh]), a.beta[bh], v, kq);
+    store_row<E>(S, l8, s);
+    if (l8 == 0) store1(a.o, d.o_dtype, bh * d.d_v + row, o);
 }
 
+// One token as loaded.
+template <typename T, int E>
+struct Token {
+    Four<T> q[E / 4], k[E / 4];
+    T v;
+    float g, beta;
+};
+
 // Grid (d_v / 32, H_v, B): the tokens of sequence b in order, 8 state rows
-// per wavefront; the next token's rows are loaded while this one is applied.
+// per wavefront.  A token takes less time than its loads, so the next kAhead
+// are in flight; past the end the last token is loaded again, since a load
+// behind a branch would be waited for at the branch's end.
+constexpr int kAhead = 4;
 template <typename T, int DK>
 __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
     constexpr int E = DK / 8;
@@ -140,50 +162,55 @@ __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
     const T* q = static_cast<const T*>(a.q) + int64_t(hk) * DK;
     const T* k = static_cast<const T*>(a.k) + int64_t(hk) * DK;
     const T* v = static_cast<const T*>(a.v) + int64_t(h) * d.d_v + row;
-    float qn[E], kn[E], vn = 0.0f, gn = 0.0f, bn = 0.0f;  // as loaded
-    auto load = [&](int64_t n) {
-        load_row<E>(q + n * d.q_stride, l8, qn);
-        load_row<E>(k + n * d.k_stride, l8, kn);
-        vn = to_float(v[n * d.v_stride]);
-        gn = a.g[n * d.H_v + h];
-        bn = a.beta[n * d.H_v + h];
-    };
-    if (t < end) load(t);
-    for (; t < end; ++t) {
-        float qc[E], kc[E];
+    if (t < end) {
+        Token<T, E> tok[kAhead];
+        auto load = [&](Token<T, E>& x, int64_t n) {
+            n = n < end ? n : end - 1;
+            load_pieces<E>(q + n * d.q_stride, l8, x.q);
+            load_pieces<E>(k + n * d.k_stride, l8, x.k);
+            x.v = v[n * d.v_stride];
+            x.g = a.g[n * d.H_v + h];
+            x.beta = a.beta[n * d.H_v + h];
+        };
+        auto apply = [&](const Token<T, E>& x) {
+            float qc[E], kc[E];
+            unpack<E>(x.q, qc);
+            unpack<E>(x.k, kc);
+            const float kq = scale_qk<E>(d, qc, kc);
+            return delta_step<E>(s, kc, qc, expf(x.g), x.beta, to_float(x.v), kq);
+        };
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            qc[j] = qn[j];
-            kc[j] = kn[j];
+        for (int i = 0; i < kAhead; ++i) load(tok[i], t + i);
+        // lane i of 8 stores token t + i
+        for (; t + kAhead <= end; t += kAhead) {
+            float o = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float x = apply(tok[i]);
+                o = l8 == i ? x : o;
+                load(tok[i], t + kAhead + i);
+            }
+            if (l8 < kAhead) store1(a.o, d.o_dtype, ((t + l8) * d.H_v + h) * d.d_v + row, o);
         }
-        const float vc = vn, gc = gn, bc = bn;
-        if (t + 1 < end) load(t + 1);
-        const float kq = scale_qk<E>(d, qc, kc);
-        const float o = delta_step<E>(s, kc, qc, expf(gc), bc, vc, kq);
-        if (l8 == 0) store1(a.o, d.o_dtype, (t * d.H_v + h) * d.d_v + row, o);
-    }
-    if (keep) {
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j)
-            *reinterpret_cast<float4*>(S + 32 * j + 4 * l8) =
-                make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+        for (int i = 0; i < kAhead - 1; ++i)
+            if (t + i < end) {
+                const float o = apply(tok[i]);
+                if (l8 == 0) store1(a.o, d.o_dtype, ((t + i) * d.H_v + h) * d.d_v + row, o);
+            }
     }
-}
-
-template <typename T, int DK>
-void decode_t(const SeqArgs& a, hipStream_t stream) {
-    const gdn_seq_dims& d = a.d;
-    decode_kernel<T, DK, 1><<<dim3(d.d_v / 32, d.H_v, d.B), 256, 0, stream>>>(a);
+    if (keep) store_row<E>(S, l8, s);
 }
 
 }  // namespace
 
 hipError_t launch_decode(const SeqArgs& a, hipStream_t stream) {
     const bool bf = a.d.qkv_dtype == GDN_BF16;
+    const dim3 grid(a.d.d_v / 32, a.d.H_v, a.d.B);
     if (a.d.d_k == 128)
-        bf ? decode_t<uint16_t, 128>(a, stream) : decode_t<float, 128>(a, stream);
+        bf ? decode_kernel<uint16_t, 128><<<grid, 256, 0, stream>>>(a) : decode_kernel<float, 128><<<grid, 256, 0, stream>>>(a);
     else
-        bf ? decode_t<uint16_t, 64>(a, stream) : decode_t<float, 64>(a, stream);
+        bf ? decode_kernel<uint16_t, 64><<<grid, 256, 0, stream>>>(a) : decode_kernel<float, 64><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -41,6 +41,14 @@ gdn_status check_ptr(const void* p, const char* name, bool required = true) {
     return GDN_OK;
 }
 
+// Rows that kernels read in pieces of any alignment.
+gdn_status check_rows(const void* p, int32_t dtype, const char* name, bool required = true) {
+    if (!p) return required ? fail(GDN_ERR_NULL, "%s is NULL", name) : GDN_OK;
+    if (reinterpret_cast<uintptr_t>(p) % (dtype == GDN_BF16 ? 2 : 4) != 0)
+        return fail(GDN_ERR_ALIGN, "%s is not aligned to its elements", name);
+    return GDN_OK;
+}
+
 gdn_status check_dtype(int32_t t, const char* name) {
     if (t != GDN_BF16 && t != GDN_F32) return fail(GDN_ERR_DTYPE, "%s must be GDN_BF16 or GDN_F32", name);
     return GDN_OK;
@@ -168,13 +176,13 @@ gdn_status gdn_add_norm(const gdn_add_norm_dims* dims, const void* x, const void
     if (h) GDN_TRY(check_out_stride(d.h_stride, d.D, d.T, "h_stride"));
     GDN_TRY(check_out_stride(d.y_stride, d.D, d.T, "y_stride"));
     if (d.T == 0) return fail(GDN_OK, "");
-    GDN_TRY(check_ptr(x, "x"));
-    GDN_TRY(check_ptr(residual, "residual", false));
+    GDN_TRY(check_rows(x, d.x_dtype, "x"));
+    GDN_TRY(check_rows(residual, d.res_dtype, "residual", false));
     GDN_TRY(check_ptr(weight, "weight"));
     GDN_TRY(check_ptr(post_weight, "post_weight", false));
     GDN_TRY(check_ptr(chan_scale, "chan_scale", false));
-    GDN_TRY(check_ptr(h, "h", false));
-    GDN_TRY(check_ptr(y, "y"));
+    GDN_TRY(check_rows(h, d.res_dtype, "h", false));
+    GDN_TRY(check_rows(y, d.y_dtype, "y"));
     if (h && h == residual && d.h_stride != d.res_stride && d.T > 1)
         return fail(GDN_ERR_SHAPE, "h in place of residual needs the same stride");
     return done(gdn::launch_add_norm({d, x, residual, weight, post_weight, chan_scale, h, y}, stream), "add_norm");
@@ -196,10 +204,10 @@ gdn_status gdn_gated_norm(const gdn_gated_norm_dims* dims, const void* o, const 
     GDN_TRY(check_in_stride(d.z_stride, "z_stride"));
     GDN_TRY(check_out_stride(d.y_stride, int64_t(d.H) * d.d, d.T, "y_stride"));
     if (d.T == 0) return fail(GDN_OK, "");
-    GDN_TRY(check_ptr(o, "o"));
-    GDN_TRY(check_ptr(z, "z"));
+    GDN_TRY(check_rows(o, d.o_dtype, "o"));
+    GDN_TRY(check_rows(z, d.z_dtype, "z"));
     GDN_TRY(check_ptr(weight, "weight"));
-    GDN_TRY(check_ptr(y, "y"));
+    GDN_TRY(check_rows(y, d.y_dtype, "y"));
     if ((y == o && (d.y_dtype != d.o_dtype || (d.y_stride != d.o_stride && d.T > 1))) ||
         (y == z && (d.y_dtype != d.z_dtype || (d.y_stride != d.z_stride && d.T > 1))))
         return fail(GDN_ERR_SHAPE, "y in place needs the same dtype and stride");

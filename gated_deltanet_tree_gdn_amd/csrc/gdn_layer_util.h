@@ -39,28 +39,39 @@ __device__ __forceinline__ void store1(void* p, int dtype, int64_t i, float x) {
         static_cast<float*>(p)[i] = x;
 }
 
-// Elements i .. i + 7 (i a multiple of 8 elements from a 16-byte boundary).
+// Elements i .. i + 7, with the alignment of an element: 16-byte accesses may
+// start anywhere.
 __device__ __forceinline__ void load8(const void* p, int dtype, int64_t i, float (&x)[8]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
     if (dtype == GDN_BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16_lo(u[j]);
+            x[2 * j + 1] = bf16_hi(u[j]);
+        }
     } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        const f32x4* f = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+        const f32x4 a = f[0], b = f[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = a[j];
+            x[4 + j] = b[j];
+        }
     }
 }
 
 __device__ __forceinline__ void store8(void* p, int dtype, int64_t i, const float (&x)[8]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
     if (dtype == GDN_BF16) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
+            u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+        f32x4* f = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+        f[0] = f32x4{x[0], x[1], x[2], x[3]};
+        f[1] = f32x4{x[4], x[5], x[6], x[7]};
     }
 }
 

@@ -26,20 +26,43 @@ __device__ __forceinline__ float block_sum(float x, float* part, int turn) {
     return s;
 }
 
-// One row per workgroup, VPT vectors of 8 elements per thread in registers.
-template <int VPT>
-__global__ void add_norm_row_kernel(AddNormArgs a) {
+// The piece of 8 elements at i of a row that has n elements from there on;
+// those beyond read as zero and are not written.  Without TAIL n is 8 or more.
+template <bool TAIL>
+__device__ __forceinline__ void load_piece(const void* p, int dtype, int64_t i, int n, float (&x)[8]) {
+    if (!TAIL || n >= 8) {
+        load8(p, dtype, i, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = e < n ? load1(p, dtype, i + e) : 0.0f;
+    }
+}
+template <bool TAIL>
+__device__ __forceinline__ void store_piece(void* p, int dtype, int64_t i, int n, const float (&x)[8]) {
+    if (!TAIL || n >= 8) {
+        store8(p, dtype, i, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) store1(p, dtype, i + e, x[e]);
+    }
+}
+
+// One row per workgroup, VPT pieces of 8 elements per thread in registers.
+// TAIL: D is not a multiple of 8.
+template <int VPT, bool TAIL>
+__global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
     __shared__ float part[32];
     const gdn_add_norm_dims& d = a.d;
-    const int nvec = d.D >> 3;
+    const int nvec = (d.D + 7) >> 3;
     const int64_t t = blockIdx.x;
     float x[VPT][8], r[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
         if (j < nvec) {
-            load8(a.x, d.x_dtype, t * d.x_stride + 8 * j, x[i]);
-            if (a.res) load8(a.res, d.res_dtype, t * d.res_stride + 8 * j, r[i]);
+            load_piece<TAIL>(a.x, d.x_dtype, t * d.x_stride + 8 * j, d.D - 8 * j, x[i]);
+            if (a.res) load_piece<TAIL>(a.res, d.res_dtype, t * d.res_stride + 8 * j, d.D - 8 * j, r[i]);
         }
     }
     if (a.post) {
@@ -55,7 +78,7 @@ __global__ void add_norm_row_kernel(AddNormArgs a) {
             const int j = threadIdx.x + i * blockDim.x;
             if (j < nvec) {
                 float p[8];
-                load8(a.post, GDN_F32, 8 * j, p);
+                load_piece<TAIL>(a.post, GDN_F32, 8 * j, d.D - 8 * j, p);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * inv * (p[e] + d.weight_offset);
             }
@@ -67,14 +90,14 @@ __global__ void add_norm_row_kernel(AddNormArgs a) {
         const int j = threadIdx.x + i * blockDim.x;
         if (j < nvec) {
             float c[8];
-            if (a.chan) load8(a.chan, GDN_F32, 8 * j, c);
+            if (a.chan) load_piece<TAIL>(a.chan, GDN_F32, 8 * j, d.D - 8 * j, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float p = a.chan ? c[e] * x[i][e] : x[i][e];
                 x[i][e] = a.res ? r[i][e] + d.scale * p : d.scale * p;
                 s += x[i][e] * x[i][e];
             }
-            if (a.h) store8(a.h, d.res_dtype, t * d.h_stride + 8 * j, x[i]);
+            if (a.h) store_piece<TAIL>(a.h, d.res_dtype, t * d.h_stride + 8 * j, d.D - 8 * j, x[i]);
         }
     }
     const float inv = inv_rms(block_sum(s, part, 1), d.D, d.eps);
@@ -83,60 +106,29 @@ __global__ void add_norm_row_kernel(AddNormArgs a) {
         const int j = threadIdx.x + i * blockDim.x;
         if (j < nvec) {
             float w[8];
-            load8(a.w, GDN_F32, 8 * j, w);
+            load_piece<TAIL>(a.w, GDN_F32, 8 * j, d.D - 8 * j, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * inv * (w[e] + d.weight_offset);
-            store8(a.y, d.y_dtype, t * d.y_stride + 8 * j, x[i]);
+            store_piece<TAIL>(a.y, d.y_dtype, t * d.y_stride + 8 * j, d.D - 8 * j, x[i]);
         }
     }
 }
 
-// Rows of any length and alignment: one row per workgroup, element by
-// element, the row kept in LDS as fp32.
-__global__ void add_norm_any_kernel(AddNormArgs a) {
-    extern __shared__ float row[];
-    __shared__ float part[32];
-    const gdn_add_norm_dims& d = a.d;
-    const int64_t t = blockIdx.x;
-    float inv = 1.0f;
-    if (a.post) {
-        float s = 0.0f;
-        for (int j = threadIdx.x; j < d.D; j += blockDim.x) {
-            const float x = load1(a.x, d.x_dtype, t * d.x_stride + j);
-            row[j] = x;
-            s += x * x;
-        }
-        inv = inv_rms(block_sum(s, part, 0), d.D, d.eps);
-    }
-    float s = 0.0f;
-    for (int j = threadIdx.x; j < d.D; j += blockDim.x) {
-        float p = a.post ? row[j] * inv * (a.post[j] + d.weight_offset) : load1(a.x, d.x_dtype, t * d.x_stride + j);
-        if (a.chan) p *= a.chan[j];
-        const float h = a.res ? load1(a.res, d.res_dtype, t * d.res_stride + j) + d.scale * p : d.scale * p;
-        if (a.h) store1(a.h, d.res_dtype, t * d.h_stride + j, h);
-        row[j] = h;  // read back by this thread only
-        s += h * h;
-    }
-    inv = inv_rms(block_sum(s, part, 1), d.D, d.eps);
-    for (int j = threadIdx.x; j < d.D; j += blockDim.x)
-        store1(a.y, d.y_dtype, t * d.y_stride + j, row[j] * inv * (a.w[j] + d.weight_offset));
-}
-
-// W lanes of 8 elements per head.
-template <int W>
+// W lanes of 8 elements per head.  TAIL: d is not a multiple of 8.
+template <int W, bool TAIL>
 __global__ void __launch_bounds__(256) gated_norm_vec_kernel(GatedNormArgs a) {
     const gdn_gated_norm_dims& d = a.d;
     const int64_t n = int64_t(d.T) * d.H, step = int64_t(gridDim.x) * (256 / W);
     const int e0 = 8 * (threadIdx.x % W);
     const bool in = e0 < d.d;
     float w[8];
-    if (in) load8(a.w, GDN_F32, e0, w);
+    if (in) load_piece<TAIL>(a.w, GDN_F32, e0, d.d - e0, w);
     for (int64_t i = int64_t(blockIdx.x) * (256 / W) + threadIdx.x / W; i < n; i += step) {
         const int64_t t = i / d.H, c = (i - t * d.H) * d.d + e0;
         float o[8], z[8], s = 0.0f;
         if (in) {
-            load8(a.o, d.o_dtype, t * d.o_stride + c, o);
-            load8(a.z, d.z_dtype, t * d.z_stride + c, z);
+            load_piece<TAIL>(a.o, d.o_dtype, t * d.o_stride + c, d.d - e0, o);
+            load_piece<TAIL>(a.z, d.z_dtype, t * d.z_stride + c, d.d - e0, z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += o[e] * o[e];
         }
@@ -144,12 +136,12 @@ __global__ void __launch_bounds__(256) gated_norm_vec_kernel(GatedNormArgs a) {
         if (in) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = o[e] * inv * w[e] * activate(d.gate, z[e]);
-            store8(a.y, d.y_dtype, t * d.y_stride + c, o);
+            store_piece<TAIL>(a.y, d.y_dtype, t * d.y_stride + c, d.d - e0, o);
         }
     }
 }
 
-// Heads of any width and alignment: one wavefront per head.
+// Heads wider than 512: one wavefront per head.
 __global__ void __launch_bounds__(256) gated_norm_any_kernel(GatedNormArgs a) {
     const gdn_gated_norm_dims& d = a.d;
     const int64_t n = int64_t(d.T) * d.H, step = int64_t(gridDim.x) * 4;
@@ -170,48 +162,44 @@ __global__ void __launch_bounds__(256) gated_norm_any_kernel(GatedNormArgs a) {
     }
 }
 
-// Rows of 16-byte pieces: the base is aligned, so the stride decides.
-bool vec_rows(int64_t stride, int64_t rows, int dtype) { return rows <= 1 || stride * dtype_size(dtype) % 16 == 0; }
-
 }  // namespace
 
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream) {
     const gdn_add_norm_dims& d = a.d;
-    const bool vec = d.D % 8 == 0 && vec_rows(d.x_stride, d.T, d.x_dtype) && vec_rows(d.y_stride, d.T, d.y_dtype) &&
-                     (!a.res || vec_rows(d.res_stride, d.T, d.res_dtype)) &&
-                     (!a.h || vec_rows(d.h_stride, d.T, d.res_dtype));
-    if (!vec) {
-        add_norm_any_kernel<<<d.T, 256, d.D * sizeof(float), stream>>>(a);
-        return hipGetLastError();
-    }
-    const int nvec = d.D / 8;
+    const int nvec = (d.D + 7) / 8;
     auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 63) / 64 * 64; };
+    const bool tail = d.D % 8 != 0;
     if (threads(1) <= 512)
-        add_norm_row_kernel<1><<<d.T, threads(1), 0, stream>>>(a);
+        tail ? add_norm_kernel<1, true><<<d.T, threads(1), 0, stream>>>(a)
+             : add_norm_kernel<1, false><<<d.T, threads(1), 0, stream>>>(a);
     else
-        add_norm_row_kernel<2><<<d.T, threads(2), 0, stream>>>(a);
+        tail ? add_norm_kernel<2, true><<<d.T, threads(2), 0, stream>>>(a)
+             : add_norm_kernel<2, false><<<d.T, threads(2), 0, stream>>>(a);
     return hipGetLastError();
 }
 
-hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t stream) {
-    const gdn_gated_norm_dims& d = a.d;
-    const int64_t n = int64_t(d.T) * d.H;
-    const bool vec = d.d % 8 == 0 && d.d <= 512 && vec_rows(d.o_stride, d.T, d.o_dtype) &&
-                     vec_rows(d.z_stride, d.T, d.z_dtype) && vec_rows(d.y_stride, d.T, d.y_dtype);
-    auto grid = [&](int per) {
-        const int64_t g = (n + per - 1) / per;
-        return dim3(static_cast<unsigned>(g < (1 << 20) ? g : (1 << 20)));
-    };
-    if (!vec)
-        gated_norm_any_kernel<<<grid(4), 256, 0, stream>>>(a);
-    else if (d.d <= 64)
-        gated_norm_vec_kernel<8><<<grid(32), 256, 0, stream>>>(a);
-    else if (d.d <= 128)
-        gated_norm_vec_kernel<16><<<grid(16), 256, 0, stream>>>(a);
-    else if (d.d <= 256)
-        gated_norm_vec_kernel<32><<<grid(8), 256, 0, stream>>>(a);
+template <int W>
+static void launch_gated(const GatedNormArgs& a, int64_t groups, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : (1 << 20)));
+    if (a.d.d % 8)
+        gated_norm_vec_kernel<W, true><<<grid, 256, 0, stream>>>(a);
     else
-        gated_norm_vec_kernel<64><<<grid(4), 256, 0, stream>>>(a);
+        gated_norm_vec_kernel<W, false><<<grid, 256, 0, stream>>>(a);
+}
+
+hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t stream) {
+    const int64_t n = int64_t(a.d.T) * a.d.H;
+    const int w = a.d.d;
+    if (w <= 64)
+        launch_gated<8>(a, (n + 31) / 32, stream);
+    else if (w <= 128)
+        launch_gated<16>(a, (n + 15) / 16, stream);
+    else if (w <= 256)
+        launch_gated<32>(a, (n + 7) / 8, stream);
+    else if (w <= 512)
+        launch_gated<64>(a, (n + 3) / 4, stream);
+    else
+        gated_norm_any_kernel<<<static_cast<unsigned>((n + 3) / 4 < (1 << 20) ? (n + 3) / 4 : (1 << 20)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
