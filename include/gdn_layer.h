@@ -14,7 +14,8 @@
  * Conventions of gdn_tree.h hold (device pointers, caller-owned buffers, no
  * allocation, no synchronisation, host argument checks before any HIP call,
  * status codes, gdn_last_error, stream order).  In addition:
- *  - Base pointers are 16-byte aligned; workspaces 256-byte aligned.
+ *  - Base pointers are 16-byte aligned (rows of the norms: aligned to their
+ *    elements); workspaces 256-byte aligned.
  *  - A "stride" is the distance in ELEMENTS between two consecutive rows
  *    (tokens); what one row holds is dense.  An input's stride may be any
  *    value >= 0 (0: every row is the same); an output's is at least the row.

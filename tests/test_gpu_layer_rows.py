@@ -1,0 +1,94 @@
+"""More of the operators around the tree verify on the GPU: norms over rows
+that are aligned to their elements only, and the walk and the chunks of
+gdn_prefill on either side of the sizes that choose between them.
+
+Tolerances as for the other tests of these operators (a row's arithmetic does
+not depend on its alignment).
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+gdn = pytest.importorskip("gated_deltanet_tree_gdn_amd")
+
+from test_gpu_layer import BF16, CHUNK_TOL, F32, FP32_TOL, check, gpu, make, rel, rms, run_prefill, say  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+def at_offset(x, off):
+    """A copy of x [T][n] as a slice that starts `off` elements into wider rows of odd length."""
+    wide = torch.full((x.shape[0], (x.shape[1] + off) | 1), 7.0, dtype=x.dtype, device=x.device)
+    view = wide[:, off:off + x.shape[1]]
+    view.copy_(x)
+    return view, wide
+
+
+@pytest.mark.parametrize("D", [1, 5, 8, 64, 101, 1001, 4096, 4097, 5119, 8199, 16383])
+@pytest.mark.parametrize("off", [1, 3, 4, 7])
+def test_add_norm_of_unaligned_rows(D, off):
+    gen = torch.Generator().manual_seed(D + off)
+    randn = lambda *n: torch.randn(*n, generator=gen).cuda()  # noqa: E731
+    w, p, c = randn(D), randn(D), randn(D)
+    for x_dt, r_dt, y_dt, post, chan in ((BF16, F32, BF16, p, c), (BF16, BF16, F32, None, None), (F32, BF16, BF16, p, None)):
+        x, _ = at_offset(randn(5, D).to(x_dt), off)
+        r, _ = at_offset((3 * randn(5, D)).to(r_dt), off)
+        h, h_wide = at_offset(torch.zeros(5, D, dtype=r_dt, device="cuda"), off)
+        y, y_wide = at_offset(torch.zeros(5, D, dtype=y_dt, device="cuda"), off)
+        X, R, W, P, C = (a.cpu().double() for a in (x, r, w, p, c))
+        gdn.gdn_add_norm(x, r, w, scale=0.7, chan_scale=chan, post_weight=post, h=h, y=y)
+        z = rms(X) * P if post is not None else X
+        want = R + 0.7 * (z * C if chan is not None else z)
+        check(h, want, FP32_TOL, f"h, D {D} at {off}")
+        check(y, rms(want) * W, FP32_TOL, "y")
+        for wide in (h_wide, y_wide):  # nothing beside the rows is written
+            assert (wide[:, :off] == 7.0).all() and (wide[:, off + D:] == 7.0).all()
+        gdn.gdn_add_norm(x, r, w, scale=0.7, chan_scale=chan, post_weight=post, h=r, y=y)
+        assert torch.equal(r, h)  # in place of the residual
+
+
+@pytest.mark.parametrize("d", [1, 5, 8, 33, 64, 80, 127, 128, 200, 511, 513])
+@pytest.mark.parametrize("off", [1, 3, 7])
+@pytest.mark.parametrize("H", [1, 7])
+def test_gated_norm_of_unaligned_rows(H, d, off):
+    gen = torch.Generator().manual_seed(H + d + off)
+    randn = lambda *n: torch.randn(*n, generator=gen).cuda()  # noqa: E731
+    w = randn(d)
+    for o_dt, z_dt, y_dt in ((F32, BF16, BF16), (BF16, BF16, F32), (BF16, F32, BF16)):
+        o, _ = at_offset(randn(9, H * d).to(o_dt), off)
+        z, _ = at_offset(randn(9, H * d).to(z_dt), off)
+        y, wide = at_offset(torch.zeros(9, H * d, dtype=y_dt, device="cuda"), off)
+        gdn.gdn_gated_norm(*(x.unflatten(1, (H, d)) for x in (o, z)), w, y=y.unflatten(1, (H, d)))
+        O, Z = (x.cpu().double().unflatten(1, (H, d)) for x in (o, z))
+        check(y, (rms(O) * w.cpu().double() * torch.nn.functional.silu(Z)).flatten(1), FP32_TOL, f"H {H} d {d} at {off}")
+        assert (wide[:, :off] == 7.0).all() and (wide[:, off + H * d:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
+def test_walk_and_chunks_agree(dk, dv):
+    """8 tokens per sequence on average are walked, one token more makes chunks of them."""
+    lengths = [1, 0, 29, 2, 8, 8]
+    extra = lengths + [1]
+    n = sum(lengths)
+    assert n == 8 * len(lengths) and n + 17 > 8 * len(extra)
+    d = make(n + 17, 2, 4, dk, dv, slots=7, seed=3)
+    o1, S1 = run_prefill({a: x if a == "S" else x[:n].contiguous() for a, x in d.items()}, lengths)
+    o2, S2 = run_prefill(d, lengths + [17])
+    assert rel(o1, o2[:n]) <= CHUNK_TOL and rel(S1[:6], S2[:6]) <= CHUNK_TOL
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B", [1, 2, 8, 9])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_walk_of_few_and_many_rows(B, dk, dv, dtype):
+    """Both splits of a state row over lanes, sequences around the four tokens that are loaded ahead."""
+    lengths = [[3, 4, 5, 0, 8, 7, 1, 2, 9][b] for b in range(B)]
+    d = make(sum(lengths), 8, 32, dk, dv, dtype=dtype, slots=B, seed=B)
+    run_prefill(d, lengths, has=[b % 2 for b in range(B)], qk_l2norm=True, q_scale=0.125, o_dtype=F32)
+
+
+def test_chunks_of_short_sequences():
+    """Sequences of a few tokens beside one long enough for all of them to be cut into chunks."""
+    lengths = [1, 2, 3, 16, 17, 63, 0, 64, 65, 200]
+    say(f"[prefill] {lengths}")
+    d = make(sum(lengths), slots=10, seed=1)
+    run_prefill(d, lengths, has=[1, 0] * 5, o_dtype=F32)
