@@ -20,18 +20,18 @@ namespace {
 
 constexpr int kBK = 64;  // elements of K per step of the tile kernel
 
-
-// Outputs n .. n + E - 1 of row m: bias, activation, scale and residual in
-// fp32, rounded once.  VEC (E = 8): all of them exist and rows of y and
-// residual are 16-byte aligned.
-template <int E, bool VEC>
+// Outputs n .. n + E - 1 of row m, those below N: bias, activation, scale and
+// residual in fp32, rounded once.
+template <int E>
 __device__ __forceinline__ void put(const LinearArgs& a, int64_t m, int n, float (&v)[E]) {
-    static_assert(!VEC || E == 8, "");
     const gdn_linear_dims& d = a.d;
+    const bool whole = E == 8 && n + 8 <= d.N;
     float b[E] = {}, r[E] = {};
-    if constexpr (VEC) {
-        if (a.bias) load8(a.bias, GDN_F32, n, b);
-        if (a.res) load8(a.res, d.res_dtype, m * d.res_stride + n, r);
+    if (whole) {
+        if constexpr (E == 8) {
+            if (a.bias) load8(a.bias, GDN_F32, n, b);
+            if (a.res) load8(a.res, d.res_dtype, m * d.res_stride + n, r);
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -52,8 +52,8 @@ __device__ __forceinline__ void put(const LinearArgs& a, int64_t m, int n, float
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = a.res ? r[e] + d.scale * v[e] : d.scale * v[e];
-    if constexpr (VEC) {
-        store8(a.y, d.y_dtype, m * d.y_stride + n, v);
+    if (whole) {
+        if constexpr (E == 8) store8(a.y, d.y_dtype, m * d.y_stride + n, v);
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -148,7 +148,7 @@ __device__ __forceinline__ void loads_barrier() {
 // LDS buffers, and add their sums at the end in a fixed order: with few tiles
 // that keeps KG times as many loads in flight on a CU.
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
-__global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a, int vec_out) {
+__global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kOutRows = TM > 4 ? 64 : TM * 16, kOutLd = TN * 16 + 4;  // epilogue: rows of a wavefront at a time
     constexpr int kGroupPieces = (BM + BN) * 8 * NB, kOutBytes = W * kOutRows * kOutLd * 4;
@@ -304,12 +304,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a, i
             const int64_t m = m0 + wm * TM * 16 + half * kOutRows + r, n = n0 + wn * TN * 16 + c;
             float v[8];
             load8(out, GDN_F32, r * kOutLd + c, v);
-            if (m < d.M && n < d.N) {
-                if (vec_out)
-                    put<8, true>(a, m, n, v);
-                else
-                    put<8, false>(a, m, n, v);
-            }
+            if (m < d.M && n < d.N) put<8>(a, m, n, v);
         }
     }
 }
@@ -354,7 +349,7 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(LinearArgs a) {
 #pragma unroll
         for (int w = 1; w < kThinWaves; ++w) acc += part[w][lane];
         float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-        put<4, false>(a, col, n0 + 4 * g, v);
+        put<4>(a, col, n0 + 4 * g, v);
     }
 }
 
@@ -367,9 +362,9 @@ void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
-void launch_tile(const LinearArgs& a, bool vec_out, hipStream_t stream) {
+void launch_tile(const LinearArgs& a, hipStream_t stream) {
     const int tiles = ((a.d.M + BM - 1) / BM) * ((a.d.N + BN - 1) / BN);
-    tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT><<<tiles, 64 * WM * WN * KG, 0, stream>>>(a, vec_out);
+    tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT><<<tiles, 64 * WM * WN * KG, 0, stream>>>(a);
 }
 
 // Rows of any alignment to rows of 16-byte pieces.
@@ -434,7 +429,6 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
     const bool aligned = p.copy || !(p.x || p.w);
     // direct loads: a tile's rows lie within 2^31 bytes of its first
     const bool direct = aligned && d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
-    const bool vec_out = d.N % 8 == 0 && (d.M <= 1 || (d.y_stride % 8 == 0 && (!a.res || d.res_stride % 8 == 0)));
     auto tiles = [&](int64_t t) { return double((d.M + t - 1) / t) * double((d.N + t - 1) / t); };
     // What each kernel takes at K = 4096 in us (measured over M = 64 .. 8192,
     // N = 4096 .. 12352); the ratios hold for other K.
@@ -448,17 +442,17 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
     if (d.M <= 16 && d.N <= 8192)
         launch_thin(a, aligned && d.K % 8 == 0, stream);
     else if (!direct)
-        launch_tile<64, 64, 2, 2, 4, 2, false>(a, vec_out, stream);
+        launch_tile<64, 64, 2, 2, 4, 2, false>(a, stream);
     else if (best == k64two)
-        launch_tile<64, 64, 2, 2, 2, 4, true>(a, vec_out, stream);
+        launch_tile<64, 64, 2, 2, 2, 4, true>(a, stream);
     else if (best == k64)
-        launch_tile<64, 64, 2, 2, 1, 4, true>(a, vec_out, stream);
+        launch_tile<64, 64, 2, 2, 1, 4, true>(a, stream);
     else if (best == k128two)
-        launch_tile<128, 128, 2, 2, 2, 2, true>(a, vec_out, stream);
+        launch_tile<128, 128, 2, 2, 2, 2, true>(a, stream);
     else if (best == k128)
-        launch_tile<128, 128, 2, 4, 1, 2, true>(a, vec_out, stream);
+        launch_tile<128, 128, 2, 4, 1, 2, true>(a, stream);
     else
-        launch_tile<256, 256, 2, 4, 1, 2, true>(a, vec_out, stream);
+        launch_tile<256, 256, 2, 4, 1, 2, true>(a, stream);
     return hipGetLastError();
 }
 
