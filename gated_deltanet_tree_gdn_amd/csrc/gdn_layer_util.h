@@ -106,12 +106,25 @@ __device__ __forceinline__ float activate(int act, float a) {
     }
 }
 
-// Orders LDS between the wavefronts of a workgroup without waiting for
-// global loads and stores in flight.
-__device__ __forceinline__ void lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+// Waits until at most N of the wavefront's loads and stores are outstanding
+// (any number: kAnyLoads) and, if READS, until its LDS accesses are done.  For
+// kernels with loads straight to LDS: a fence would wait for every one of them
+// (they count as LDS writes); what has to have arrived is exactly what the
+// count says.
+constexpr int kAnyLoads = 63;
+template <int N, bool READS = true>
+__device__ __forceinline__ void wait_count() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (READS ? 0 : 15) << 8 | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
+}
+
+// The same, then meets the workgroup.
+template <int N, bool READS = true>
+__device__ __forceinline__ void loads_barrier() {
+    wait_count<N, READS>();
     __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    asm volatile("" ::: "memory");
 }
 
 }  // namespace gdn

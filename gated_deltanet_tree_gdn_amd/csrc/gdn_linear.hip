@@ -131,18 +131,6 @@ __device__ __forceinline__ void stage_any(uint4* lds, const uint16_t* base, int6
     for (int i = 0; i < L; ++i) lds[(wave * L + i) * 64 + lane] = x[i];
 }
 
-// Waits until at most N of the wavefront's direct loads are outstanding (and, if
-// READS, until its LDS reads are done), then meets the workgroup.  A fence would wait for every
-// direct load (they count as LDS writes); what has to have arrived is exactly
-// what the count says.
-template <int N, bool READS = true>
-__device__ __forceinline__ void loads_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (READS ? 0 : 15) << 8 | (N >> 4) << 14);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // KG groups of WM x WN wavefronts; a wavefront has (BM / WM) x (BN / WN)
 // outputs.  The groups take turns at the steps of K, each through its own NB
 // LDS buffers, and add their sums at the end in a fixed order: with few tiles

@@ -430,38 +430,42 @@ __device__ __forceinline__ uint2 read_tr(const uint2* p) {
         uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v*)(p)));
 }
 
-// Rows of K and Q are loaded in the order of memory (a wavefront's load covers
-// whole rows; loading the MFMA layout directly would touch 16 rows per 256
-// bytes) and turned into operands in LDS.  The 16-byte pieces of a row are
-// permuted so that both reads below use all banks: a fragment (piece p of 16
-// rows) and a transposing read (4 adjacent pieces of 4 adjacent rows).
+// Rows of K and Q go straight to LDS in the order of memory (a wavefront's load
+// covers whole rows; loading the MFMA layout directly would touch 16 rows per
+// 256 bytes) and are read from there as operands.  The 16-byte pieces of a row
+// are permuted so that both reads below use all banks: a fragment (piece p of
+// 16 rows) and a transposing read (4 adjacent pieces of 4 adjacent rows).
+template <int DK>
+__device__ __forceinline__ int piece_xor(int row) {
+    return DK == 128 ? ((row >> 2) & 3) | (row & 3) << 2 : ((row >> 2) & 3) | (row >> 1 & 1) << 2;
+}
 template <int DK>
 __device__ __forceinline__ int piece_at(int row, int p) {
-    constexpr int P = DK / 8;
-    const int f = P == 16 ? ((row >> 2) & 3) | (row & 3) << 2 : ((row >> 2) & 3) | (row >> 1 & 1) << 2;
-    return row * P + (p ^ f);
+    return row * (DK / 8) + (p ^ piece_xor<DK>(row));
 }
 
-// The 16 rows of one token tile: load number j of lane l is piece l % P of row
-// j 64 / P + l / P.
+// The 16 rows of one token tile: load number j brings slots 64 j .. 64 j + 63.
 template <int DK>
 struct TileRows {
-    static constexpr int P = DK / 8, L = DK / 32, RPL = 64 / P;  // pieces per row, loads, rows per load
-    uint4 x[L];
-    uint32_t off[L];  // bytes, the lane's piece of each load's row
+    static constexpr int P = DK / 8, L = DK / 32;  // pieces per row, loads
+    uint32_t off[L];                               // bytes
     // `left` > 0 rows exist from the chunk's first on; further ones repeat the last.
     __device__ __forceinline__ void rows(int64_t stride, int left, int tile, int lane) {
 #pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int r = (64 * j + lane) / P;
+            off[j] = (uint32_t(min(16 * tile + r, left - 1)) * uint32_t(stride) + 8 * (lane % P ^ piece_xor<DK>(r))) * 2;
+        }
+    }
+    __device__ __forceinline__ void load(const uint16_t* base, uint4* tile_lds) const {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass rejects the 16-byte form
+        // rows lie within 63 * 2^24 elements of the first
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, 0x7fffffff, 0x00027000);
+#pragma unroll
         for (int j = 0; j < L; ++j)
-            off[j] = (uint32_t(min(16 * tile + j * RPL + lane / P, left - 1)) * uint32_t(stride) + 8 * (lane % P)) * 2;
-    }
-    __device__ __forceinline__ void load(const uint16_t* base) {
-#pragma unroll
-        for (int j = 0; j < L; ++j) x[j] = load_at<uint4>(base, off[j]);
-    }
-    __device__ __forceinline__ void put(uint4* tile_lds, int lane) const {
-#pragma unroll
-        for (int j = 0; j < L; ++j) tile_lds[piece_at<DK>(j * RPL + lane / P, lane % P)] = x[j];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(tile_lds + 64 * j), 16,
+                                                     off[j], 0, 0, 0);
+#endif
     }
 };
 
@@ -469,7 +473,7 @@ struct TileRows {
 // tokens as [step][part][column tile][lane].
 template <int DK, int NCT>
 struct ChainLds {
-    uint4 K[4][16 * DK / 8];       // rows of K by token tile, pieces permuted
+    uint4 K[2][4][16 * DK / 8];    // rows of this chunk's K and the next one's by token tile, pieces permuted
     uint4 Q[4][16 * DK / 8];       // rows of Q, each tile read by its own wavefront only
     uint4 S[DK / 32][2][NCT][64];  // state: hi, lo
     uint4 R[2][2][NCT][64];        // R: hi, lo
@@ -477,14 +481,14 @@ struct ChainLds {
     f32x4 U[4][NCT][64];           // U in fp32, rows of token tile [i] as accumulated
     uint4 V[kC * 2 * NCT];         // the chunk's rows of the slice's values
     float sc[kScalars];            // its scalars
-    int4 marks;                    // whether wavefront i's R has a value that is not finite
+    uint32_t marks[4];             // whether wavefront i's R has a value that is not finite
     uint8_t badrow[4][NCT][64];    // its rows, where marked
 };
 
 // The first row of each of the lane's columns that is not finite; kC if none.
 template <int DK, int NCT>
 __device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int col, int (&first)[NCT]) {
-    const int marks[4] = {l.marks.x, l.marks.y, l.marks.z, l.marks.w};
+    const uint32_t marks[4] = {l.marks[0], l.marks[1], l.marks[2], l.marks[3]};
     for (int ct = 0; ct < NCT; ++ct) {
         first[ct] = kC;
         for (int w = 0; w < 4; ++w)
@@ -530,41 +534,42 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     const Range seq = seq_range(a, b);
     const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
     const int64_t sh0 = int64_t(base) * d.H_v + h;
-    if (lane == 0 && wave < 4) (&l.marks.x)[w] = 0;
+    if (lane == 0 && wave < 4) l.marks[w] = 0;
 
     if (wave >= 4) {
         // ---- outputs ----
         if (chunks == 0) return;
         const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq.start * d.q_stride + int64_t(hk) * DK;
+        const uint16_t* kp = static_cast<const uint16_t*>(a.k) + seq.start * d.k_stride + int64_t(hk) * DK;
         const uint4* mp = c.m + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const int64_t q_step = kC * d.q_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        const int64_t q_step = kC * d.q_stride, k_step = kC * d.k_stride, m_step = int64_t(d.H_v) * kPairs * 2 * 64;
         const uint32_t ld = uint32_t(d.H_v) * d.d_v, o_off = (16 * w + col) * ld + 4 * g;
         int64_t o_at = (seq.start * d.H_v + h) * d.d_v + v0;
         auto run = [&](auto steps_of_tile) {
             constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
             uint4 mf[kSteps][2], qf[KS];
-            TileRows<DK> qr;
+            TileRows<DK> qr, kr;
             qr.rows(d.q_stride, seq.len, w, lane);
+            kr.rows(d.k_stride, seq.len, w, lane);
             // The chunk that `left` tokens are left from on.  The loads are not behind
             // a branch (whose end would wait for them): past the sequence the last
             // chunk is loaded again.
             auto load_q = [&](int left) {
                 if (left < kC && left > 0) qr.rows(d.q_stride, left, w, lane);
                 qp += left > 0 ? q_step : 0;
-                qr.load(qp - q_step);
+                qr.load(qp - q_step, l.Q[w]);
+            };
+            auto load_k = [&](int left, int buffer) {
+                if (left < kC && left > 0) kr.rows(d.k_stride, left, w, lane);
+                kp += left > 0 ? k_step : 0;
+                kr.load(kp - k_step, l.K[buffer][w]);
             };
             auto load_m = [&]() {
 #pragma unroll
                 for (int i = 0; i < 2 * kSteps; ++i) mf[i >> 1][i & 1] = load_at<uint4>(mp + i * 64, lane * 16);
                 mp += m_step;
             };
-            auto turn_q = [&]() {  // rows to operands
-                wave_lds_fence();
-                qr.put(l.Q[w], lane);
-                wave_lds_fence();
-#pragma unroll
-                for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
-            };
+            load_k(seq.len, 0);
             load_q(seq.len);
             __builtin_amdgcn_sched_barrier(0);
             load_m();
@@ -592,11 +597,17 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 o_at += int64_t(kC) * ld;
             };
             for (int ch = 0; ch < chunks; ++ch) {
-                lds_barrier();  // state operands, values and scalars written
-                turn_q();
+                // state operands, values and scalars written; K and Q there, since only
+                // the loads of M are younger
+                loads_barrier<2 * kSteps>();
+#pragma unroll
+                for (int s = 0; s < KS; ++s) qf[s] = l.Q[w][piece_at<DK>(col, 4 * s + g)];
+                load_k(seq.len - (ch + 1) * kC, ~ch & 1);
+                wait_count<kAnyLoads>();  // Q read
                 load_q(seq.len - (ch + 1) * kC);
+                __builtin_amdgcn_sched_barrier(0);
                 if (ch > 0) store(kC);
-                lds_barrier();  // R written
+                loads_barrier<kAnyLoads>();  // R written
                 const float cq = l.sc[3 * kC + 16 * w + col];
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
@@ -614,8 +625,8 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     }
                     O[ct] = cq * (Qh + Ql);
                 }
-                lds_barrier();  // U written
-                const int4 marks = l.marks;
+                loads_barrier<kAnyLoads>();  // U written
+                const uint32_t mark = l.marks[lane & 3];
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
                     f32x4 u[2 * kSteps];
@@ -634,11 +645,14 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         O[ct] = mfma(uh, ml, O[ct]);
                     }
                 }
-                poisoned = __ballot((marks.x | marks.y | marks.z | marks.w) != 0) != 0;
+                poisoned = __ballot(mark) != 0;
                 if (poisoned) first_bad(l, col, first);
+                __builtin_amdgcn_sched_barrier(0);
                 load_m();
+                __builtin_amdgcn_sched_barrier(0);
             }
             store(seq.len - (chunks - 1) * kC);
+            wait_count<0>();  // nothing is on its way to LDS when the workgroup ends
         };
         if (w < 2)
             run(std::integral_constant<int, 1>());
@@ -648,7 +662,6 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     }
 
     // ---- the state ----
-    __builtin_amdgcn_s_setprio(3);  // the outputs only fill what the chain leaves
     if (a.seq_status && threadIdx.x == 0 && h == 0 && v0 == 0) a.seq_status[b] = seq.ok ? GDN_OK : GDN_ERR_SHAPE;
     const int pool = a.slot ? a.slot[b] : b;
     const bool keep = pool >= 0 && pool < d.n_slots;
@@ -666,10 +679,9 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         }
     auto run = [&](auto steps_of_tile) {
         constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
-        const uint16_t* kp = static_cast<const uint16_t*>(a.k) + seq.start * d.k_stride + int64_t(hk) * DK;
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
         const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const int64_t k_step = kC * d.k_stride, v_step = kC * d.v_stride, t_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        const int64_t v_step = kC * d.v_stride, t_step = int64_t(d.H_v) * kPairs * 2 * 64;
         // wavefront 2 loads the scalars of every token, wavefront 3 gamma_64
         const float* xp = c.sc + sh0 * kScalars;
         const uint32_t x_off = (w == 3 ? kC : lane) * 16;
@@ -678,8 +690,6 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         // soon as this chunk has used it, so one set of registers covers a chunk's
         // latency.  As for the outputs, no load is behind a branch.
         uint4 tf[kSteps][2], vr, xr;
-        TileRows<DK> kr;
-        kr.rows(d.k_stride, seq.len, w, lane);
         // V: a row of the slice is 2 NCT pieces; the lane's piece
         const int vi = (w * 64 + lane) % (kC * 2 * NCT);
         uint32_t v_off;
@@ -687,11 +697,6 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             v_off = (uint32_t(min(vi / (2 * NCT), left - 1)) * uint32_t(d.v_stride) + 8 * (vi % (2 * NCT))) * 2;
         };
         v_rows(seq.len);
-        auto load_k = [&](int left) {
-            if (left < kC && left > 0) kr.rows(d.k_stride, left, w, lane);
-            kp += left > 0 ? k_step : 0;
-            kr.load(kp - k_step);
-        };
         auto load_v = [&](int left) {
             if (NCT > 1 || kSteps == 1) {  // one tile: wavefronts 0 and 1 hold all pieces
                 if (left < kC && left > 0) v_rows(left);
@@ -716,12 +721,8 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         };
         // issued in the order of the loop: a wait for one group then lets the
         // groups behind it stay in flight
-        load_k(seq.len);
         load_v(seq.len);
-        kr.put(l.K[w], lane);
         put_v();
-        __builtin_amdgcn_sched_barrier(0);
-        load_k(seq.len - kC);
         __builtin_amdgcn_sched_barrier(0);
         load_t();
         __builtin_amdgcn_sched_barrier(0);
@@ -742,13 +743,19 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     reinterpret_cast<uint2*>(&l.S[tau >> 1][0][ct][lane])[tau & 1] = hi;
                     reinterpret_cast<uint2*>(&l.S[tau >> 1][1][ct][lane])[tau & 1] = lo;
                 }
-            lds_barrier();
+            loads_barrier<kAnyLoads>();
 
             // K S^T of token tile w, then R = V - gamma K S^T
             f32x4 R[NCT], Ph[NCT], Pl[NCT];
             uint4 kf[KS];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) kf[s] = l.K[w][piece_at<DK>(col, 4 * s + g)];
+            for (int s = 0; s < KS; ++s) kf[s] = l.K[ch & 1][w][piece_at<DK>(col, 4 * s + g)];
+            const f32x4 cp = *reinterpret_cast<const f32x4*>(&l.sc[16 * w + 4 * g]);
+            uint2 v[NCT];  // the lane's column of rows 16 w + 4 g + r
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+                v[ct] = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * (4 * NCT) + 4 * ct +
+                                (col & 3));
             float check = 0.0f;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
@@ -778,18 +785,15 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     uint2 x[2];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint4* p = &l.K[2 * s + half][piece_at<DK>(4 * g + (col >> 2), 4 * (tau >> 1) + (col & 3))];
+                        const uint4* p =
+                            &l.K[ch & 1][2 * s + half][piece_at<DK>(4 * g + (col >> 2), 4 * (tau >> 1) + (col & 3))];
                         x[half] = read_tr(reinterpret_cast<const uint2*>(p) + (tau & 1));
                     }
                     ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
                 }
-            const f32x4 cp = *reinterpret_cast<const f32x4*>(&l.sc[16 * w + 4 * g]);
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                // the lane's column of rows 16 w + 4 g + r
-                const uint2 v = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * (4 * NCT) +
-                                        4 * ct + (col & 3));
-                const f32x4 vv = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+                const f32x4 vv = {bf16_lo(v[ct].x), bf16_hi(v[ct].x), bf16_lo(v[ct].y), bf16_hi(v[ct].y)};
                 R[ct] = vv - cp * (Ph[ct] + Pl[ct]);
             }
             if (n < kC)
@@ -807,7 +811,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 for (int r = 0; r < 4; ++r) check = fmaf(R[ct][r], 0.0f, check);
             const bool marked = __ballot(!(check == 0.0f)) != 0;
             if (marked || was_marked) {
-                if (lane == 0) (&l.marks.x)[w] = marked;
+                if (lane == 0) l.marks[w] = marked;
                 was_marked = marked;
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
@@ -828,7 +832,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = hi;
                 reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = lo;
             }
-            lds_barrier();
+            loads_barrier<kAnyLoads>();
 
             // U = beta R + T R below the diagonal
             f32x4 u0[NCT], u1[NCT];
@@ -853,16 +857,14 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     u1[ct] = mfma(th, rl[s], u1[ct]);
                 }
             }
-            const int4 marks = l.marks;
-            kr.put(l.K[w], lane);
-            load_k(n - 2 * kC);
+            const uint32_t mark = l.marks[lane & 3];
             f32x4 e[NCT];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 u0[ct] += u1[ct];
                 e[ct] = u0[ct] * cu;
             }
-            if (__ballot((marks.x | marks.y | marks.z | marks.w) != 0)) {
+            if (__ballot(mark)) {
                 int first[NCT];
                 first_bad(l, col, first);
 #pragma unroll
@@ -880,8 +882,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = lo;
                 l.U[w][ct][lane] = u0[ct];
             }
-            load_t();
-            lds_barrier();
+            loads_barrier<kAnyLoads>();
 
             // S <- gamma_64 S + K^T diag(decay) U
 #pragma unroll
@@ -901,8 +902,12 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                         for (int i = 0; i < TPW; ++i)
                             S[i][ct] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i][ct]);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            load_t();
+            __builtin_amdgcn_sched_barrier(0);
             put_v();
             load_v(n - 2 * kC);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
     if (chunks > 0) {
