@@ -470,40 +470,40 @@ struct TileRows {
 };
 
 // LDS of one chain workgroup: operands of the products over the state and over
-// tokens as [step][part][column tile][lane].
-template <int DK, int NCT>
+// tokens as [step][part][lane].
+template <int DK>
 struct ChainLds {
     uint4 K[2][4][16 * DK / 8];    // rows of this chunk's K and the next one's by token tile, pieces permuted
     uint4 Q[4][16 * DK / 8];       // rows of Q, each tile read by its own wavefront only
-    uint4 S[DK / 32][2][NCT][64];  // state: hi, lo
-    uint4 R[2][2][NCT][64];        // R: hi, lo
-    uint4 D[2][3][NCT][64];        // decayed U: three parts
-    f32x4 U[4][NCT][64];           // U in fp32, rows of token tile [i] as accumulated
-    uint4 V[kC * 2 * NCT];         // the chunk's rows of the slice's values
+    uint4 S[DK / 32][2][64];       // state: hi, lo
+    uint4 R[2][2][64];             // R: hi, lo
+    uint4 D[2][3][64];             // decayed U: three parts
+    f32x4 U[4][64];                // U in fp32, rows of token tile [i] as accumulated
+    uint4 V[kC * 2];               // the chunk's rows of the slice's values
     float sc[kScalars];            // its scalars
     uint32_t marks[4];             // whether wavefront i's R has a value that is not finite
-    uint8_t badrow[4][NCT][64];    // its rows, where marked
+    uint8_t badrow[4][64];         // its rows, where marked
 };
 
-// The first row of each of the lane's columns that is not finite; kC if none.
-template <int DK, int NCT>
-__device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int col, int (&first)[NCT]) {
-    const uint32_t marks[4] = {l.marks[0], l.marks[1], l.marks[2], l.marks[3]};
-    for (int ct = 0; ct < NCT; ++ct) {
-        first[ct] = kC;
-        for (int w = 0; w < 4; ++w)
-            if (marks[w])
-                for (int g = 0; g < 4; ++g) {
-                    const unsigned m = l.badrow[w][ct][16 * g + col];
-                    if (m) first[ct] = min(first[ct], 16 * w + 4 * g + __builtin_ctz(m));
-                }
-    }
+// The first row of the lane's column that is not finite; kC if none.
+template <int DK>
+__device__ __forceinline__ int first_bad(const ChainLds<DK>& l, int col) {
+    for (int w = 0; w < 4; ++w)
+        if (l.marks[w]) {
+            int first = kC;
+            for (int g = 0; g < 4; ++g) {
+                const unsigned m = l.badrow[w][16 * g + col];
+                if (m) first = min(first, 16 * w + 4 * g + __builtin_ctz(m));
+            }
+            if (first < kC) return first;
+        }
+    return kC;
 }
 
 // Eight wavefronts: 0 .. 3 carry the state from chunk to chunk, 4 .. 7 form
 // the outputs beside them.  Three barriers per chunk:
-//   chain:  state operands | K S^T, R, K^T operands | U, next K | state update
-//   output:                | next Q, store          | Q S^T     | M U
+//   chain:  state operands | K S^T, R, K^T operands | U     | state update, next T, V
+//   output:                | store, next K and Q    | Q S^T | M U, next M
 // LDS bandwidth is what the phases compete for: the outputs read the state
 // operands a phase after the chain does, and operands that do not depend on the
 // chain are read outside its critical phases.
@@ -513,12 +513,10 @@ __device__ __forceinline__ void first_bad(const ChainLds<DK, NCT>& l, int col, i
 // Vector memory instructions are dear too (16 clocks each for 1 KiB or less), so
 // values and scalars go through LDS rather than to each lane from memory, and
 // outputs are formed transposed: a lane then stores 4 adjacent values.
-//
-// NCT column tiles of 16 values per workgroup.
-template <int DK, int NCT>
+template <int DK>
 __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     constexpr int KS = DK / 32, TPW = DK / 64;
-    __shared__ ChainLds<DK, NCT> l;
+    __shared__ ChainLds<DK> l;
     const SeqArgs& a = c.s;
     const gdn_seq_dims& d = a.d;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -526,10 +524,11 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     // Workgroups go to the 8 XCDs in turn: the slices and value heads of one
     // (sequence, key head) are numbered onto one XCD, whose L2 then serves
     // their common K, Q, K^T, T and M.
-    const int group = d.H_v / d.H_k, slices = d.d_v / (16 * NCT), per = group * slices;
+    const int group = d.H_v / d.H_k, slices = d.d_v / 16, per = group * slices;
     const int j8 = blockIdx.x >> 3, item = (blockIdx.x & 7) + 8 * (j8 / per), part = j8 % per;
     if (item >= d.B * d.H_k) return;
-    const int b = longest_seq(a, item / d.H_k), hk = item % d.H_k, h = hk * group + part / slices, v0 = (part % slices) * 16 * NCT;
+    const int b = longest_seq(a, item / d.H_k), hk = item % d.H_k, h = hk * group + part / slices;
+    const int v0 = part % slices * 16;
 
     const Range seq = seq_range(a, b);
     const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
@@ -574,26 +573,21 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             __builtin_amdgcn_sched_barrier(0);
             load_m();
             __builtin_amdgcn_sched_barrier(0);
-            f32x4 O[NCT];  // transposed: column = token 16 w + col, rows = values 16 ct + 4 g + r
-            int first[NCT];
+            f32x4 O;  // transposed: column = token 16 w + col, rows = values 4 g + r
+            int first = kC;
             bool poisoned = false;
             auto store = [&](int n) {
                 if (poisoned)
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (16 * w + col >= __shfl(first[ct], 4 * g + r)) O[ct][r] = __builtin_nanf("");
-                if (16 * w + col < n)
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        const int64_t at = o_at + 16 * ct + o_off;
-                        if (d.o_dtype == GDN_BF16)
-                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + at) =
-                                make_uint2(pack_bf16(O[ct][0], O[ct][1]), pack_bf16(O[ct][2], O[ct][3]));
-                        else
-                            *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + at) = O[ct];
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * w + col >= __shfl(first, 4 * g + r)) O[r] = __builtin_nanf("");
+                if (16 * w + col < n) {
+                    if (d.o_dtype == GDN_BF16)
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + o_at + o_off) =
+                            make_uint2(pack_bf16(O[0], O[1]), pack_bf16(O[2], O[3]));
+                    else
+                        *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + o_at + o_off) = O;
+                }
                 o_at += int64_t(kC) * ld;
             };
             for (int ch = 0; ch < chunks; ++ch) {
@@ -609,44 +603,38 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 if (ch > 0) store(kC);
                 loads_barrier<kAnyLoads>();  // R written
                 const float cq = l.sc[3 * kC + 16 * w + col];
+                bf16x8 sh[KS], sl[KS];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    bf16x8 sh[KS], sl[KS];
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
-                        sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
-                    }
-                    f32x4 Qh = {0.0f, 0.0f, 0.0f, 0.0f}, Ql = Qh;
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        Qh = mfma(sh[s], __builtin_bit_cast(bf16x8, qf[s]), Qh);
-                        Ql = mfma(sl[s], __builtin_bit_cast(bf16x8, qf[s]), Ql);
-                    }
-                    O[ct] = cq * (Qh + Ql);
+                for (int s = 0; s < KS; ++s) {
+                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][lane]);
+                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][lane]);
                 }
+                f32x4 Qh = {0.0f, 0.0f, 0.0f, 0.0f}, Ql = Qh;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Qh = mfma(sh[s], __builtin_bit_cast(bf16x8, qf[s]), Qh);
+                    Ql = mfma(sl[s], __builtin_bit_cast(bf16x8, qf[s]), Ql);
+                }
+                O = cq * (Qh + Ql);
                 loads_barrier<kAnyLoads>();  // U written
                 const uint32_t mark = l.marks[lane & 3];
+                f32x4 u[2 * kSteps];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    f32x4 u[2 * kSteps];
+                for (int i = 0; i < 2 * kSteps; ++i) u[i] = l.U[i][lane];
 #pragma unroll
-                    for (int i = 0; i < 2 * kSteps; ++i) u[i] = l.U[i][ct][lane];
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        uint2 h0, l0, h1, l1;
-                        split4(u[2 * s], h0, l0);
-                        split4(u[2 * s + 1], h1, l1);
-                        const bf16x8 uh = __builtin_bit_cast(bf16x8, make_uint4(h0.x, h0.y, h1.x, h1.y));
-                        const bf16x8 ul = __builtin_bit_cast(bf16x8, make_uint4(l0.x, l0.y, l1.x, l1.y));
-                        const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
-                        O[ct] = mfma(uh, mh, O[ct]);
-                        O[ct] = mfma(ul, mh, O[ct]);
-                        O[ct] = mfma(uh, ml, O[ct]);
-                    }
+                for (int s = 0; s < kSteps; ++s) {
+                    uint2 h0, l0, h1, l1;
+                    split4(u[2 * s], h0, l0);
+                    split4(u[2 * s + 1], h1, l1);
+                    const bf16x8 uh = __builtin_bit_cast(bf16x8, make_uint4(h0.x, h0.y, h1.x, h1.y));
+                    const bf16x8 ul = __builtin_bit_cast(bf16x8, make_uint4(l0.x, l0.y, l1.x, l1.y));
+                    const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
+                    O = mfma(uh, mh, O);
+                    O = mfma(ul, mh, O);
+                    O = mfma(uh, ml, O);
                 }
                 poisoned = __ballot(mark) != 0;
-                if (poisoned) first_bad(l, col, first);
+                if (poisoned) first = first_bad(l, col);
                 __builtin_amdgcn_sched_barrier(0);
                 load_m();
                 __builtin_amdgcn_sched_barrier(0);
@@ -668,15 +656,13 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     const bool resume = keep && (!a.has_state || a.has_state[b] != 0);
     // state rows (elements of d_k) 32 (tau / 2) + 8 g + 4 (tau % 2) + r of tile tau
     float* Sp = keep ? a.S + ((int64_t(pool) * d.H_v + h) * d.d_v + v0 + col) * DK + 8 * g : nullptr;
-    f32x4 S[TPW][NCT];
+    f32x4 S[TPW];
 #pragma unroll
-    for (int i = 0; i < TPW; ++i)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-            const int tau = w * TPW + i;
-            S[i][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (resume) S[i][ct] = *reinterpret_cast<const f32x4*>(Sp + ct * 16 * DK + 32 * (tau >> 1) + 4 * (tau & 1));
-        }
+    for (int i = 0; i < TPW; ++i) {
+        const int tau = w * TPW + i;
+        S[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (resume) S[i] = *reinterpret_cast<const f32x4*>(Sp + 32 * (tau >> 1) + 4 * (tau & 1));
+    }
     auto run = [&](auto steps_of_tile) {
         constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
@@ -690,29 +676,28 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         // soon as this chunk has used it, so one set of registers covers a chunk's
         // latency.  As for the outputs, no load is behind a branch.
         uint4 tf[kSteps][2], vr, xr;
-        // V: a row of the slice is 2 NCT pieces; the lane's piece
-        const int vi = (w * 64 + lane) % (kC * 2 * NCT);
+        // V: a row of the slice is 2 pieces, wavefronts 0 and 1 hold all of them
+        const int vi = w * 64 + lane;
         uint32_t v_off;
         auto v_rows = [&](int left) {
-            v_off = (uint32_t(min(vi / (2 * NCT), left - 1)) * uint32_t(d.v_stride) + 8 * (vi % (2 * NCT))) * 2;
+            v_off = (uint32_t(min(vi / 2, left - 1)) * uint32_t(d.v_stride) + 8 * (vi % 2)) * 2;
         };
         v_rows(seq.len);
         auto load_v = [&](int left) {
-            if (NCT > 1 || kSteps == 1) {  // one tile: wavefronts 0 and 1 hold all pieces
+            if constexpr (kSteps == 1) {
                 if (left < kC && left > 0) v_rows(left);
                 vp += left > 0 ? v_step : 0;
                 vr = load_at<uint4>(vp - v_step, v_off);
-            }
-            if (kSteps == 2) {
+            } else {
                 xp += left > 0 ? x_step : 0;
                 xr = load_at<uint4>(xp - x_step, x_off);
             }
         };
         auto put_v = [&]() {
-            if (NCT > 1 || kSteps == 1) l.V[vi] = vr;
-            if (kSteps == 2) {
-                if (w == 2 || lane == 0) *reinterpret_cast<uint4*>(&l.sc[x_off / 4]) = xr;
-            }
+            if constexpr (kSteps == 1)
+                l.V[vi] = vr;
+            else if (w == 2 || lane == 0)
+                *reinterpret_cast<uint4*>(&l.sc[x_off / 4]) = xr;
         };
         auto load_t = [&]() {
 #pragma unroll
@@ -734,43 +719,33 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 
             // the state as operands
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < TPW; ++i) {
-                    const int tau = w * TPW + i;
-                    uint2 hi, lo;
-                    split4(S[i][ct], hi, lo);
-                    reinterpret_cast<uint2*>(&l.S[tau >> 1][0][ct][lane])[tau & 1] = hi;
-                    reinterpret_cast<uint2*>(&l.S[tau >> 1][1][ct][lane])[tau & 1] = lo;
-                }
+            for (int i = 0; i < TPW; ++i) {
+                const int tau = w * TPW + i;
+                uint2 hi, lo;
+                split4(S[i], hi, lo);
+                reinterpret_cast<uint2*>(&l.S[tau >> 1][0][lane])[tau & 1] = hi;
+                reinterpret_cast<uint2*>(&l.S[tau >> 1][1][lane])[tau & 1] = lo;
+            }
             loads_barrier<kAnyLoads>();
 
             // K S^T of token tile w, then R = V - gamma K S^T
-            f32x4 R[NCT], Ph[NCT], Pl[NCT];
             uint4 kf[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) kf[s] = l.K[ch & 1][w][piece_at<DK>(col, 4 * s + g)];
             const f32x4 cp = *reinterpret_cast<const f32x4*>(&l.sc[16 * w + 4 * g]);
-            uint2 v[NCT];  // the lane's column of rows 16 w + 4 g + r
+            // the lane's column of rows 16 w + 4 g + r
+            const uint2 v = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * 4 + (col & 3));
+            bf16x8 sh[KS], sl[KS];
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-                v[ct] = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * (4 * NCT) + 4 * ct +
-                                (col & 3));
-            float check = 0.0f;
+            for (int s = 0; s < KS; ++s) {
+                sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][lane]);
+                sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][lane]);
+            }
+            f32x4 Ph = {0.0f, 0.0f, 0.0f, 0.0f}, Pl = Ph;
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                bf16x8 sh[KS], sl[KS];
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][ct][lane]);
-                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][ct][lane]);
-                }
-                Ph[ct] = Pl[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    Ph[ct] = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph[ct]);
-                    Pl[ct] = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl[ct]);
-                }
+            for (int s = 0; s < KS; ++s) {
+                Ph = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph);
+                Pl = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl);
             }
             // K^T of the wavefront's state rows: accumulator row rho of tile tau is
             // element 32 (tau / 2) + 8 (rho / 4) + 4 (tau % 2) + rho % 4.  In a
@@ -791,117 +766,87 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     }
                     ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
                 }
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const f32x4 vv = {bf16_lo(v[ct].x), bf16_hi(v[ct].x), bf16_lo(v[ct].y), bf16_hi(v[ct].y)};
-                R[ct] = vv - cp * (Ph[ct] + Pl[ct]);
-            }
+            const f32x4 vv = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+            f32x4 R = vv - cp * (Ph + Pl);
             if (n < kC)
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * w + 4 * g + r >= n) R[ct][r] = 0.0f;
+                for (int r = 0; r < 4; ++r)
+                    if (16 * w + 4 * g + r >= n) R[r] = 0.0f;
             // A value that is not finite must not reach earlier tokens through a
             // product with a masked zero: it is taken out here, its row is marked,
             // and rows from the first marked one on come out as NaN.
+            float check = 0.0f;
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) check = fmaf(R[ct][r], 0.0f, check);
+            for (int r = 0; r < 4; ++r) check = fmaf(R[r], 0.0f, check);
             const bool marked = __ballot(!(check == 0.0f)) != 0;
             if (marked || was_marked) {
                 if (lane == 0) l.marks[w] = marked;
                 was_marked = marked;
+                unsigned m = 0;
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    unsigned m = 0;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (!finite(R[ct][r])) {
-                            m |= 1u << r;
-                            R[ct][r] = 0.0f;
-                        }
-                    l.badrow[w][ct][lane] = m;
-                }
+                for (int r = 0; r < 4; ++r)
+                    if (!finite(R[r])) {
+                        m |= 1u << r;
+                        R[r] = 0.0f;
+                    }
+                l.badrow[w][lane] = m;
             }
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                uint2 hi, lo;
-                split4(R[ct], hi, lo);
-                reinterpret_cast<uint2*>(&l.R[w >> 1][0][ct][lane])[w & 1] = hi;
-                reinterpret_cast<uint2*>(&l.R[w >> 1][1][ct][lane])[w & 1] = lo;
-            }
+            uint2 r_hi, r_lo;
+            split4(R, r_hi, r_lo);
+            reinterpret_cast<uint2*>(&l.R[w >> 1][0][lane])[w & 1] = r_hi;
+            reinterpret_cast<uint2*>(&l.R[w >> 1][1][lane])[w & 1] = r_lo;
             loads_barrier<kAnyLoads>();
 
             // U = beta R + T R below the diagonal
-            f32x4 u0[NCT], u1[NCT];
             const f32x4 be = *reinterpret_cast<const f32x4*>(&l.sc[kC + 16 * w + 4 * g]);
             const f32x4 cu = *reinterpret_cast<const f32x4*>(&l.sc[2 * kC + 16 * w + 4 * g]);
             const float gam = l.sc[4 * kC];
+            bf16x8 rh[kSteps], rl[kSteps];
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                bf16x8 rh[kSteps], rl[kSteps];
+            for (int s = 0; s < kSteps; ++s) {
+                rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][lane]);
+                rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][lane]);
+            }
+            f32x4 u0 = be * R, u1 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][ct][lane]);
-                    rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][ct][lane]);
-                }
-                u0[ct] = be * R[ct];
-                u1[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
-                    u1[ct] = mfma(tl, rh[s], u1[ct]);
-                    u0[ct] = mfma(th, rh[s], u0[ct]);
-                    u1[ct] = mfma(th, rl[s], u1[ct]);
-                }
+            for (int s = 0; s < kSteps; ++s) {
+                const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
+                u1 = mfma(tl, rh[s], u1);
+                u0 = mfma(th, rh[s], u0);
+                u1 = mfma(th, rl[s], u1);
             }
             const uint32_t mark = l.marks[lane & 3];
-            f32x4 e[NCT];
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u0[ct] += u1[ct];
-                e[ct] = u0[ct] * cu;
-            }
+            u0 += u1;
+            f32x4 e = u0 * cu;
             if (__ballot(mark)) {
-                int first[NCT];
-                first_bad(l, col, first);
+                const int first = first_bad(l, col);
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * w + 4 * g + r == first[ct]) e[ct][r] = __builtin_nanf("");
+                for (int r = 0; r < 4; ++r)
+                    if (16 * w + 4 * g + r == first) e[r] = __builtin_nanf("");
             }
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                uint2 hi, mid, lo;
-                split4(e[ct], hi, mid, lo);
-                reinterpret_cast<uint2*>(&l.D[w >> 1][0][ct][lane])[w & 1] = hi;
-                reinterpret_cast<uint2*>(&l.D[w >> 1][1][ct][lane])[w & 1] = mid;
-                reinterpret_cast<uint2*>(&l.D[w >> 1][2][ct][lane])[w & 1] = lo;
-                l.U[w][ct][lane] = u0[ct];
-            }
+            uint2 hi, mid, lo;
+            split4(e, hi, mid, lo);
+            reinterpret_cast<uint2*>(&l.D[w >> 1][0][lane])[w & 1] = hi;
+            reinterpret_cast<uint2*>(&l.D[w >> 1][1][lane])[w & 1] = mid;
+            reinterpret_cast<uint2*>(&l.D[w >> 1][2][lane])[w & 1] = lo;
+            l.U[w][lane] = u0;
             loads_barrier<kAnyLoads>();
 
             // S <- gamma_64 S + K^T diag(decay) U
+            bf16x8 du[2][3];
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                bf16x8 du[2][3];
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int p = 0; p < 3; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][lane]);
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][ct][lane]);
+            for (int i = 0; i < TPW; ++i) S[i] *= gam;
 #pragma unroll
-                for (int i = 0; i < TPW; ++i) S[i][ct] *= gam;
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int p = 0; p < 3; ++p)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
-#pragma unroll
-                        for (int i = 0; i < TPW; ++i)
-                            S[i][ct] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i][ct]);
-            }
+                    for (int i = 0; i < TPW; ++i)
+                        S[i] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i]);
             __builtin_amdgcn_sched_barrier(0);
             load_t();
             __builtin_amdgcn_sched_barrier(0);
@@ -918,12 +863,10 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     }
     if (keep)
 #pragma unroll
-        for (int i = 0; i < TPW; ++i)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const int tau = w * TPW + i;
-                *reinterpret_cast<f32x4*>(Sp + ct * 16 * DK + 32 * (tau >> 1) + 4 * (tau & 1)) = S[i][ct];
-            }
+        for (int i = 0; i < TPW; ++i) {
+            const int tau = w * TPW + i;
+            *reinterpret_cast<f32x4*>(Sp + 32 * (tau >> 1) + 4 * (tau & 1)) = S[i];
+        }
 }
 
 template <int DK>
@@ -931,11 +874,7 @@ hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
     const gdn_seq_dims& d = c.s.d;
     prep_kernel<DK><<<dim3(c.slots, d.H_k), 256, 0, stream>>>(c);
     const int items8 = (d.B * d.H_k + 7) / 8 * 8, per16 = d.H_v / d.H_k * (d.d_v / 16);
-    const int64_t wgs = int64_t(d.B) * d.H_v * (d.d_v / 16);
-    if (wgs > 512)
-        chain_kernel<DK, 2><<<items8 * per16 / 2, 512, 0, stream>>>(c);
-    else
-        chain_kernel<DK, 1><<<items8 * per16, 512, 0, stream>>>(c);
+    chain_kernel<DK><<<items8 * per16, 512, 0, stream>>>(c);
     return hipGetLastError();
 }
 
