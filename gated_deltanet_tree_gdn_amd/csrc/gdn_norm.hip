@@ -2,7 +2,12 @@
 //
 // Both are one pass over rows held in registers: every input is read once,
 // every output written once, sums in fp32 over lanes (and over wavefronts
-// through LDS where one row spans several).  HBM-bound.
+// through LDS where one row spans several).  Memory-bound: 8191 x 5120, x bf16,
+// residual fp32, both norms: 503 MB in 108 us, 4.6 TB/s; gated, 16384 x 32 x 128
+// bf16: 403 MB in 70 us, 5.7 TB/s (the last calls' rows are partly in cache; a
+// copy of 1 GiB reaches 5.2).  Rows need not start on 16 bytes: pieces of 8
+// elements are loaded wherever they start (8191 x 5119: 125 us; one element at a
+// time 242 us).
 
 #include "gdn_layer_internal.h"
 #include "gdn_layer_util.h"
