@@ -105,6 +105,9 @@ __device__ __forceinline__ float delta_step(float (&S)[E], const float (&k)[E], 
 }
 
 // Grid (d_v / 32, H_v, B): a wavefront takes 8 state rows.
+// Bound by the states, read and written once: 114 of 120 rows live, H_v 32, d
+// 128: 478 MB in 89 us, 5.4 TB/s (a copy of 1 GiB reaches 5.2).  One token alone is
+// 4 MB in 3.5 us, most of it latency, over 512 wavefronts.
 template <typename T, int DK>
 __global__ void __launch_bounds__(256) decode_kernel(SeqArgs a) {
     constexpr int E = DK / 8;
@@ -129,10 +132,6 @@ __global__ void __launch_bounds__(256) decode_kernel(SeqArgs a) {
     if (l8 == 0) store1(a.o, d.o_dtype, bh * d.d_v + row, o);
 }
 
-// Bound by the states, read and written once: 114 of 120 rows live, H_v 32, d
-// 128: 478 MB in 89 us, 5.4 TB/s (a copy of 1 GiB reaches 5.2).  One token alone is
-// 4 MB and 3.5 us, most of it latency; 8 rows per wavefront then give 512
-// wavefronts or more, 16 rows were slower there and no faster with many.
 // One token as loaded.
 template <typename T, int E>
 struct Token {

@@ -9,8 +9,8 @@
 //    buffers filled by direct loads while others are multiplied.
 //
 // Measured: 1 x 12352 x 4096 18 us (101 MB of weights, partly in cache: 5.7 TB/s);
-// 777 x 4096 x 4096 with bias, silu and a residual 40 us (650 TFLOP/s: 224 tiles
-// of 128 x 128 on 256 CUs, 12 us of it the epilogue and the start); 16384 x 12352
+// 777 x 4096 x 4096 with bias, silu and a residual 40 us (650 TFLOP/s: one round of 224
+// tiles of 128 x 128 on 256 CUs, its loads ahead by a step); 16384 x 12352
 // x 4096 1400 us (1180 TFLOP/s).  With 256 x 256 tiles LDS carries 256 KiB per
 // step (192 read as operands, 64 written by the loads), 2,048 clocks, as many as
 // the MFMAs take: the two compete, and the kernel without its loads takes three

@@ -30,7 +30,7 @@
 // throughout, 1.7e-3 for an output rounded to bf16).
 //
 // Measured, H_k 16, H_v 32, d 128, bf16, states not resumed: one sequence of
-// 16384 tokens 445 us (prep 92, chain 353), 13 of 7919 tokens in all 209 us.
+// 16384 tokens 437 us (prep 87, chain 350), 13 of 7919 tokens in all 205 us.
 // The inputs, outputs and states are 404 MB and 169 MB; at the rate of a copy
 // (5.2 TB/s) that is 78 and 33 us.
 
@@ -173,7 +173,7 @@ __device__ __forceinline__ float exp_diff(double hi, double lo) {
 // blocks by substitution (a column per lane), the blocks below them by fp32 MFMA
 // (bf16 parts of the inverse would lose what the substitution kept).  Bound by
 // memory: it writes T and M, 768 bytes per (token, value head), and reads q and k;
-// 16384 tokens, H_v 32: 336 MB in 92 us, 3.7 TB/s.
+// 16384 tokens, H_v 32: 336 MB in 87 us, 3.9 TB/s.
 template <int DK>
 __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     constexpr int KS = DK / 32;
@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     const SeqArgs& a = c.s;
     const gdn_seq_dims& d = a.d;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
-    const int slot = blockIdx.x, hk = blockIdx.y;
+    // The key heads of a slot run on one XCD one after the other: rows of g and
+    // beta hold all heads, so its L2 reads them once.
+    const int j8 = blockIdx.x >> 3, slot = j8 / d.H_k * 8 + (blockIdx.x & 7), hk = j8 % d.H_k;
+    if (slot >= c.slots) return;
     const int b = find_seq(a, slot);
     const Range seq = seq_range(a, b);
     const int ch = slot - slot_base(a, b);
@@ -894,7 +897,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 template <int DK>
 hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
     const gdn_seq_dims& d = c.s.d;
-    prep_kernel<DK><<<dim3(c.slots, d.H_k), 256, 0, stream>>>(c);
+    prep_kernel<DK><<<(c.slots + 7) / 8 * 8 * d.H_k, 256, 0, stream>>>(c);
     const int items8 = (d.B * d.H_k + 7) / 8 * 8, per16 = d.H_v / d.H_k * (d.d_v / 16);
     chain_kernel<DK><<<items8 * per16, 512, 0, stream>>>(c);
     return hipGetLastError();
