@@ -92,3 +92,40 @@ def test_chunks_of_short_sequences():
     say(f"[prefill] {lengths}")
     d = make(sum(lengths), slots=10, seed=1)
     run_prefill(d, lengths, has=[1, 0] * 5, o_dtype=F32)
+
+
+def test_a_decode_step_in_a_graph():
+    """norm, projection, decode, gated norm and projection captured once and replayed: every replay equals the eager step
+    bit for bit, from the same state, with eager work of other sizes between the replays."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    randn = lambda *n: torch.randn(*n, generator=gen, device="cuda")  # noqa: E731
+    B, D, Hk, Hv, dh = 9, 200, 2, 4, 64
+    x, h = randn(B, D).to(BF16), randn(B, D)
+    w, wo, norm, head = randn((2 * Hk + 2 * Hv) * dh, D).to(BF16), randn(D, Hv * dh).to(BF16), randn(D), randn(dh)
+    g, beta, S = -torch.rand(B, Hv, device="cuda"), torch.rand(B, Hv, device="cuda"), randn(B, Hv, dh, dh)
+    S0 = S.clone()
+
+    def step():
+        y, r = gdn.gdn_add_norm(x, h, norm)
+        q, k, v, z = gdn.gdn_linear(y, w).unflatten(1, (-1, dh)).split([Hk, Hk, Hv, Hv], dim=1)
+        o = gdn.gdn_decode(q, k, v, g, beta, S, qk_l2norm=True, o_dtype=F32)
+        return gdn.gdn_linear(gdn.gdn_gated_norm(o, z, head).flatten(1), wo, residual=r, y_dtype=F32)
+
+    want = step().clone()
+    want_S = S.clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        S.copy_(S0)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(S, want_S), i
+        gdn.gdn_linear(randn(300 + i, D).to(BF16), w)
+        torch.cuda.synchronize()
