@@ -11,7 +11,7 @@
 // Measured: 1 x 12352 x 4096 18 us (101 MB of weights, partly in cache: 5.7 TB/s);
 // 777 x 4096 x 4096 with bias, silu and a residual 40 us (650 TFLOP/s: one round of 224
 // tiles of 128 x 128 on 256 CUs, its loads ahead by a step); 16384 x 12352
-// x 4096 1400 us (1180 TFLOP/s).  With 256 x 256 tiles LDS carries 256 KiB per
+// x 4096 1360 us (1220 TFLOP/s).  With 256 x 256 tiles LDS carries 256 KiB per
 // step (192 read as operands, 64 written by the loads), 2,048 clocks, as many as
 // the MFMAs take: the two compete, and the kernel without its loads takes three
 // quarters of the time.  Steps of 32 (4% slower), wavefronts of 128 x 128 (spills)
@@ -73,9 +73,11 @@ __device__ __forceinline__ void put(const LinearArgs& a, int64_t m, int n, float
 // Workgroups go to the 8 XCDs in turn; here each XCD gets a run of
 // consecutive tiles, ordered in bands of 8 tile rows, so that the tiles it has
 // in flight share rows of x and w in its L2.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
-    const int total = tiles_m * tiles_n, q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
-    const int t = xcd * q + min(xcd, r) + i;
+__device__ __forceinline__ int xcd_run(int id, int total) {
+    const int q = total / 8, r = total % 8, xcd = id % 8;
+    return xcd * q + min(xcd, r) + id / 8;
+}
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
     constexpr int kBand = 8;
     const int band = t / (kBand * tiles_n), in = t - band * kBand * tiles_n, rows = min(kBand, tiles_m - band * kBand);
     tm = band * kBand + in % rows;
@@ -114,12 +116,16 @@ struct Stage {
             off[i] = (row * uint32_t(stride) + 8 * ((lane & 7) ^ (r & 7))) * 2;
         }
     }
-    __device__ __forceinline__ void load(uint4* lds, int k, int wave) const {
+    // Pieces from `pieces` on repeat the last one before: K ends there.
+    template <bool TAIL>
+    __device__ __forceinline__ void load(uint4* lds, int k, int pieces, int wave, int lane) const {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass rejects the 16-byte form
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, 0x7fffffff, 0x00027000);
+        const uint32_t back = !TAIL ? 0 : max(((lane & 7) ^ (lane >> 3)) - (pieces - 1), 0) * 16;
 #pragma unroll
         for (int i = 0; i < L; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(lds + (wave * L + i) * 64), 16, off[i], k * 2, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(lds + (wave * L + i) * 64), 16, off[i] - back, k * 2,
+                                                     0, 0);
 #endif
     }
 };
@@ -144,22 +150,25 @@ __device__ __forceinline__ void stage_any(uint4* lds, const uint16_t* base, int6
 // outputs.  The groups take turns at the steps of K, each through its own NB
 // LDS buffers, and add their sums at the end in a fixed order: with few tiles
 // that keeps KG times as many loads in flight on a CU.
-template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
-__global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
+template <int BM, int BN, int WM, int WN, int KG, int NB>
+constexpr int tile_lds_bytes() {
+    constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int out = W * (TM > 4 ? 64 : TM * 16) * (TN * 16 + 4) * 4;
+    return std::max({KG * (BM + BN) * 8 * NB * 16, out, (KG - 1) * W * TM * TN * 1024});
+}
+
+// DIRECT: rows in whole 16-byte pieces; TAIL: K is not a multiple of 64 (looking
+// after the last step costs every step 2 to 4 %).
+template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT, bool TAIL>
+__device__ __forceinline__ void tile(const LinearArgs& a, char* lds, int64_t m0, int64_t n0) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int kOutRows = TM > 4 ? 64 : TM * 16, kOutLd = TN * 16 + 4;  // epilogue: rows of a wavefront at a time
-    constexpr int kGroupPieces = (BM + BN) * 8 * NB, kOutBytes = W * kOutRows * kOutLd * 4;
-    constexpr int kSumBytes = (KG - 1) * W * TM * TN * 1024, kStageBytes = KG * kGroupPieces * 16;
-    constexpr int kMax1 = kStageBytes > kOutBytes ? kStageBytes : kOutBytes;
-    __shared__ __align__(16) char lds[kMax1 > kSumBytes ? kMax1 : kSumBytes];
+    constexpr int kGroupPieces = (BM + BN) * 8 * NB;
     const gdn_linear_dims& d = a.d;
     const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = all % W, grp = all / W, col = lane & 15, g = lane >> 4;
     auto xs = [&](int p) { return reinterpret_cast<uint4*>(lds) + grp * kGroupPieces + p * BM * 8; };
     auto ws = [&](int p) { return reinterpret_cast<uint4*>(lds) + grp * kGroupPieces + (NB * BM + p * BN) * 8; };
-    int tm, tn;
-    tile_of(blockIdx.x, (d.M + BM - 1) / BM, (d.N + BN - 1) / BN, tm, tn);
-    const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
     const int wm = wave % WM, wn = wave / WM;
     const uint16_t* xp = static_cast<const uint16_t*>(a.x);
     const uint16_t* wp = static_cast<const uint16_t*>(a.w);
@@ -194,7 +203,20 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
         __syncthreads();
     };
     if constexpr (DIRECT) {
-        const int steps = d.K / kBK;
+        // Whole pieces of 8 elements go through the pipeline; where the last step has
+        // fewer than 8 of them, its operands are cleared from there on (both: what the
+        // loads bring instead may be infinite).
+        const bool whole = !TAIL || d.K % 8 == 0;
+        const int steps = TAIL && whole ? (d.K + kBK - 1) / kBK : d.K / kBK;
+        const int last = TAIL && whole ? d.K % kBK / 8 : 8;
+        auto finish = [&](Frags& f, int t, int s) {
+            if (TAIL && t == steps - 1 && 4 * s + g >= last) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) f.x[i] = bf16x8{};
+#pragma unroll
+                for (int j = 0; j < TN; ++j) f.w[j] = bf16x8{};
+            }
+        };
         if (steps > 0) {
             Stage<BM, W> sx;
             Stage<BN, W> sw;
@@ -206,8 +228,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
             auto load = [&](int round) {
                 const int t = round * KG + grp, p = round % NB;
                 if (t < steps) {
-                    sx.load(xs(p), t * kBK, wave);
-                    sw.load(ws(p), t * kBK, wave);
+                    const int pieces = t == steps - 1 ? last : 8;
+                    sx.template load<TAIL>(xs(p), t * kBK, pieces, wave, lane);
+                    sw.template load<TAIL>(ws(p), t * kBK, pieces, wave, lane);
                 }
             };
 #pragma unroll
@@ -222,6 +245,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             read(f, r & 1, s);
+                            finish(f, r * KG + grp, s);
                             multiply(f);
                         }
                     }
@@ -243,10 +267,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
                     load(r + NB - 1);
                     read(f1, p, 1);
                     __builtin_amdgcn_sched_barrier(0);
+                    finish(f0, r * KG + grp, 0);
                     if (mine) multiply(f0);
                     __builtin_amdgcn_sched_barrier(0);
                     read(f0, next, 0);
                     __builtin_amdgcn_sched_barrier(0);
+                    finish(f1, r * KG + grp, 1);
                     if (mine) multiply(f1);
                     __builtin_amdgcn_sched_barrier(0);
                     if ((r + NB) * KG <= steps)
@@ -258,9 +284,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
                 loads_barrier<0>();
             }
         }
-        // the end of K: past it both operands are staged as zeros, so every
-        // group but the first adds nothing
-        if (d.K % kBK) any_step(grp == 0 ? d.K / kBK * kBK : d.K);
+        // the end of K in elements: past it both operands are staged as zeros, so
+        // every group but the first adds nothing
+        if (TAIL && !whole) any_step(grp == 0 ? d.K / kBK * kBK : d.K);
     } else {
         for (int k = 0; k < d.K; k += kBK * KG) any_step(k + grp * kBK);
     }
@@ -303,6 +329,37 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
             load8(out, GDN_F32, r * kOutLd + c, v);
             if (m < d.M && n < d.N) put<8>(a, m, n, v);
         }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT, bool TAIL>
+__global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
+    __shared__ __align__(16) char lds[tile_lds_bytes<BM, BN, WM, WN, KG, NB>()];
+    const int tiles_m = (a.d.M + BM - 1) / BM, tiles_n = (a.d.N + BN - 1) / BN;
+    int tm, tn;
+    tile_at(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    tile<BM, BN, WM, WN, KG, NB, DIRECT, TAIL>(a, lds, int64_t(tm) * BM, int64_t(tn) * BN);
+}
+
+// The first `whole` tiles of 256 x 256 as such, the rest in quarters, with two
+// groups over K each: what does not fill a round of CUs then takes a third of a
+// round for 64 tiles or fewer, two thirds for 128.  In quarters and as another
+// round: 4096 x 12352 x 4096 (16 tiles over) 356 and 442 us, 5000 x 4096 x 4096 (64)
+// 141 and 163, 6000 x 4096 x 4096 (128) 179 and 182.
+template <bool TAIL>
+__global__ void __launch_bounds__(512) tile256_kernel(LinearArgs a, int whole) {
+    __shared__ __align__(16) char
+        lds[std::max(tile_lds_bytes<256, 256, 2, 4, 1, 2>(), tile_lds_bytes<128, 128, 2, 2, 2, 2>())];
+    const int tiles_m = (a.d.M + 255) / 256, tiles_n = (a.d.N + 255) / 256, id = blockIdx.x;
+    int tm, tn;
+    if (id < whole) {
+        tile_at(xcd_run(id, whole), tiles_m, tiles_n, tm, tn);
+        tile<256, 256, 2, 4, 1, 2, true, TAIL>(a, lds, int64_t(tm) * 256, int64_t(tn) * 256);
+    } else {
+        const int u = xcd_run(id - whole, 4 * (tiles_m * tiles_n - whole));
+        tile_at(whole + (u >> 2), tiles_m, tiles_n, tm, tn);
+        const int64_t m0 = int64_t(tm) * 256 + (u & 1) * 128, n0 = int64_t(tn) * 256 + (u >> 1 & 1) * 128;
+        if (m0 < a.d.M && n0 < a.d.N) tile<128, 128, 2, 2, 2, 2, true, TAIL>(a, lds, m0, n0);
     }
 }
 
@@ -360,8 +417,18 @@ void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
 
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
 void launch_tile(const LinearArgs& a, hipStream_t stream) {
-    const int tiles = ((a.d.M + BM - 1) / BM) * ((a.d.N + BN - 1) / BN);
-    tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT><<<tiles, 64 * WM * WN * KG, 0, stream>>>(a);
+    const int tiles = ((a.d.M + BM - 1) / BM) * ((a.d.N + BN - 1) / BN), threads = 64 * WM * WN * KG;
+    if (DIRECT && a.d.K % kBK)
+        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, DIRECT><<<tiles, threads, 0, stream>>>(a);
+    else
+        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, false><<<tiles, threads, 0, stream>>>(a);
+}
+
+void launch_tile256(const LinearArgs& a, int tiles, int cut, hipStream_t stream) {
+    if (a.d.K % kBK)
+        tile256_kernel<true><<<tiles + 3 * cut, 512, 0, stream>>>(a, tiles - cut);
+    else
+        tile256_kernel<false><<<tiles + 3 * cut, 512, 0, stream>>>(a, tiles - cut);
 }
 
 // Rows of any alignment to rows of 16-byte pieces.
@@ -422,19 +489,30 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
             a.w = ws;
             d.w_stride = (int64_t(d.K) + 7) / 8 * 8;
         }
+        if (p.x && p.w) d.K = int(d.x_stride);  // the copies end in zeros
     }
     const bool aligned = p.copy || !(p.x || p.w);
     // direct loads: a tile's rows lie within 2^31 bytes of its first
     const bool direct = aligned && d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
     auto tiles = [&](int64_t t) { return double((d.M + t - 1) / t) * double((d.N + t - 1) / t); };
-    // What each kernel takes at K = 4096 in us (measured over M = 64 .. 8192,
-    // N = 4096 .. 12352); the ratios hold for other K.
-    const double t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
-    const double k64two = 16.0 * std::ceil(t64 / 256);   // 256 KiB of loads in flight per CU: few tiles
-    const double k64 = std::max(20.0, 0.05 * t64);       // two workgroups per CU
-    const double k128two = t128 <= 256 ? 36.0 : 1e30;    // one round of tiles, two groups per CU
-    const double k128 = std::max(43.0, 0.133 * t128);    // two workgroups per CU
-    const double k256 = 108.0 * std::ceil(t256 / 256);   // fewest bytes through LDS per product
+    // What each kernel takes in us, a part that grows with K and one that does not
+    // (start and epilogue), fitted to measurements at K = 256, 1024 and 4096 over M
+    // = 64 .. 16384, N = 1024 .. 12352.
+    const double k = d.K / 4096.0, t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
+    // 256 KiB of loads in flight per CU: few tiles
+    const double k64two = (2.4 + 15.5 * k) * std::ceil(t64 / 256);
+    // two workgroups per CU
+    const double k64 = std::max(2.0 + 18.0 * k, (0.005 + 0.0516 * k) * t64);
+    // one round of tiles, two groups per CU
+    const double k128two = t128 <= 256 ? 7.8 + 34.5 * k : 1e30;
+    // two workgroups per CU
+    const double k128 = std::max(6.5 + 42.0 * k, (0.009 + 0.122 * k) * t128);
+    // fewest bytes through LDS per product; up to half a round of tiles over whole
+    // rounds in quarters (their start overlaps the end of the round before)
+    const double k256round = 11.0 + 100.0 * k, over = t256 - 256 * std::floor(t256 / 256);
+    const double quarters = 34.5 * k * std::ceil(over / 64);
+    const bool cut = t256 > 256 && over > 0 && over <= 128;
+    const double k256 = 2.0 + k256round * (cut ? std::floor(t256 / 256) : std::ceil(t256 / 256)) + (cut ? quarters : 0.0);
     const double best = std::min({k64two, k64, k128two, k128, k256});
     if (d.M <= 16 && d.N <= 8192)
         launch_thin(a, aligned && d.K % 8 == 0, stream);
@@ -449,7 +527,7 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
     else if (best == k128)
         launch_tile<128, 128, 2, 4, 1, 2, true>(a, stream);
     else
-        launch_tile<256, 256, 2, 4, 1, 2, true>(a, stream);
+        launch_tile256(a, int(t256), cut ? int(over) : 0, stream);
     return hipGetLastError();
 }
 

@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 gdn = pytest.importorskip("gated_deltanet_tree_gdn_amd")
 
-from test_gpu_layer import BF16, CHUNK_TOL, F32, FP32_TOL, check, gpu, make, rel, rms, run_prefill, say  # noqa: E402,F401
+from test_gpu_layer import BF16, CHUNK_TOL, F32, FP32_TOL, LINEAR_TOL, check, gpu, make, rel, rms, run_prefill, say  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,24 @@ def test_a_decode_step_in_a_graph():
         assert torch.equal(out, want) and torch.equal(S, want_S), i
         gdn.gdn_linear(randn(300 + i, D).to(BF16), w)
         torch.cuda.synchronize()
+
+
+# one for each tile and for 256 x 256 tiles with the last ones in quarters
+@pytest.mark.parametrize("M,N", [(40, 300), (300, 900), (130, 5000), (777, 4096), (1100, 4100), (4300, 4096)])
+@pytest.mark.parametrize("K", [8, 56, 64, 72, 200, 264, 440])
+def test_linear_ends_of_k(M, N, K):
+    """K in whole pieces of 8 but not in whole steps of 64, the rows slices of wider ones that hold NaN beside them."""
+    if M > 4000 and K not in (72, 200):
+        pytest.skip("two of the largest are enough")
+    gen = torch.Generator(device="cuda").manual_seed(M + N + K)
+    wide = [torch.full((n, K + 16), float("nan"), dtype=BF16, device="cuda") for n in (M, N)]
+    x, w = (t[:, 8:8 + K] for t in wide)
+    x.copy_(torch.randn(M, K, generator=gen, device="cuda"))
+    w.copy_(torch.randn(N, K, generator=gen, device="cuda") * K ** -0.5)
+    y = gdn.gdn_linear(x, w, y_dtype=F32)
+    want = x.double().contiguous() @ w.double().t().contiguous()
+    check(y, want, LINEAR_TOL, f"{M} x {N} x {K}")
+    x[3, K - 1] = float("inf")  # the last element: its row alone, no NaN from what was cleared
+    y2 = gdn.gdn_linear(x, w, y_dtype=F32)
+    assert torch.isinf(y2[3]).all()
+    assert torch.equal(y2[:3], y[:3]) and torch.equal(y2[4:], y[4:])
