@@ -505,14 +505,15 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
     const double k64 = std::max(2.0 + 18.0 * k, (0.005 + 0.0516 * k) * t64);
     // one round of tiles, two groups per CU
     const double k128two = t128 <= 256 ? 7.8 + 34.5 * k : 1e30;
-    // two workgroups per CU
-    const double k128 = std::max(6.5 + 42.0 * k, (0.009 + 0.122 * k) * t128);
-    // fewest bytes through LDS per product; up to half a round of tiles over whole
-    // rounds in quarters (their start overlaps the end of the round before)
-    const double k256round = 11.0 + 100.0 * k, over = t256 - 256 * std::floor(t256 / 256);
-    const double quarters = 34.5 * k * std::ceil(over / 64);
-    const bool cut = t256 > 256 && over > 0 && over <= 128;
-    const double k256 = 2.0 + k256round * (cut ? std::floor(t256 / 256) : std::ceil(t256 / 256)) + (cut ? quarters : 0.0);
+    // two workgroups per CU, rounds of 512 tiles
+    const double k128 = std::max(6.5 + 42.0 * k, (6.0 + 59.0 * k) * std::ceil(t128 / 512));
+    // fewest bytes through LDS per product; rounds of 256 tiles, and up to half a round
+    // of tiles over whole ones in quarters (their start overlaps the end of the round
+    // before)
+    const double full = std::floor(t256 / 256), over = t256 - 256 * full;
+    const bool cut = full > 0 && over > 0 && over <= 128;
+    const double part = cut ? 34.5 * k * std::ceil(over / 64) : 11.0 + (75.0 + 25.0 * over / 256) * k;
+    const double k256 = 2.0 + (11.0 + 100.0 * k) * full + (over > 0 ? part : 0.0);
     const double best = std::min({k64two, k64, k128two, k128, k256});
     if (d.M <= 16 && d.N <= 8192)
         launch_thin(a, aligned && d.K % 8 == 0, stream);
