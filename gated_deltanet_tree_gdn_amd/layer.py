@@ -44,13 +44,13 @@ class LinearDims(ctypes.Structure):
 
 _lib = None
 _torch = None
-_Tensor = _raw_stream = _current_device = None  # from torch, bound on first use
+_Tensor = _raw_stream = _current_device = _empty_like = None  # from torch, bound on first use
 _codes = {}  # torch dtype -> gdn_dtype
 
 
 def layer_library():
     """The HIP library with this header's entry points declared."""
-    global _lib, _torch, _Tensor, _raw_stream, _current_device
+    global _lib, _torch, _Tensor, _raw_stream, _current_device, _empty_like
     if _lib is None:
         lib = load_library()
         import torch
@@ -68,7 +68,7 @@ def layer_library():
         for name in ("gdn_prefill", "gdn_decode", "gdn_add_norm", "gdn_gated_norm", "gdn_linear"):
             getattr(lib, name).restype = ctypes.c_int
         _codes.update({torch.bfloat16: GDN_BF16, torch.float32: GDN_F32})
-        _torch, _Tensor = torch, torch.Tensor
+        _torch, _Tensor, _empty_like = torch, torch.Tensor, torch.empty_like
         _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         _lib = lib
     return _lib
@@ -134,11 +134,14 @@ def _stream(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(like, shape, dtype, index, raw):
+def _empty(like, shape, dtype, index, raw, stream):
     """Memory for an output.  The allocator hands it out for the current
     stream; where the call runs on another, it is marked as used there."""
-    t = like.new_empty(shape, dtype=dtype)
-    if raw != _raw_stream(index):
+    if like.shape == shape and like.is_contiguous():  # 0.5 us less than from a shape
+        t = _empty_like(like, dtype=dtype)
+    else:
+        t = like.new_empty(shape, dtype=dtype)
+    if stream is not None and raw != _raw_stream(index):
         t.record_stream(_torch.cuda.ExternalStream(raw, device=index))
     return t
 
@@ -192,13 +195,13 @@ def gdn_prefill(q, k, v, g, beta, cu_seqlens, S, slot=None, has_state=None, q_sc
     seq_status = _dense(seq_status, "seq_status", (n,), index, i32)
     raw = _stream(stream, index)
     if o is None:
-        o = _empty(q, v.shape, o_dtype, index, raw)
+        o = _empty(v, v.shape, o_dtype, index, raw, stream)
         op = o.data_ptr()
     else:
         op = _dense(o, "o", v.shape, index, o_dtype)
     if workspace is None:
         need = _lib.gdn_prefill_workspace_bytes(dims)
-        workspace = _empty(q, (need,), _torch.uint8, index, raw)
+        workspace = _empty(q, (need,), _torch.uint8, index, raw, stream)
     _run(index, _lib.gdn_prefill, dims, qp, kp, vp, gp, bp, cu, slot, has_state, sp, op, seq_status,
          workspace.data_ptr(), workspace.numel(), raw)
     return o
@@ -223,7 +226,7 @@ def gdn_decode(q, k, v, g, beta, S, slot=None, q_scale=1.0, qk_l2norm=False, l2_
     slot = _dense(slot, "slot", (q.shape[0],), index, _torch.int32)
     raw = _stream(stream, index)
     if o is None:
-        o = _empty(q, v.shape, o_dtype, index, raw)
+        o = _empty(v, v.shape, o_dtype, index, raw, stream)
         op = o.data_ptr()
     else:
         op = _dense(o, "o", v.shape, index, o_dtype)
@@ -250,11 +253,11 @@ def gdn_add_norm(x, residual, weight, scale=1.0, chan_scale=None, post_weight=No
     f32 = _torch.float32
     raw = _stream(stream, index)
     if h is None:
-        h, hs = _empty(x, shape, h_dtype, index, raw), D
+        h, hs = _empty(x, shape, h_dtype, index, raw, stream), D
     else:
         hs = _rows(h, "h", shape, index, h_dtype)
     if y is None:
-        y, ys = _empty(x, shape, y_dtype or _torch.bfloat16, index, raw), D
+        y, ys = _empty(x, shape, y_dtype or _torch.bfloat16, index, raw, stream), D
     else:
         ys = _rows(y, "y", shape, index, y_dtype)
     dims = AddNormDims(T, D, _code(x.dtype, "x"), _code(h_dtype, "residual"), _code(y.dtype, "y"), scale, eps,
@@ -277,7 +280,7 @@ def gdn_gated_norm(o, z, weight, eps=1e-6, gate="silu", y=None, y_dtype=None, st
     zs = _rows(z, "z", shape, index)
     raw = _stream(stream, index)
     if y is None:
-        y, ys = _empty(o, shape, y_dtype or _torch.bfloat16, index, raw), H * d
+        y, ys = _empty(o, shape, y_dtype or _torch.bfloat16, index, raw, stream), H * d
     else:
         ys = _rows(y, "y", shape, index, y_dtype)
     if gate not in ("silu", "sigmoid"):
@@ -309,7 +312,7 @@ def gdn_linear(x, w, bias=None, act="none", residual=None, scale=1.0, y=None, y_
         rs, rp, r_code = _rows(residual, "residual", (M, N), index), residual.data_ptr(), _code(residual.dtype, "residual")
     raw = _stream(stream, index)
     if y is None:
-        y, ys = _empty(x, (M, N), y_dtype or bf16, index, raw), N
+        y, ys = _empty(x if residual is None else residual, (M, N), y_dtype or bf16, index, raw, stream), N
     else:
         ys = _rows(y, "y", (M, N), index, y_dtype)
     act_code = ACTS.get(act)
@@ -319,7 +322,7 @@ def gdn_linear(x, w, bias=None, act="none", residual=None, scale=1.0, y=None, y_
     if workspace is None:
         need = _lib.gdn_linear_workspace_bytes(dims)
         if need:
-            workspace = _empty(x, (need,), _torch.uint8, index, raw)
+            workspace = _empty(x, (need,), _torch.uint8, index, raw, stream)
     wp, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _run(index, _lib.gdn_linear, dims, x.data_ptr(), w.data_ptr(), _dense(bias, "bias", (N,), index, _torch.float32), rp,
          y.data_ptr(), wp, nbytes, raw)
