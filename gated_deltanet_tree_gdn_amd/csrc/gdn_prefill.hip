@@ -20,17 +20,18 @@
 // T / 64 + B slots).
 //
 // Precision: q, k and v are exact bf16 operands.  fp32 operands are split
-// into bf16 parts: S, R = V - gamma K S^T, the off-diagonal part of T, and M
-// into two (about 17 bits; a third part would be half as much again of LDS, and
-// of T and M in memory), the decayed U that is accumulated into the state into
-// three (24 bits), since its error stays.  The diagonal of T acts in fp32.
+// into bf16 parts: S, the off-diagonal part of T, and M into two (about 17 bits; a
+// third part would be half as much again of LDS, and of T and M in memory), R = V -
+// gamma K S^T and the decayed U, whose errors stay in the state, into three (24
+// bits; for R 1.5 % of the time and a quarter of the state's error).  The diagonal
+// of T acts in fp32.
 // Sums, states, T and the decay are fp32, G is fp64 (a difference G_i - G_j stays
 // exact to fp32 however far the chunk has decayed).  Relative error after 2000
-// tokens: states 1.2e-6, fp32 outputs 3.9e-6 (2e-7 and 3e-7 with fp32
+// tokens: states 1.0e-6, fp32 outputs 3.8e-6 (2e-7 and 3e-7 with fp32
 // throughout, 1.7e-3 for an output rounded to bf16).
 //
 // Measured, H_k 16, H_v 32, d 128, bf16, states not resumed: one sequence of
-// 16384 tokens 437 us (prep 87, chain 350), 13 of 7919 tokens in all 205 us.
+// 16384 tokens 440 us (prep 87, chain 353), 13 of 7919 tokens in all 207 us.
 // The inputs, outputs and states are 404 MB and 169 MB; at the rate of a copy
 // (5.2 TB/s) that is 78 and 33 us.
 
@@ -493,7 +494,7 @@ struct ChainLds {
     uint4 K[2][4][16 * DK / 8];    // rows of this chunk's K and the next one's by token tile, pieces permuted
     uint4 Q[4][16 * DK / 8];       // rows of Q, each tile read by its own wavefront only
     uint4 S[DK / 32][2][64];       // state: hi, lo
-    uint4 R[2][2][64];             // R: hi, lo
+    uint4 R[2][3][64];             // R: three parts
     uint4 D[2][3][64];             // decayed U: three parts
     f32x4 U[4][64];                // U in fp32, rows of token tile [i] as accumulated
     uint4 V[kC * 2];               // the chunk's rows of the slice's values
@@ -815,30 +816,33 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     }
                 l.badrow[w][lane] = m;
             }
-            uint2 r_hi, r_lo;
-            split4(R, r_hi, r_lo);
+            uint2 r_hi, r_mid, r_lo;
+            split4(R, r_hi, r_mid, r_lo);
             reinterpret_cast<uint2*>(&l.R[w >> 1][0][lane])[w & 1] = r_hi;
-            reinterpret_cast<uint2*>(&l.R[w >> 1][1][lane])[w & 1] = r_lo;
+            reinterpret_cast<uint2*>(&l.R[w >> 1][1][lane])[w & 1] = r_mid;
+            reinterpret_cast<uint2*>(&l.R[w >> 1][2][lane])[w & 1] = r_lo;
             loads_barrier<kAnyLoads>();
 
             // U = beta R + T R below the diagonal
             const f32x4 be = *reinterpret_cast<const f32x4*>(&l.sc[kC + 16 * w + 4 * g]);
             const f32x4 cu = *reinterpret_cast<const f32x4*>(&l.sc[2 * kC + 16 * w + 4 * g]);
             const float gam = l.sc[4 * kC];
-            bf16x8 rh[kSteps], rl[kSteps];
+            bf16x8 rh[kSteps], rm[kSteps], rl[kSteps];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][lane]);
-                rl[s] = __builtin_bit_cast(bf16x8, l.R[s][1][lane]);
+                rm[s] = __builtin_bit_cast(bf16x8, l.R[s][1][lane]);
+                rl[s] = __builtin_bit_cast(bf16x8, l.R[s][2][lane]);
             }
             f32x4 u0 = be * R, u1 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
-                u1 = mfma(tl, rl[s], u1);
+                u1 = mfma(th, rl[s], u1);
+                u1 = mfma(tl, rm[s], u1);
                 u1 = mfma(tl, rh[s], u1);
                 u0 = mfma(th, rh[s], u0);
-                u1 = mfma(th, rl[s], u1);
+                u1 = mfma(th, rm[s], u1);
             }
             const uint32_t mark = l.marks[lane & 3];
             u0 += u1;
