@@ -63,10 +63,13 @@ __device__ __forceinline__ void store_row(float* row, int l, const float (&x)[E]
 
 template <int E>
 __device__ __forceinline__ float dot(const float (&a)[E], const float (&b)[E]) {
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s0 = a[0] * b[0], s1 = a[1] * b[1];
 #pragma unroll
-    for (int j = 0; j < E; ++j) s[j & 3] += a[j] * b[j];
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    for (int j = 2; j < E; j += 2) {
+        s0 += a[j] * b[j];
+        s1 += a[j + 1] * b[j + 1];
+    }
+    return s0 + s1;
 }
 
 // 1 / sqrt(x): the hardware's estimate (1 ulp) after one Newton step.
@@ -96,7 +99,8 @@ __device__ __forceinline__ QkScale qk_scale(const gdn_seq_dims& d, const float (
 template <int L, int E>
 __device__ __forceinline__ float delta_step(float (&S)[E], const float (&k)[E], const float (&q)[E], const QkScale& f,
                                             float g, float beta, float v) {
-    const float alpha = expf(g);
+    // the hardware's 2^x, off by |g| 2^-24 and an ulp: least where the state stays
+    const float alpha = __builtin_amdgcn_exp2f(g * 1.44269504f);
     const float sk = lane_sum<L>(dot(S, k)), sq = lane_sum<L>(dot(S, q));
     const float u = beta * (v - alpha * (f.rk * sk)) * f.rk;
 #pragma unroll
@@ -172,13 +176,23 @@ __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
     const T* v = static_cast<const T*>(a.v) + int64_t(h) * d.d_v + row;
     if (t < end) {
         Token<T, E> tok[kAhead];
-        auto load = [&](Token<T, E>& x, int64_t n) {
-            n = n < end ? n : end - 1;
-            load_pieces<L>(q + n * d.q_stride, l, x.q);
-            load_pieces<L>(k + n * d.k_stride, l, x.k);
-            x.v = v[n * d.v_stride];
-            x.g = a.g[n * d.H_v + h];
-            x.beta = a.beta[n * d.H_v + h];
+        // the next token to load: running addresses, as products of 64-bit strides
+        // would be a third of a token's instructions
+        const T *qn = q + t * d.q_stride, *kn = k + t * d.k_stride, *vn = v + t * d.v_stride;
+        const float *gn = a.g + t * d.H_v + h, *bn = a.beta + t * d.H_v + h;
+        int64_t left = end - t;  // tokens from it on
+        auto load = [&](Token<T, E>& x) {
+            load_pieces<L>(qn, l, x.q);
+            load_pieces<L>(kn, l, x.k);
+            x.v = *vn;
+            x.g = *gn;
+            x.beta = *bn;
+            const bool more = --left > 0;
+            qn += more ? d.q_stride : 0;
+            kn += more ? d.k_stride : 0;
+            vn += more ? d.v_stride : 0;
+            gn += more ? d.H_v : 0;
+            bn += more ? d.H_v : 0;
         };
         auto apply = [&](const Token<T, E>& x) {
             float qc[E], kc[E];
@@ -187,7 +201,7 @@ __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
             return delta_step<L>(s, kc, qc, qk_scale<L>(d, qc, kc), x.g, x.beta, to_float(x.v));
         };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(tok[i], t + i);
+        for (int i = 0; i < kAhead; ++i) load(tok[i]);
         // lane i of a row stores token t + i
         for (; t + kAhead <= end; t += kAhead) {
             float o = 0.0f;
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
             for (int i = 0; i < kAhead; ++i) {
                 const float x = apply(tok[i]);
                 o = l == i ? x : o;
-                load(tok[i], t + kAhead + i);
+                load(tok[i]);
             }
             if (l < kAhead) store1(a.o, d.o_dtype, ((t + l) * d.H_v + h) * d.d_v + row, o);
         }
