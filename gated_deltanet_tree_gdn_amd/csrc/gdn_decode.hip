@@ -148,6 +148,8 @@ struct Token {
 // rows per wavefront.  A token takes less time than its loads, so the next kAhead
 // are in flight; past the end the last token is loaded again, since a load
 // behind a branch would be waited for at the branch's end.
+// Bound by instructions, some 80 per token with 4 elements of a row per lane
+// (d 64): 0.24 us per token of the longest sequence.
 constexpr int kAhead = 4;
 template <typename T, int DK, int L>
 __global__ void __launch_bounds__(256) walk_kernel(SeqArgs a) {
@@ -249,8 +251,8 @@ static void launch_walk(const SeqArgs& a, hipStream_t stream) {
 
 // 16 lanes to a row halve a wavefront's work per token, which is what a walk
 // waits for until the wavefronts crowd each other.  16 and 8 lanes, fp32, H_v
-// 32, d 128: 1500 tokens in 1 sequence 632 and 775 us, 500 in 8 147 and 172 us,
-// 1500 in 32 343 and 304 us.
+// 32, d 128: 1500 tokens in 1 sequence 495 and 647 us, 500 in 8 120 and 161 us,
+// 1500 in 32 294 and 271 us.
 hipError_t launch_prefill_walk(const SeqArgs& a, hipStream_t stream) {
     if (int64_t(a.d.B) * a.d.H_v * a.d.d_v <= 32768)
         launch_walk<16>(a, stream);

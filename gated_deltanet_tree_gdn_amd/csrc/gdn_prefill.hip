@@ -910,9 +910,9 @@ hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
 // fp32 operands would need three parts each, so those are walked token by
 // token, as are sequences of 8 tokens on average, which fill a small part of
 // their chunks.  (The lengths themselves are on the device.)  Walk and chunks,
-// H_v 32, d 128: B 1, T 8: 13 and 18 us; B 8, T 72: 28 and 37 us; B 32, T 264:
-// 79 and 121 us; B 120, T 500: 190 and 317 us; but B 1, T 64: 31 and 17 us, and
-// B 32, T 1000: 232 and 131 us.
+// H_v 32, d 128: B 1, T 8: 14 and 18 us; B 8, T 72: 25 and 37 us; B 32, T 264:
+// 73 and 114 us; B 120, T 500: 182 and 317 us; but B 1, T 64: 25 and 18 us, and
+// B 32, T 1000: 209 and 123 us.
 bool use_chunks(const gdn_seq_dims& d) { return d.qkv_dtype == GDN_BF16 && d.T > 8 * int64_t(d.B); }
 
 }  // namespace
