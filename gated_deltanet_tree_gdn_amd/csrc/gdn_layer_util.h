@@ -12,6 +12,14 @@ namespace gdn {
 
 __host__ __device__ constexpr int dtype_size(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
+// A grid of n workgroups or more, in rows of 2^20: one dimension may not have
+// 2^32 threads.  Kernels number workgroups by block_id() and drop those from n on.
+inline dim3 grid_of(int64_t n) {
+    const int64_t row = n < (1 << 20) ? n : 1 << 20;
+    return dim3(static_cast<unsigned>(row), static_cast<unsigned>((n + row - 1) / row));
+}
+__device__ __forceinline__ int64_t block_id() { return int64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 

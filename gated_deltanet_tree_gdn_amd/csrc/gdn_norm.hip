@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
     __shared__ float part[32];
     const gdn_add_norm_dims& d = a.d;
     const int nvec = (d.D + 7) >> 3;
-    const int64_t t = blockIdx.x;
+    const int64_t t = block_id();
+    if (t >= d.T) return;
     float x[VPT][8], r[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -175,11 +176,11 @@ hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream) {
     auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 63) / 64 * 64; };
     const bool tail = d.D % 8 != 0;
     if (threads(1) <= 512)
-        tail ? add_norm_kernel<1, true><<<d.T, threads(1), 0, stream>>>(a)
-             : add_norm_kernel<1, false><<<d.T, threads(1), 0, stream>>>(a);
+        tail ? add_norm_kernel<1, true><<<grid_of(d.T), threads(1), 0, stream>>>(a)
+             : add_norm_kernel<1, false><<<grid_of(d.T), threads(1), 0, stream>>>(a);
     else
-        tail ? add_norm_kernel<2, true><<<d.T, threads(2), 0, stream>>>(a)
-             : add_norm_kernel<2, false><<<d.T, threads(2), 0, stream>>>(a);
+        tail ? add_norm_kernel<2, true><<<grid_of(d.T), threads(2), 0, stream>>>(a)
+             : add_norm_kernel<2, false><<<grid_of(d.T), threads(2), 0, stream>>>(a);
     return hipGetLastError();
 }
 

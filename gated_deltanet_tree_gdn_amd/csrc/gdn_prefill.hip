@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
     // The key heads of a slot run on one XCD one after the other: rows of g and
     // beta hold all heads, so its L2 reads them once.
-    const int j8 = blockIdx.x >> 3, slot = j8 / d.H_k * 8 + (blockIdx.x & 7), hk = j8 % d.H_k;
+    const int id = int(block_id()), j8 = id >> 3, slot = j8 / d.H_k * 8 + (id & 7), hk = j8 % d.H_k;
     if (slot >= c.slots) return;
     const int b = find_seq(a, slot);
     const Range seq = seq_range(a, b);
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     // (sequence, key head) are numbered onto one XCD, whose L2 then serves
     // their common K, Q, K^T, T and M.
     const int group = d.H_v / d.H_k, slices = d.d_v / 16, per = group * slices;
-    const int j8 = blockIdx.x >> 3, item = (blockIdx.x & 7) + 8 * (j8 / per), part = j8 % per;
+    const int id = int(block_id()), j8 = id >> 3, item = (id & 7) + 8 * (j8 / per), part = j8 % per;
     if (item >= d.B * d.H_k) return;
     const int b = longest_seq(a, item / d.H_k), hk = item % d.H_k, h = hk * group + part / slices;
     const int v0 = part % slices * 16;
@@ -901,9 +901,9 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 template <int DK>
 hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
     const gdn_seq_dims& d = c.s.d;
-    prep_kernel<DK><<<(c.slots + 7) / 8 * 8 * d.H_k, 256, 0, stream>>>(c);
+    prep_kernel<DK><<<grid_of(int64_t(c.slots + 7) / 8 * 8 * d.H_k), 256, 0, stream>>>(c);
     const int items8 = (d.B * d.H_k + 7) / 8 * 8, per16 = d.H_v / d.H_k * (d.d_v / 16);
-    chain_kernel<DK><<<items8 * per16, 512, 0, stream>>>(c);
+    chain_kernel<DK><<<grid_of(int64_t(items8) * per16), 512, 0, stream>>>(c);
     return hipGetLastError();
 }
 

@@ -150,3 +150,29 @@ def test_linear_ends_of_k(M, N, K):
     y2 = gdn.gdn_linear(x, w, y_dtype=F32)
     assert torch.isinf(y2[3]).all()
     assert torch.equal(y2[:3], y[:3]) and torch.equal(y2[4:], y[4:])
+
+
+def test_more_workgroups_than_one_grid_dimension_holds():
+    """More than 2^20 rows, and more than 2^20 workgroups of the chunked delta rule: sequences of no tokens beside a few."""
+    T, D = (1 << 20) + 3, 8
+    x = torch.randn(T, D, device="cuda")
+    y, _ = gdn.gdn_add_norm(x, None, torch.ones(D, device="cuda"), y_dtype=F32)
+    check(y[-5:], rms(x[-5:].cpu().double()), FP32_TOL, "the last rows")
+    check(y[(1 << 20) - 2:(1 << 20) + 2], rms(x[(1 << 20) - 2:(1 << 20) + 2].cpu().double()), FP32_TOL, "around 2^20")
+
+    B, H = 20000, 16
+    n = 8 * B + 64
+    d = make(200, 1, H, 64, 64, slots=2, seed=2)
+    far = [B - 3, B - 1]
+    q, k, v, g, beta = (torch.zeros(n, *d[a].shape[1:], dtype=d[a].dtype, device="cuda") for a in ("q", "k", "v", "g", "beta"))
+    cu = torch.zeros(B + 1, dtype=torch.int32)
+    cu[far[0] + 1:] += 120
+    cu[far[1] + 1:] += 80
+    for t, a in ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (beta, "beta")):
+        t[:200] = d[a]
+    slot = torch.full((B,), -1, dtype=torch.int32)
+    slot[far] = torch.tensor([0, 1], dtype=torch.int32)
+    S = d["S"].clone()
+    o = gdn.gdn_prefill(q, k, v, g, beta, cu.cuda(), S, slot=slot.cuda(), o_dtype=F32)
+    want, S2 = run_prefill(d, [120, 80])
+    assert torch.equal(o[:200], want) and torch.equal(S, S2)
