@@ -19,19 +19,20 @@
 // leaves every sequence room without a prefix sum over lengths (at most
 // T / 64 + B slots).
 //
-// Precision: q, k and v are exact bf16 operands.  fp32 operands are split
-// into bf16 parts: S, the off-diagonal part of T, and M into two (about 17 bits; a
-// third part would be half as much again of LDS, and of T and M in memory), R = V -
-// gamma K S^T and the decayed U, whose errors stay in the state, into three (24
-// bits; for R 1.5 % of the time and a quarter of the state's error).  The diagonal
-// of T acts in fp32.
-// Sums, states, T and the decay are fp32, G is fp64 (a difference G_i - G_j stays
-// exact to fp32 however far the chunk has decayed).  Relative error after 2000
-// tokens: states 1.0e-6, fp32 outputs 3.8e-6 (2e-7 and 3e-7 with fp32
-// throughout, 1.7e-3 for an output rounded to bf16).
+// Precision: q, k and v are exact bf16 operands.  Every fp32 operand (S, R = V -
+// gamma K S^T, the off-diagonal part of T, U, the decayed U, M) is split into three
+// bf16 parts, 24 bits, and of a product of two such operands the six products of
+// parts above 2^-24 of it are taken.  The diagonal of T acts in fp32.  Two parts of
+// any of them cost 10 to 200 times the error of fp32 where keys reach |k|^2 = 2 and
+// nothing decays, and 20 times in outputs of ordinary inputs.
+// Sums, states and the decay are fp32, G is fp64 (a difference G_i - G_j stays exact
+// to fp32 however far the chunk has decayed), and so are the products that form T:
+// near |k|^2 = 2 their terms are larger than T.  Relative error after 2000 tokens:
+// states and fp32 outputs 2e-7 (3e-7 token by token in fp32); with |k|^2 = 2, beta
+// = 1 and no decay up to 6e-6 (keys in a plane; 1e-6 token by token).
 //
 // Measured, H_k 16, H_v 32, d 128, bf16, half of the 13 states resumed: one of
-// 16384 tokens 440 us (prep 87, chain 353), 13 of 7919 tokens in all 207 us.
+// 16384 tokens 540 us (prep 98, chain 442), 13 of 7919 tokens in all 253 us.
 // The inputs, outputs and states are 409 MB and 238 MB; at the rate of a copy
 // (5.2 TB/s) that is 79 and 46 us.
 
@@ -47,7 +48,9 @@ namespace {
 constexpr int kC = 64;  // tokens per chunk
 
 // What prep_kernel hands to chain_kernel, all in the order in which a
-// wavefront's lanes read it (16 bytes per lane, 1 KiB per fragment).  Tokens
+// wavefront's lanes read it (16 bytes per lane, 1 KiB per fragment): T in parts, M
+// in fp32 (the outputs have the time to split it, 20 us less of 560 for the long
+// prompt; the chain has not, 30 us more).  Tokens
 // of a 32-token step sit at k-slot j of lane group g as token
 // 16 (j / 4) + 4 g + j % 4, the order in which accumulators hold rows, so that
 // a product's result is the next product's operand without moving lanes.
@@ -57,6 +60,8 @@ struct PrepLayout {
 constexpr int kScalars = 4 * kC + 4;  // floats per (slot, head), whole 16-byte pieces
 // T and M: the (row tile, 32-token step) pairs that reach the lower triangle.
 constexpr int kPairs = 6;
+// bf16 parts of an fp32 operand.
+constexpr int kParts = 3;
 __host__ __device__ constexpr int pair_at(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
 
 __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
@@ -64,7 +69,7 @@ __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
     const size_t slots = size_t(d.T) / kC + d.B + 1, heads = slots * d.H_v;
     PrepLayout l;
     l.t = 0;
-    l.m = l.t + heads * kPairs * 2 * 1024;
+    l.m = l.t + heads * kPairs * kParts * 1024;
     l.sc = l.m + heads * kPairs * 2 * 1024;
     l.total = (l.sc + heads * kScalars * sizeof(float) + 255) & ~size_t(255);
     return l;
@@ -128,24 +133,38 @@ __device__ __forceinline__ int longest_seq(const SeqArgs& a, int r) {
     return __builtin_ctzll(__ballot(lane < B && rank == r));
 }
 
-__device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+// Accumulator r of lane group g is row 4 r + g of the product; in the other MFMAs
+// here it is row 4 g + r.  The operand whose rows those are takes them in the order
+// of row_of (column by column of a 4 x 4 arrangement), so that both agree.
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f64x4 mfma_f64(double a, double b, const f64x4& c) {
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ int row_of(int i) { return 4 * (i & 3) + (i >> 2); }
 
-// Four accumulators as packed bf16 parts, x = hi + lo or hi + mid + lo, each
+// Four accumulators as packed bf16 parts, x = part[0] + part[1] + part[2], each
 // rounded to nearest; in pairs, as the conversions come.
 __device__ __forceinline__ uint2 take4(f32x4& x) {  // the leading part; x keeps the rest
     const uint2 part = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     x -= f32x4{bf16_lo(part.x), bf16_hi(part.x), bf16_lo(part.y), bf16_hi(part.y)};
     return part;
 }
-__device__ __forceinline__ void split4(f32x4 x, uint2& hi, uint2& lo) {
-    hi = take4(x);
-    lo = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+__device__ __forceinline__ void split4(f32x4 x, uint2 (&part)[kParts]) {
+    part[0] = take4(x);
+    part[1] = take4(x);
+    part[2] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
-__device__ __forceinline__ void split4(f32x4 x, uint2& hi, uint2& mid, uint2& lo) {
-    hi = take4(x);
-    split4(x, mid, lo);
+__device__ __forceinline__ uint4 join(const uint2& a, const uint2& b) { return make_uint4(a.x, a.y, b.x, b.y); }
+
+// Adds a b of operands in three parts: the six products above 2^-24 of it, by
+// size into three sums.
+__device__ __forceinline__ void mfma_parts(const bf16x8 (&a)[kParts], const bf16x8 (&b)[kParts], f32x4 (&sum)[kParts]) {
+    sum[2] = mfma(a[2], b[0], sum[2]);
+    sum[1] = mfma(a[1], b[0], sum[1]);
+    sum[0] = mfma(a[0], b[0], sum[0]);
+    sum[2] = mfma(a[1], b[1], sum[2]);
+    sum[1] = mfma(a[0], b[1], sum[1]);
+    sum[2] = mfma(a[0], b[2], sum[2]);
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
@@ -171,10 +190,10 @@ __device__ __forceinline__ float exp_diff(double hi, double lo) {
 
 // Four wavefronts: the Gram matrices on MFMA once per key head; then two value
 // heads at a time, a wavefront each half of T's row blocks: 16 x 16 diagonal
-// blocks by substitution (a column per lane), the blocks below them by fp32 MFMA
-// (bf16 parts of the inverse would lose what the substitution kept).  Bound by
-// memory: it writes T and M, 768 bytes per (token, value head), and reads q and k;
-// 16384 tokens, H_v 32: 336 MB in 87 us, 3.9 TB/s.
+// blocks by substitution (a column per lane), the blocks below them by fp64 MFMA
+// (in fp32 their rounding is most of the error where |k|^2 is 2).  Bound by memory: it
+// writes T and M, 480 bytes per (token, value head), and reads q and k; 16384
+// tokens, H_v 32: 387 MB in 98 us, 3.9 TB/s.
 template <int DK>
 __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     constexpr int KS = DK / 32;
@@ -355,43 +374,45 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
             // Row block i of T, transposed: X[j] = T_ij^T = -T_jj^T sum_m A_mj^T T_im^T
             // as accumulators (column = row of block i, rows = columns of block j);
             // then T diag(beta) without its diagonal as fragments of tile i's rows.
-            uint4* tp = c.t + sh * kPairs * 2 * 64;
+            uint4* tp = c.t + sh * kPairs * kParts * 64;
             auto row_block = [&](auto ii) {
                 constexpr int i = ii.value;
-                f32x4 X[i + 1];
-                X[i] = *reinterpret_cast<const f32x4*>(&tri[i][col][4 * g]);
+                f64x4 X[i + 1];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[i][r] = tri[i][col][4 * g + r];
+                const int pc = row_of(col);
 #pragma unroll
                 for (int j = i - 1; j >= 0; --j) {
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, out = acc;
-                    const double Gj = G[16 * j + col];
+                    f64x4 acc = {0.0, 0.0, 0.0, 0.0}, out = acc;
+                    const double Gj = G[16 * j + pc];
 #pragma unroll
                     for (int m = j + 1; m <= i; ++m)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int tm = 16 * m + 4 * g + r;
-                            acc = mfma_f32(be[tm] * exp_diff(G[tm], Gj) * gram[tm * kGramLd + 16 * j + col], X[m][r], acc);
+                            acc = mfma_f64(be[tm] * exp_diff(G[tm], Gj) * gram[tm * kGramLd + 16 * j + pc], X[m][r], acc);
                         }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) out = mfma_f32(-tri[j][4 * g + r][col], acc[r], out);
+                    for (int r = 0; r < 4; ++r) out = mfma_f64(-tri[j][4 * g + r][pc], acc[r], out);
                     X[j] = out;
                 }
 #pragma unroll
                 for (int s = 0; s <= i / 2; ++s) {
-                    uint2 hi[2], lo[2];
+                    uint2 x[2][kParts];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int jt = 2 * s + half;
                         const f32x4 bj = *reinterpret_cast<const f32x4*>(&be[16 * jt + 4 * g]);
                         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if (jt < i) v = X[jt < i ? jt : i] * bj;
-                        if (jt == i)
+                        if (jt <= i)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) v[r] = 4 * g + r < col ? X[i][r] * bj[r] : 0.0f;
-                        split4(v, hi[half], lo[half]);
+                            for (int r = 0; r < 4; ++r)
+                                v[r] = jt < i || 4 * g + r < col ? static_cast<float>(X[jt < i ? jt : i][r]) * bj[r] : 0.0f;
+                        split4(v, x[half]);
                     }
-                    uint4* p = tp + pair_at(i, s) * 2 * 64 + lane;
-                    p[0] = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
-                    p[64] = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
+                    uint4* p = tp + pair_at(i, s) * kParts * 64 + lane;
+#pragma unroll
+                    for (int q = 0; q < kParts; ++q) p[64 * q] = join(x[0][q], x[1][q]);
                 }
             };
             if (part == 0) {
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (2 * s > w) continue;
-                uint2 hi[2], lo[2];
+                uint4* p = mp + pair_at(w, s) * 2 * 64 + lane;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int jt = 2 * s + half;
@@ -420,11 +441,8 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
                         const int tok = 16 * jt + 4 * g + r;
                         v[r] = tok <= row ? exp_diff(Gi, gcum[hh][tok]) * qk[jt][r] : 0.0f;
                     }
-                    split4(v, hi[half], lo[half]);
+                    p[64 * half] = __builtin_bit_cast(uint4, v);
                 }
-                uint4* p = mp + pair_at(w, s) * 2 * 64 + lane;
-                p[0] = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
-                p[64] = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
             }
         }
         __syncthreads();
@@ -493,9 +511,9 @@ template <int DK>
 struct ChainLds {
     uint4 K[2][4][16 * DK / 8];    // rows of this chunk's K and the next one's by token tile, pieces permuted
     uint4 Q[4][16 * DK / 8];       // rows of Q, each tile read by its own wavefront only
-    uint4 S[DK / 32][2][64];       // state: hi, lo
-    uint4 R[2][3][64];             // R: three parts
-    uint4 D[2][3][64];             // decayed U: three parts
+    uint4 S[DK / 32][kParts][64];  // state
+    uint4 R[2][kParts][64];        // R
+    uint4 D[2][kParts][64];        // decayed U
     f32x4 U[4][64];                // U in fp32, rows of token tile [i] as accumulated
     uint4 V[kC * 2];               // the chunk's rows of the slice's values
     float sc[kScalars];            // its scalars
@@ -571,7 +589,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         int64_t o_at = (seq.start * d.H_v + h) * d.d_v + v0;
         auto run = [&](auto steps_of_tile) {
             constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
-            uint4 mf[kSteps][2], qf[KS];
+            uint4 mf[2 * kSteps], qf[KS];
             TileRows<DK> qr, kr;
             qr.rows(d.q_stride, seq.len, w, lane);
             kr.rows(d.k_stride, seq.len, w, lane);
@@ -590,7 +608,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             };
             auto load_m = [&]() {
 #pragma unroll
-                for (int i = 0; i < 2 * kSteps; ++i) mf[i >> 1][i & 1] = load_at<uint4>(mp + i * 64, lane * 16);
+                for (int i = 0; i < 2 * kSteps; ++i) mf[i] = load_at<uint4>(mp + i * 64, lane * 16);
                 mp += m_step;
             };
             load_k(seq.len, 0);
@@ -628,36 +646,36 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                 if (ch > 0) store(kC);
                 loads_barrier<kAnyLoads>();  // R written
                 const float cq = l.sc[3 * kC + 16 * w + col];
-                bf16x8 sh[KS], sl[KS];
+                f32x4 Q[kParts] = {};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][lane]);
-                    sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][lane]);
-                }
-                f32x4 Qh = {0.0f, 0.0f, 0.0f, 0.0f}, Ql = Qh;
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    Qh = mfma(sh[s], __builtin_bit_cast(bf16x8, qf[s]), Qh);
-                    Ql = mfma(sl[s], __builtin_bit_cast(bf16x8, qf[s]), Ql);
-                }
-                O = cq * (Qh + Ql);
+                    for (int p = 0; p < kParts; ++p)
+                        Q[p] = mfma(__builtin_bit_cast(bf16x8, l.S[s][p][lane]), __builtin_bit_cast(bf16x8, qf[s]), Q[p]);
+                O = cq * (Q[0] + (Q[1] + Q[2]));
                 loads_barrier<kAnyLoads>();  // U written
                 const uint32_t mark = l.marks[lane & 3];
                 f32x4 u[2 * kSteps];
 #pragma unroll
                 for (int i = 0; i < 2 * kSteps; ++i) u[i] = l.U[i][lane];
+                f32x4 sum[kParts] = {O};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    uint2 h0, l0, h1, l1;
-                    split4(u[2 * s], h0, l0);
-                    split4(u[2 * s + 1], h1, l1);
-                    const bf16x8 uh = __builtin_bit_cast(bf16x8, make_uint4(h0.x, h0.y, h1.x, h1.y));
-                    const bf16x8 ul = __builtin_bit_cast(bf16x8, make_uint4(l0.x, l0.y, l1.x, l1.y));
-                    const bf16x8 mh = __builtin_bit_cast(bf16x8, mf[s][0]), ml = __builtin_bit_cast(bf16x8, mf[s][1]);
-                    O = mfma(uh, mh, O);
-                    O = mfma(ul, mh, O);
-                    O = mfma(uh, ml, O);
+                    uint2 x0[kParts], x1[kParts];
+                    split4(u[2 * s], x0);
+                    split4(u[2 * s + 1], x1);
+                    uint2 m0[kParts], m1[kParts];
+                    split4(__builtin_bit_cast(f32x4, mf[2 * s]), m0);
+                    split4(__builtin_bit_cast(f32x4, mf[2 * s + 1]), m1);
+                    bf16x8 uq[kParts], mq[kParts];
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        uq[p] = __builtin_bit_cast(bf16x8, join(x0[p], x1[p]));
+                        mq[p] = __builtin_bit_cast(bf16x8, join(m0[p], m1[p]));
+                    }
+                    mfma_parts(uq, mq, sum);
                 }
+                O = sum[0] + (sum[1] + sum[2]);
                 poisoned = __ballot(mark) != 0;
                 if (poisoned) first = first_bad(l, col);
                 __builtin_amdgcn_sched_barrier(0);
@@ -691,8 +709,8 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     auto run = [&](auto steps_of_tile) {
         constexpr int kSteps = steps_of_tile.value;  // 32-token steps up to token tile w
         const uint16_t* vp = static_cast<const uint16_t*>(a.v) + seq.start * d.v_stride + int64_t(h) * d.d_v + v0;
-        const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * 2 * 64;
-        const int64_t v_step = kC * d.v_stride, t_step = int64_t(d.H_v) * kPairs * 2 * 64;
+        const uint4* tp = c.t + (sh0 * kPairs + pair_at(w, 0)) * kParts * 64;
+        const int64_t v_step = kC * d.v_stride, t_step = int64_t(d.H_v) * kPairs * kParts * 64;
         // wavefront 2 loads the scalars of every token, wavefront 3 gamma_64
         const float* xp = c.sc + sh0 * kScalars;
         const uint32_t x_off = (w == 3 ? kC : lane) * 16;
@@ -700,7 +718,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         // Each group of inputs is loaded for the next chunk (or the one after) as
         // soon as this chunk has used it, so one set of registers covers a chunk's
         // latency.  As for the outputs, no load is behind a branch.
-        uint4 tf[kSteps][2], vr, xr;
+        uint4 tf[kSteps][kParts], vr, xr;
         // V: a row of the slice is 2 pieces, wavefronts 0 and 1 hold all of them
         const int vi = w * 64 + lane;
         uint32_t v_off;
@@ -726,7 +744,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
         };
         auto load_t = [&]() {
 #pragma unroll
-            for (int i = 0; i < 2 * kSteps; ++i) tf[i >> 1][i & 1] = load_at<uint4>(tp + i * 64, lane * 16);
+            for (int i = 0; i < kParts * kSteps; ++i) tf[i / kParts][i % kParts] = load_at<uint4>(tp + i * 64, lane * 16);
             tp += t_step;
         };
         // issued in the order of the loop: a wait for one group then lets the
@@ -746,10 +764,10 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 #pragma unroll
             for (int i = 0; i < TPW; ++i) {
                 const int tau = w * TPW + i;
-                uint2 hi, lo;
-                split4(S[i], hi, lo);
-                reinterpret_cast<uint2*>(&l.S[tau >> 1][0][lane])[tau & 1] = hi;
-                reinterpret_cast<uint2*>(&l.S[tau >> 1][1][lane])[tau & 1] = lo;
+                uint2 x[kParts];
+                split4(S[i], x);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) reinterpret_cast<uint2*>(&l.S[tau >> 1][p][lane])[tau & 1] = x[p];
             }
             loads_barrier<kAnyLoads>();
 
@@ -760,18 +778,12 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
             const f32x4 cp = *reinterpret_cast<const f32x4*>(&l.sc[16 * w + 4 * g]);
             // the lane's column of rows 16 w + 4 g + r
             const uint2 v = read_tr(reinterpret_cast<const uint2*>(l.V) + (16 * w + 4 * g + (col >> 2)) * 4 + (col & 3));
-            bf16x8 sh[KS], sl[KS];
+            f32x4 P[kParts] = {};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                sh[s] = __builtin_bit_cast(bf16x8, l.S[s][0][lane]);
-                sl[s] = __builtin_bit_cast(bf16x8, l.S[s][1][lane]);
-            }
-            f32x4 Ph = {0.0f, 0.0f, 0.0f, 0.0f}, Pl = Ph;
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                Ph = mfma(__builtin_bit_cast(bf16x8, kf[s]), sh[s], Ph);
-                Pl = mfma(__builtin_bit_cast(bf16x8, kf[s]), sl[s], Pl);
-            }
+                for (int p = 0; p < kParts; ++p)
+                    P[p] = mfma(__builtin_bit_cast(bf16x8, kf[s]), __builtin_bit_cast(bf16x8, l.S[s][p][lane]), P[p]);
             // K^T of the wavefront's state rows: accumulator row rho of tile tau is
             // element 32 (tau / 2) + 8 (rho / 4) + 4 (tau % 2) + rho % 4.  In a
             // transposing read lane i of 16 names 4 elements of row i / 4 and gets
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     ktf[i][s] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
                 }
             const f32x4 vv = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-            f32x4 R = vv - cp * (Ph + Pl);
+            f32x4 R = vv - cp * (P[0] + (P[1] + P[2]));
             if (n < kC)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -816,63 +828,54 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
                     }
                 l.badrow[w][lane] = m;
             }
-            uint2 r_hi, r_mid, r_lo;
-            split4(R, r_hi, r_mid, r_lo);
-            reinterpret_cast<uint2*>(&l.R[w >> 1][0][lane])[w & 1] = r_hi;
-            reinterpret_cast<uint2*>(&l.R[w >> 1][1][lane])[w & 1] = r_mid;
-            reinterpret_cast<uint2*>(&l.R[w >> 1][2][lane])[w & 1] = r_lo;
+            uint2 x[kParts];
+            split4(R, x);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) reinterpret_cast<uint2*>(&l.R[w >> 1][p][lane])[w & 1] = x[p];
             loads_barrier<kAnyLoads>();
 
             // U = beta R + T R below the diagonal
             const f32x4 be = *reinterpret_cast<const f32x4*>(&l.sc[kC + 16 * w + 4 * g]);
             const f32x4 cu = *reinterpret_cast<const f32x4*>(&l.sc[2 * kC + 16 * w + 4 * g]);
             const float gam = l.sc[4 * kC];
-            bf16x8 rh[kSteps], rm[kSteps], rl[kSteps];
+            f32x4 sum[kParts] = {be * R};
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                rh[s] = __builtin_bit_cast(bf16x8, l.R[s][0][lane]);
-                rm[s] = __builtin_bit_cast(bf16x8, l.R[s][1][lane]);
-                rl[s] = __builtin_bit_cast(bf16x8, l.R[s][2][lane]);
-            }
-            f32x4 u0 = be * R, u1 = {0.0f, 0.0f, 0.0f, 0.0f};
+                bf16x8 tq[kParts], rq[kParts];
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const bf16x8 th = __builtin_bit_cast(bf16x8, tf[s][0]), tl = __builtin_bit_cast(bf16x8, tf[s][1]);
-                u1 = mfma(th, rl[s], u1);
-                u1 = mfma(tl, rm[s], u1);
-                u1 = mfma(tl, rh[s], u1);
-                u0 = mfma(th, rh[s], u0);
-                u1 = mfma(th, rm[s], u1);
+                for (int p = 0; p < kParts; ++p) {
+                    tq[p] = __builtin_bit_cast(bf16x8, tf[s][p]);
+                    rq[p] = __builtin_bit_cast(bf16x8, l.R[s][p][lane]);
+                }
+                mfma_parts(tq, rq, sum);
             }
             const uint32_t mark = l.marks[lane & 3];
-            u0 += u1;
-            f32x4 e = u0 * cu;
+            const f32x4 u = sum[0] + (sum[1] + sum[2]);
+            f32x4 e = u * cu;
             if (__ballot(mark)) {
                 const int first = first_bad(l, col);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     if (16 * w + 4 * g + r == first) e[r] = __builtin_nanf("");
             }
-            uint2 hi, mid, lo;
-            split4(e, hi, mid, lo);
-            reinterpret_cast<uint2*>(&l.D[w >> 1][0][lane])[w & 1] = hi;
-            reinterpret_cast<uint2*>(&l.D[w >> 1][1][lane])[w & 1] = mid;
-            reinterpret_cast<uint2*>(&l.D[w >> 1][2][lane])[w & 1] = lo;
-            l.U[w][lane] = u0;
+            split4(e, x);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) reinterpret_cast<uint2*>(&l.D[w >> 1][p][lane])[w & 1] = x[p];
+            l.U[w][lane] = u;
             loads_barrier<kAnyLoads>();
 
             // S <- gamma_64 S + K^T diag(decay) U
-            bf16x8 du[2][3];
+            bf16x8 du[2][kParts];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int p = 0; p < 3; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][lane]);
+                for (int p = 0; p < kParts; ++p) du[s][p] = __builtin_bit_cast(bf16x8, l.D[s][p][lane]);
 #pragma unroll
             for (int i = 0; i < TPW; ++i) S[i] *= gam;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
+                for (int p = 0; p < kParts; ++p)
 #pragma unroll
                     for (int i = 0; i < TPW; ++i)
                         S[i] = mfma(__builtin_bit_cast(bf16x8, ktf[i][s]), du[s][p], S[i]);
