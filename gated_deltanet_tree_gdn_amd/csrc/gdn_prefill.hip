@@ -17,7 +17,10 @@
 //
 // Chunk slots: sequence b's chunks are numbered from cu[b] / 64 + b, which
 // leaves every sequence room without a prefix sum over lengths (at most
-// T / 64 + B slots).
+// T / 64 + B slots) as long as the offsets do not decrease.  Where they do, slots
+// may belong to two sequences or be taken for another's, so no sequence uses them:
+// the first kernel's first workgroup looks at all offsets, and the second kernel then
+// walks every sequence token by token.
 //
 // Precision: q, k and v are exact bf16 operands.  Every fp32 operand (S, R = V -
 // gamma K S^T, the off-diagonal part of T, U, the decayed U, M) is split into three
@@ -55,7 +58,7 @@ constexpr int kC = 64;  // tokens per chunk
 // 16 (j / 4) + 4 g + j % 4, the order in which accumulators hold rows, so that
 // a product's result is the next product's operand without moving lanes.
 struct PrepLayout {
-    size_t t, m, sc, total;
+    size_t t, m, sc, ordered, total;
 };
 constexpr int kScalars = 4 * kC + 4;  // floats per (slot, head), whole 16-byte pieces
 // T and M: the (row tile, 32-token step) pairs that reach the lower triangle.
@@ -71,7 +74,8 @@ __host__ inline PrepLayout prep_layout(const gdn_seq_dims& d) {
     l.t = 0;
     l.m = l.t + heads * kPairs * kParts * 1024;
     l.sc = l.m + heads * kPairs * 2 * 1024;
-    l.total = (l.sc + heads * kScalars * sizeof(float) + 255) & ~size_t(255);
+    l.ordered = l.sc + heads * kScalars * sizeof(float);
+    l.total = (l.ordered + sizeof(int) + 255) & ~size_t(255);
     return l;
 }
 
@@ -81,6 +85,7 @@ struct ChunkArgs {
     uint4* m;
     float* sc;     // 4 x 64: gamma |k|^-1, beta, e^{G_64 - G} |k|^-1 and scale gamma |q|^-1 of every token (norms
                    // 1 unless asked for), the first NaN where k, g or beta is not finite; then gamma_64
+    int* ordered;  // whether cu is 0 <= cu[0] <= .. <= cu[B] <= T
     int slots;
 };
 
@@ -209,9 +214,16 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     const SeqArgs& a = c.s;
     const gdn_seq_dims& d = a.d;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+    if (block_id() == 0) {
+        bool ok = true;
+        for (int i = threadIdx.x; i <= d.B; i += 256) ok &= 0 <= a.cu[i] && a.cu[i] <= (i < d.B ? a.cu[i + 1] : d.T);
+        ok = __syncthreads_and(ok);
+        if (threadIdx.x == 0) *c.ordered = ok;
+        return;
+    }
     // The key heads of a slot run on one XCD one after the other: rows of g and
     // beta hold all heads, so its L2 reads them once.
-    const int id = int(block_id()), j8 = id >> 3, slot = j8 / d.H_k * 8 + (id & 7), hk = j8 % d.H_k;
+    const int id = int(block_id()) - 1, j8 = id >> 3, slot = j8 / d.H_k * 8 + (id & 7), hk = j8 % d.H_k;
     if (slot >= c.slots) return;
     const int b = find_seq(a, slot);
     const Range seq = seq_range(a, b);
@@ -536,6 +548,47 @@ __device__ __forceinline__ int first_bad(const ChainLds<DK>& l, int col) {
     return kC;
 }
 
+// 16 state rows of one sequence token by token, 32 lanes to a row.
+template <int DK>
+__device__ __forceinline__ void walk_rows(const SeqArgs& a, int b, int hk, int h, int v0) {
+    constexpr int E = DK / 32;
+    const gdn_seq_dims& d = a.d;
+    const int l = threadIdx.x & 31, row = v0 + (threadIdx.x >> 5);
+    const Range seq = seq_range(a, b);
+    if (a.seq_status && threadIdx.x == 0 && h == 0 && v0 == 0) a.seq_status[b] = seq.ok ? GDN_OK : GDN_ERR_SHAPE;
+    const int pool = a.slot ? a.slot[b] : b;
+    const bool keep = pool >= 0 && pool < d.n_slots;
+    const bool resume = keep && (!a.has_state || a.has_state[b] != 0);
+    float* Sp = keep ? a.S + ((int64_t(pool) * d.H_v + h) * d.d_v + row) * DK + E * l : nullptr;
+    float s[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] = resume ? Sp[e] : 0.0f;
+    for (int64_t t = seq.start; t < seq.start + seq.len; ++t) {
+        float kk = 0.0f, qq = 0.0f, kq = 0.0f, sk = 0.0f, sq = 0.0f, k[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            k[e] = load1(a.k, GDN_BF16, t * d.k_stride + int64_t(hk) * DK + E * l + e);
+            const float q = load1(a.q, GDN_BF16, t * d.q_stride + int64_t(hk) * DK + E * l + e);
+            kk += k[e] * k[e];
+            qq += q * q;
+            kq += k[e] * q;
+            sk += s[e] * k[e];
+            sq += s[e] * q;
+        }
+        const float rk = d.qk_l2norm ? 1.0f / sqrtf(lane_sum<32>(kk) + d.l2_eps) : 1.0f;
+        const float rq = d.q_scale * (d.qk_l2norm ? 1.0f / sqrtf(lane_sum<32>(qq) + d.l2_eps) : 1.0f);
+        const float alpha = expf(a.g[t * d.H_v + h]), v = load1(a.v, GDN_BF16, t * d.v_stride + int64_t(h) * d.d_v + row);
+        const float u = a.beta[t * d.H_v + h] * (v - alpha * (rk * lane_sum<32>(sk))) * rk;
+        const float o = rq * (alpha * lane_sum<32>(sq) + u * lane_sum<32>(kq));
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] = alpha * s[e] + u * k[e];
+        if (l == 0) store1(a.o, d.o_dtype, (t * d.H_v + h) * d.d_v + row, o);
+    }
+    if (keep)
+#pragma unroll
+        for (int e = 0; e < E; ++e) Sp[e] = s[e];
+}
+
 // What bounds it: a chunk takes 1.4 us (3,000 clocks) of three dependent phases,
 // each a chain of LDS reads (some 300 clocks), 6 to 12 MFMAs, the split of their
 // sums and a barrier; LDS is busy for 1,700 of the clocks, a SIMD for 640 with
@@ -572,6 +625,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
     if (item >= d.B * d.H_k) return;
     const int b = longest_seq(a, item / d.H_k), hk = item % d.H_k, h = hk * group + part / slices;
     const int v0 = part % slices * 16;
+    if (!*c.ordered) return walk_rows<DK>(a, b, hk, h, v0);
 
     const Range seq = seq_range(a, b);
     const int base = slot_base(a, b), chunks = (seq.len + kC - 1) / kC;
@@ -904,7 +958,7 @@ __global__ void __launch_bounds__(512, 2) chain_kernel(ChunkArgs c) {
 template <int DK>
 hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
     const gdn_seq_dims& d = c.s.d;
-    prep_kernel<DK><<<grid_of(int64_t(c.slots + 7) / 8 * 8 * d.H_k), 256, 0, stream>>>(c);
+    prep_kernel<DK><<<grid_of(int64_t(c.slots + 7) / 8 * 8 * d.H_k + 1), 256, 0, stream>>>(c);
     const int items8 = (d.B * d.H_k + 7) / 8 * 8, per16 = d.H_v / d.H_k * (d.d_v / 16);
     chain_kernel<DK><<<grid_of(int64_t(items8) * per16), 512, 0, stream>>>(c);
     return hipGetLastError();
@@ -930,6 +984,7 @@ hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream) {
                 reinterpret_cast<uint4*>(p + l.t),
                 reinterpret_cast<uint4*>(p + l.m),
                 reinterpret_cast<float*>(p + l.sc),
+                reinterpret_cast<int*>(p + l.ordered),
                 a.d.T / kC + a.d.B};
     return a.d.d_k == 128 ? launch_chunks<128>(c, stream) : launch_chunks<64>(c, stream);
 }

@@ -90,7 +90,9 @@ size_t gdn_prefill_workspace_bytes(const gdn_seq_dims* dims);
  *   o          [T][H_v][d_v]  o_dtype, dense
  *   seq_status [B]            int32, written, or NULL: 0, or GDN_ERR_SHAPE
  *                             for a sequence whose cu_seqlens entries are
- *                             not 0 <= start <= end <= T (it is run as empty)
+ *                             not 0 <= start <= end <= T (it is run as empty;
+ *                             the others are right all the same, if slower, and
+ *                             a token of two of them holds the output of either)
  * Tokens that no sequence owns are not written. */
 gdn_status gdn_prefill(const gdn_seq_dims* dims, const void* q, const void* k, const void* v, const float* g,
                        const float* beta, const int32_t* cu_seqlens, const int32_t* slot, const int32_t* has_state,
