@@ -266,8 +266,10 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     qq += __shfl_xor(qq, 16);
     qq += __shfl_xor(qq, 32);
     __syncthreads();
-    // a non-finite k is taken out of the chunk here and its token marked
-    const bool kbad = in && !finite(kk);
+    // a k that is not finite, or whose inverse norm is not (k = 0 without an epsilon),
+    // is taken out of the chunk here and its token marked
+    const float rk = d.qk_l2norm ? 1.0f / sqrtf(kk + d.l2_eps) : 1.0f;
+    const bool kbad = in && !(finite(kk) && finite(rk));
     if (kbad && g == 0) atomicOr(&badk[row >> 5], 1u << (row & 31));
     if (!in || kbad)
 #pragma unroll
@@ -275,7 +277,6 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     if (!in)
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = make_uint4(0, 0, 0, 0);
-    const float rk = d.qk_l2norm ? 1.0f / sqrtf((kbad ? 0.0f : kk) + d.l2_eps) : 1.0f;
     const float rq = d.q_scale * (d.qk_l2norm ? 1.0f / sqrtf(qq + d.l2_eps) : 1.0f);
     if (g == 0) {
         rks[row] = in && !kbad ? rk : 0.0f;

@@ -51,3 +51,29 @@ def test_keys_at_the_edge_of_the_range(dims, dtype):
     d["beta"].fill_(1.0)
     d["g"].zero_()
     run(d, CHUNK_TOL, f"{dims} dimensions")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["k", "q"])
+@pytest.mark.parametrize("at", [0, 20, 40, 63, 100])
+def test_zero_vectors_without_an_epsilon_stay_behind(at, name, dtype):
+    """0 / 0: no earlier token and no other key head sees it; a key reaches every later token, a query its own"""
+    d = make(130, 2, 4, seed=at, dtype=dtype)
+    args = [d[a] for a in ("q", "k", "v", "g", "beta")]
+    runs = []
+    for i in range(2):
+        S = d["S"].clone()
+        o = gdn.gdn_prefill(*args, i32(0, 130), S, qk_l2norm=True, l2_eps=0.0, o_dtype=F32)
+        runs.append((o, S))
+        d[name][at, 1] = 0.0
+    (o1, S1), (o2, S2) = runs
+    assert torch.isfinite(o1).all() and torch.isfinite(S1).all()
+    check(o2[:at], o1[:at], FP32_TOL, "tokens before it")
+    check(o2[:, :2], o1[:, :2], FP32_TOL, "the other key head")
+    check(S2[0, :2], S1[0, :2], FP32_TOL, "the other key head's state")
+    if name == "k":
+        assert torch.isnan(o2[at:, 2:]).all() and torch.isnan(S2[0, 2:]).all()
+    else:
+        assert torch.isnan(o2[at, 2:]).all()
+        check(o2[at + 1:], o1[at + 1:], FP32_TOL, "later tokens")
+        check(S2, S1, FP32_TOL, "S")
