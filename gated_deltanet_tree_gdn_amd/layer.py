@@ -127,6 +127,17 @@ def _dense(t, name, shape, index, dtype):
     return t.data_ptr()
 
 
+def _workspace(t, index):
+    """The address and size of a caller's workspace."""
+    if not isinstance(t, _Tensor):
+        raise TypeError("workspace must be a torch tensor")
+    if t.dtype != _torch.uint8:
+        raise TypeError(f"workspace must be {_torch.uint8}, got {t.dtype}")
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {index}")
+    return t.data_ptr(), t.numel()
+
+
 def _stream(stream, index):
     """The raw handle of the call's stream."""
     if stream is None:
@@ -202,8 +213,8 @@ def gdn_prefill(q, k, v, g, beta, cu_seqlens, S, slot=None, has_state=None, q_sc
     if workspace is None:
         need = _lib.gdn_prefill_workspace_bytes(dims)
         workspace = _empty(q, (need,), _torch.uint8, index, raw, stream)
-    _run(index, _lib.gdn_prefill, dims, qp, kp, vp, gp, bp, cu, slot, has_state, sp, op, seq_status,
-         workspace.data_ptr(), workspace.numel(), raw)
+    wp, nbytes = _workspace(workspace, index)
+    _run(index, _lib.gdn_prefill, dims, qp, kp, vp, gp, bp, cu, slot, has_state, sp, op, seq_status, wp, nbytes, raw)
     return o
 
 
@@ -323,7 +334,7 @@ def gdn_linear(x, w, bias=None, act="none", residual=None, scale=1.0, y=None, y_
         need = _lib.gdn_linear_workspace_bytes(dims)
         if need:
             workspace = _empty(x, (need,), _torch.uint8, index, raw, stream)
-    wp, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    wp, nbytes = (None, 0) if workspace is None else _workspace(workspace, index)
     _run(index, _lib.gdn_linear, dims, x.data_ptr(), w.data_ptr(), _dense(bias, "bias", (N,), index, _torch.float32), rp,
          y.data_ptr(), wp, nbytes, raw)
     return y
