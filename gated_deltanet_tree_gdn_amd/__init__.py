@@ -106,6 +106,15 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream, device=None):
+    """The torch stream of a stream object or a raw handle."""
+    torch = _torch()
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(stream)
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.bfloat16:

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import GDN_BF16, GDN_F32, GdnError, load_library
+from . import GDN_BF16, GDN_F32, GdnError, _torch_stream, load_library
 
 LAYER_EXPORTS = ["gdn_prefill_workspace_bytes", "gdn_prefill", "gdn_decode", "gdn_add_norm", "gdn_gated_norm",
                  "gdn_linear_workspace_bytes", "gdn_linear"]
@@ -145,16 +145,20 @@ def _stream(stream, index):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(like, shape, dtype, index, raw, stream):
-    """Memory for an output.  The allocator hands it out for the current
-    stream; where the call runs on another, it is marked as used there."""
-    if like.shape == shape and like.is_contiguous():  # 0.5 us less than from a shape
-        t = _empty_like(like, dtype=dtype)
-    else:
-        t = like.new_empty(shape, dtype=dtype)
+def _empty(like, shape, dtype, index, raw, stream, keep=True):
+    """Memory for an output, or with ``keep`` false for this call alone.  The
+    allocator hands out what is free in the order of one stream, so a call on
+    another stream than the current one allocates there; what its caller keeps
+    is marked as used on the current stream as well."""
     if stream is not None and raw != _raw_stream(index):
-        t.record_stream(_torch.cuda.ExternalStream(raw, device=index))
-    return t
+        with _torch.cuda.stream(_torch_stream(stream, index)):
+            t = like.new_empty(shape, dtype=dtype)
+        if keep:
+            t.record_stream(_torch.cuda.current_stream(index))
+        return t
+    if like.shape == shape and like.is_contiguous():  # 0.5 us less than from a shape
+        return _empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _run(index, fn, *args):
@@ -212,7 +216,7 @@ def gdn_prefill(q, k, v, g, beta, cu_seqlens, S, slot=None, has_state=None, q_sc
         op = _dense(o, "o", v.shape, index, o_dtype)
     if workspace is None:
         need = _lib.gdn_prefill_workspace_bytes(dims)
-        workspace = _empty(q, (need,), _torch.uint8, index, raw, stream)
+        workspace = _empty(q, (need,), _torch.uint8, index, raw, stream, keep=False)
     wp, nbytes = _workspace(workspace, index)
     _run(index, _lib.gdn_prefill, dims, qp, kp, vp, gp, bp, cu, slot, has_state, sp, op, seq_status, wp, nbytes, raw)
     return o
@@ -333,7 +337,7 @@ def gdn_linear(x, w, bias=None, act="none", residual=None, scale=1.0, y=None, y_
     if workspace is None:
         need = _lib.gdn_linear_workspace_bytes(dims)
         if need:
-            workspace = _empty(x, (need,), _torch.uint8, index, raw, stream)
+            workspace = _empty(x, (need,), _torch.uint8, index, raw, stream, keep=False)
     wp, nbytes = (None, 0) if workspace is None else _workspace(workspace, index)
     _run(index, _lib.gdn_linear, dims, x.data_ptr(), w.data_ptr(), _dense(bias, "bias", (N,), index, _torch.float32), rp,
          y.data_ptr(), wp, nbytes, raw)
