@@ -115,6 +115,20 @@ def _torch_stream(stream, device=None):
     return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
 
 
+def _new(shape, dtype, device, stream, make="empty"):
+    """Memory for an output.  The allocator hands out what is free in the order
+    of one stream, so a call on another stream than the current one allocates
+    there; its caller may use and free it on the current one."""
+    torch = _torch()
+    make = getattr(torch, make)
+    if stream is None or _stream(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.bfloat16:
@@ -187,7 +201,7 @@ def gdn_tree_verify(ctx: GdnContext, q, k, v, g, beta, parent, S0, o=None, strea
     _require(parent, "parent", torch.int32, (B, N))
     _require(S0, "S0", torch.float32, (B, Hv, dv, dk))
     if o is None:
-        o = torch.empty((B, N, Hv, dv), dtype=torch.float32, device=q.device)
+        o = _new((B, N, Hv, dv), torch.float32, q.device, stream)
     _require(o, "o", torch.float32, (B, N, Hv, dv))
     lib = load_library()
     _check(lib.gdn_tree_verify(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent),
@@ -211,7 +225,7 @@ def gdn_tree_verify_branches(ctx: GdnContext, q, k, v, g, beta, parent, S0, o=No
     _require(parent, "parent", torch.int32, (B, N))
     _require(S0, "S0", torch.float32, (B, Hv, dv, dk))
     if o is None:
-        o = torch.empty((B, N, Hv, dv), dtype=torch.float32, device=q.device)
+        o = _new((B, N, Hv, dv), torch.float32, q.device, stream)
     _require(o, "o", torch.float32, (B, N, Hv, dv))
     _check(load_library().gdn_tree_verify_branches(ctx.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                                    _ptr(parent), _ptr(S0), _ptr(o), _stream(stream)))
@@ -227,7 +241,7 @@ def gdn_commit_path(ctx: GdnContext, accepted, S_new=None, stream=None):
     d = ctx.dims
     _require(accepted, "accepted", torch.int32, (d.B,))
     if S_new is None:
-        S_new = torch.empty((d.B, d.H_v, d.d_v, d.d_k), dtype=torch.float32, device=accepted.device)
+        S_new = _new((d.B, d.H_v, d.d_v, d.d_k), torch.float32, accepted.device, stream)
     _require(S_new, "S_new", torch.float32, (d.B, d.H_v, d.d_v, d.d_k))
     _check(load_library().gdn_commit_path(ctx.handle, _ptr(accepted), _ptr(S_new), _stream(stream)))
     return S_new
@@ -250,10 +264,10 @@ def gdn_commit_verify(ctx: GdnContext, accepted, q, k, v, g, beta, parent, S_nex
     _require(beta, "beta", torch.float32, (B, N, Hv))
     _require(parent, "parent", torch.int32, (B, N))
     if S_next is None:
-        S_next = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device)
+        S_next = _new((B, Hv, dv, dk), torch.float32, q.device, stream)
     _require(S_next, "S_next", torch.float32, (B, Hv, dv, dk))
     if o is None:
-        o = torch.empty((B, N, Hv, dv), dtype=torch.float32, device=q.device)
+        o = _new((B, N, Hv, dv), torch.float32, q.device, stream)
     _require(o, "o", torch.float32, (B, N, Hv, dv))
     _check(load_library().gdn_commit_verify(ctx.handle, _ptr(accepted), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                             _ptr(beta), _ptr(parent), _ptr(S_next), _ptr(o), _stream(stream)))
@@ -268,9 +282,9 @@ def gdn_tree_ancestors(parent, stream=None):
     _require(parent, "parent", torch.int32)
     B, N = parent.shape
     W = max((N + 31) // 32, 1)
-    anc = torch.zeros((B, N, W), dtype=torch.int32, device=parent.device)
-    depth = torch.zeros((B, N), dtype=torch.int32, device=parent.device)
-    status = torch.zeros((max(B, 1),), dtype=torch.int32, device=parent.device)
+    anc = _new((B, N, W), torch.int32, parent.device, stream, make="zeros")
+    depth = _new((B, N), torch.int32, parent.device, stream, make="zeros")
+    status = _new((max(B, 1),), torch.int32, parent.device, stream, make="zeros")
     dims = Dims(B, N, 1, 1, 64, 64, GDN_BF16)
     _check(load_library().gdn_tree_ancestors(ctypes.byref(dims), _ptr(parent), _ptr(anc), _ptr(depth),
                                              _ptr(status), _stream(stream)))
@@ -286,7 +300,7 @@ def gdn_accept_path(parent, draft_token, target_token, stream=None):
     _require(draft_token, "draft_token", torch.int32, (B, N))
     _require(target_token, "target_token", torch.int32, (B, N + 1))
     dev = parent.device
-    accepted, accept_len, status = (torch.empty((max(B, 1),), dtype=torch.int32, device=dev) for _ in range(3))
+    accepted, accept_len, status = (_new((max(B, 1),), torch.int32, dev, stream) for _ in range(3))
     dims = Dims(B, N, 1, 1, 64, 64, GDN_BF16)
     _check(load_library().gdn_accept_path(ctypes.byref(dims), _ptr(parent), _ptr(draft_token),
                                           _ptr(target_token), _ptr(accepted), _ptr(accept_len), _ptr(status),
@@ -305,11 +319,11 @@ def gdn_tree_build(root_logp, node_logp, w, max_depth, stream=None):
     N = node_logp.shape[1]
     _require(node_logp, "node_logp", torch.float32, (B, N, C))
     dev = root_logp.device
-    parent = torch.empty((B, N), dtype=torch.int32, device=dev)
-    rank = torch.empty((B, N), dtype=torch.int32, device=dev)
-    score = torch.empty((B, N), dtype=torch.float32, device=dev)
-    steps = torch.empty((max(B, 1),), dtype=torch.int32, device=dev)
-    status = torch.empty((max(B, 1),), dtype=torch.int32, device=dev)
+    parent = _new((B, N), torch.int32, dev, stream)
+    rank = _new((B, N), torch.int32, dev, stream)
+    score = _new((B, N), torch.float32, dev, stream)
+    steps = _new((max(B, 1),), torch.int32, dev, stream)
+    status = _new((max(B, 1),), torch.int32, dev, stream)
     dims = Dims(B, N, 1, 1, 64, 64, GDN_BF16)
     _check(load_library().gdn_tree_build(ctypes.byref(dims), int(C), int(w), int(max_depth), _ptr(root_logp),
                                          _ptr(node_logp), _ptr(parent), _ptr(rank), _ptr(score), _ptr(steps),
@@ -328,7 +342,7 @@ def gdn_tree_verify_static(q, k, v, g, beta, parent, S0, o=None, stream=None):
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (parent, "parent"), (S0, "S0")):
         _require(t, name)
     if o is None:
-        o = torch.empty((B, N, Hv, dv), dtype=torch.float32, device=q.device)
+        o = _new((B, N, Hv, dv), torch.float32, q.device, stream)
     _require(o, "o", torch.float32, (B, N, Hv, dv))
     dims = Dims(B, N, Hk, Hv, dk, dv, code)
     _check(load_library().gdn_tree_verify_static(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
