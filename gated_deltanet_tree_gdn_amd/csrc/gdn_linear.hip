@@ -70,6 +70,9 @@ __device__ __forceinline__ void put(const LinearArgs& a, int64_t m, int n, float
     }
 }
 
+// Tiles of `size` that n rows or outputs (one or more, up to 2^31 - 1) need.
+__host__ __device__ constexpr int tiles_of(int n, int size) { return (n - 1) / size + 1; }
+
 // Workgroups go to the 8 XCDs in turn; here each XCD gets a run of
 // consecutive tiles, ordered in bands of 8 tile rows, so that the tiles it has
 // in flight share rows of x and w in its L2.
@@ -335,9 +338,10 @@ __device__ __forceinline__ void tile(const LinearArgs& a, char* lds, int64_t m0,
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT, bool TAIL>
 __global__ void __launch_bounds__(64 * WM * WN * KG) tile_kernel(LinearArgs a) {
     __shared__ __align__(16) char lds[tile_lds_bytes<BM, BN, WM, WN, KG, NB>()];
-    const int tiles_m = (a.d.M + BM - 1) / BM, tiles_n = (a.d.N + BN - 1) / BN;
+    const int tiles_m = tiles_of(a.d.M, BM), tiles_n = tiles_of(a.d.N, BN), id = int(block_id());
+    if (id >= tiles_m * tiles_n) return;
     int tm, tn;
-    tile_at(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    tile_at(xcd_run(id, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
     tile<BM, BN, WM, WN, KG, NB, DIRECT, TAIL>(a, lds, int64_t(tm) * BM, int64_t(tn) * BN);
 }
 
@@ -350,7 +354,8 @@ template <bool TAIL>
 __global__ void __launch_bounds__(512) tile256_kernel(LinearArgs a, int whole) {
     __shared__ __align__(16) char
         lds[std::max(tile_lds_bytes<256, 256, 2, 4, 1, 2>(), tile_lds_bytes<128, 128, 2, 2, 2, 2>())];
-    const int tiles_m = (a.d.M + 255) / 256, tiles_n = (a.d.N + 255) / 256, id = blockIdx.x;
+    const int tiles_m = tiles_of(a.d.M, 256), tiles_n = tiles_of(a.d.N, 256), id = int(block_id());
+    if (id >= whole + 4 * (tiles_m * tiles_n - whole)) return;
     int tm, tn;
     if (id < whole) {
         tile_at(xcd_run(id, whole), tiles_m, tiles_n, tm, tn);
@@ -417,18 +422,19 @@ void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
 
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
 void launch_tile(const LinearArgs& a, hipStream_t stream) {
-    const int tiles = ((a.d.M + BM - 1) / BM) * ((a.d.N + BN - 1) / BN), threads = 64 * WM * WN * KG;
+    const dim3 grid = grid_of(int64_t(tiles_of(a.d.M, BM)) * tiles_of(a.d.N, BN));
+    constexpr int threads = 64 * WM * WN * KG;
     if (DIRECT && a.d.K % kBK)
-        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, DIRECT><<<tiles, threads, 0, stream>>>(a);
+        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, DIRECT><<<grid, threads, 0, stream>>>(a);
     else
-        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, false><<<tiles, threads, 0, stream>>>(a);
+        tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, false><<<grid, threads, 0, stream>>>(a);
 }
 
 void launch_tile256(const LinearArgs& a, int tiles, int cut, hipStream_t stream) {
     if (a.d.K % kBK)
-        tile256_kernel<true><<<tiles + 3 * cut, 512, 0, stream>>>(a, tiles - cut);
+        tile256_kernel<true><<<grid_of(tiles + 3 * int64_t(cut)), 512, 0, stream>>>(a, tiles - cut);
     else
-        tile256_kernel<false><<<tiles + 3 * cut, 512, 0, stream>>>(a, tiles - cut);
+        tile256_kernel<false><<<grid_of(tiles + 3 * int64_t(cut)), 512, 0, stream>>>(a, tiles - cut);
 }
 
 // Rows of any alignment to rows of 16-byte pieces.
