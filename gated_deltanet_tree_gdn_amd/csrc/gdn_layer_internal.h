@@ -56,6 +56,15 @@ struct LinearArgs {
     void* ws;
 };
 
+// The kernel that gdn_linear runs.
+enum LinearKernel { kThin, kTileAny, kTile64Two, kTile64, kTile128Two, kTile128, kTile256 };
+struct LinearChoice {
+    LinearKernel kernel;
+    bool tail;  // with the code for ends of K (thin: for rows that are not whole 16-byte pieces)
+    int cut;    // tiles of 256 x 256 in quarters
+};
+LinearChoice linear_choice(const gdn_linear_dims& d);
+
 size_t prefill_ws_bytes(const gdn_seq_dims& d);
 size_t linear_ws_bytes(const gdn_linear_dims& d);
 hipError_t launch_prefill(const SeqArgs& a, hipStream_t stream);

@@ -421,20 +421,22 @@ void launch_thin(const LinearArgs& a, bool vec, hipStream_t stream) {
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int NB, bool DIRECT>
-void launch_tile(const LinearArgs& a, hipStream_t stream) {
+void launch_tile(const LinearArgs& a, bool tail, hipStream_t stream) {
     const dim3 grid = grid_of(int64_t(tiles_of(a.d.M, BM)) * tiles_of(a.d.N, BN));
     constexpr int threads = 64 * WM * WN * KG;
-    if (DIRECT && a.d.K % kBK)
+    if (DIRECT && tail)
         tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, DIRECT><<<grid, threads, 0, stream>>>(a);
     else
         tile_kernel<BM, BN, WM, WN, KG, NB, DIRECT, false><<<grid, threads, 0, stream>>>(a);
 }
 
-void launch_tile256(const LinearArgs& a, int tiles, int cut, hipStream_t stream) {
-    if (a.d.K % kBK)
-        tile256_kernel<true><<<grid_of(tiles + 3 * int64_t(cut)), 512, 0, stream>>>(a, tiles - cut);
+void launch_tile256(const LinearArgs& a, bool tail, int cut, hipStream_t stream) {
+    const int whole = tiles_of(a.d.M, 256) * tiles_of(a.d.N, 256) - cut;
+    const dim3 grid = grid_of(whole + 4 * int64_t(cut));
+    if (tail)
+        tile256_kernel<true><<<grid, 512, 0, stream>>>(a, whole);
     else
-        tile256_kernel<false><<<grid_of(tiles + 3 * int64_t(cut)), 512, 0, stream>>>(a, tiles - cut);
+        tile256_kernel<false><<<grid, 512, 0, stream>>>(a, whole);
 }
 
 // Rows of any alignment to rows of 16-byte pieces.
@@ -478,33 +480,19 @@ size_t linear_ws_bytes(const gdn_linear_dims& d) {
     return p.copy ? (p.x ? packed_bytes(d.M, d.K) : 0) + (p.w ? packed_bytes(d.N, d.K) : 0) : 0;
 }
 
-hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
-    LinearArgs a = args;
-    gdn_linear_dims& d = a.d;
+LinearChoice linear_choice(const gdn_linear_dims& d) {
     const Packing p = packing(d);
-    if (p.copy) {
-        char* ws = static_cast<char*>(a.ws);
-        if (p.x) {
-            launch_pack(a.x, d.x_stride, d.M, d.K, ws, stream);
-            a.x = ws;
-            d.x_stride = (int64_t(d.K) + 7) / 8 * 8;
-            ws += packed_bytes(d.M, d.K);
-        }
-        if (p.w) {
-            launch_pack(a.w, d.w_stride, d.N, d.K, ws, stream);
-            a.w = ws;
-            d.w_stride = (int64_t(d.K) + 7) / 8 * 8;
-        }
-        if (p.x && p.w) d.K = int(d.x_stride);  // the copies end in zeros
-    }
+    const int64_t packed = (int64_t(d.K) + 7) / 8 * 8;                  // a copied row
+    const int K = p.copy && p.x && p.w ? int(packed) : d.K;  // the copies end in zeros
     const bool aligned = p.copy || !(p.x || p.w);
     // direct loads: a tile's rows lie within 2^31 bytes of its first
-    const bool direct = aligned && d.x_stride < (1 << 21) && d.w_stride < (1 << 21);
+    auto near = [&](bool copied, int64_t stride) { return (copied ? packed : stride) < (1 << 21); };
+    const bool direct = aligned && near(p.copy && p.x, d.x_stride) && near(p.copy && p.w, d.w_stride);
     auto tiles = [&](int64_t t) { return double((d.M + t - 1) / t) * double((d.N + t - 1) / t); };
     // What each kernel takes in us, a part that grows with K and one that does not
     // (start and epilogue), fitted to measurements at K = 256, 1024 and 4096 over M
     // = 64 .. 16384, N = 1024 .. 12352.
-    const double k = d.K / 4096.0, t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
+    const double k = K / 4096.0, t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
     // 256 KiB of loads in flight per CU: few tiles
     const double k64two = (2.4 + 15.5 * k) * std::ceil(t64 / 256);
     // two workgroups per CU
@@ -521,20 +509,45 @@ hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
     const double part = cut ? 34.5 * k * std::ceil(over / 64) : 11.0 + (75.0 + 25.0 * over / 256) * k;
     const double k256 = 2.0 + (11.0 + 100.0 * k) * full + (over > 0 ? part : 0.0);
     const double best = std::min({k64two, k64, k128two, k128, k256});
-    if (d.M <= 16 && d.N <= 8192)
-        launch_thin(a, aligned && d.K % 8 == 0, stream);
-    else if (!direct)
-        launch_tile<64, 64, 2, 2, 4, 2, false>(a, stream);
-    else if (best == k64two)
-        launch_tile<64, 64, 2, 2, 2, 4, true>(a, stream);
-    else if (best == k64)
-        launch_tile<64, 64, 2, 2, 1, 4, true>(a, stream);
-    else if (best == k128two)
-        launch_tile<128, 128, 2, 2, 2, 2, true>(a, stream);
-    else if (best == k128)
-        launch_tile<128, 128, 2, 4, 1, 2, true>(a, stream);
-    else
-        launch_tile256(a, int(t256), cut ? int(over) : 0, stream);
+    const bool tail = K % kBK != 0;
+    if (d.M <= 16 && d.N <= 8192) return {kThin, !aligned || K % 8 != 0, 0};
+    if (!direct) return {kTileAny, true, 0};
+    if (best == k64two) return {kTile64Two, tail, 0};
+    if (best == k64) return {kTile64, tail, 0};
+    if (best == k128two) return {kTile128Two, tail, 0};
+    if (best == k128) return {kTile128, tail, 0};
+    return {kTile256, tail, cut ? int(over) : 0};
+}
+
+hipError_t launch_linear(const LinearArgs& args, hipStream_t stream) {
+    LinearArgs a = args;
+    gdn_linear_dims& d = a.d;
+    const LinearChoice c = linear_choice(d);
+    const Packing p = packing(d);
+    if (p.copy) {
+        char* ws = static_cast<char*>(a.ws);
+        if (p.x) {
+            launch_pack(a.x, d.x_stride, d.M, d.K, ws, stream);
+            a.x = ws;
+            d.x_stride = (int64_t(d.K) + 7) / 8 * 8;
+            ws += packed_bytes(d.M, d.K);
+        }
+        if (p.w) {
+            launch_pack(a.w, d.w_stride, d.N, d.K, ws, stream);
+            a.w = ws;
+            d.w_stride = (int64_t(d.K) + 7) / 8 * 8;
+        }
+        if (p.x && p.w) d.K = int(d.x_stride);  // the copies end in zeros
+    }
+    switch (c.kernel) {
+        case kThin: launch_thin(a, !c.tail, stream); break;
+        case kTileAny: launch_tile<64, 64, 2, 2, 4, 2, false>(a, false, stream); break;
+        case kTile64Two: launch_tile<64, 64, 2, 2, 2, 4, true>(a, c.tail, stream); break;
+        case kTile64: launch_tile<64, 64, 2, 2, 1, 4, true>(a, c.tail, stream); break;
+        case kTile128Two: launch_tile<128, 128, 2, 2, 2, 2, true>(a, c.tail, stream); break;
+        case kTile128: launch_tile<128, 128, 2, 4, 1, 2, true>(a, c.tail, stream); break;
+        case kTile256: launch_tile256(a, c.tail, c.cut, stream); break;
+    }
     return hipGetLastError();
 }
 
