@@ -77,3 +77,10 @@ def test_zero_vectors_without_an_epsilon_stay_behind(at, name, dtype):
         assert torch.isnan(o2[at, 2:]).all()
         check(o2[at + 1:], o1[at + 1:], FP32_TOL, "later tokens")
         check(S2, S1, FP32_TOL, "S")
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("n", [1, 9, 449, 1500])
+def test_the_walk_in_fp32(n, dk, dv):
+    """q, k and v in fp32 are walked token by token at any length: the bound of that path, not of the chunks"""
+    run(make(n, 1, 2, dk, dv, seed=n, dtype=F32), FP32_TOL, f"{n} tokens")
