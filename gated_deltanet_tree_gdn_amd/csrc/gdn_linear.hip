@@ -510,6 +510,12 @@ LinearChoice linear_choice(const gdn_linear_dims& d) {
     const double k256 = 2.0 + (11.0 + 100.0 * k) * full + (over > 0 ? part : 0.0);
     const double best = std::min({k64two, k64, k128two, k128, k256});
     const bool tail = K % kBK != 0;
+    // One tile of 16 rows is all that the thin kernel multiplies, and it reads x again for
+    // every 16 outputs, which many outputs make dearer than tiles.  Thin and tiles, cold
+    // weights, in us: K 4096, N 256: 6.9 and 14.4 (1 row), 9.5 and 14.4 (16 rows); N
+    // 8192: 16.6 and 23.2, 23.3 and 23.8; N 10240: 21.2 and 24.5, 31.1 and 24.9; N 12352:
+    // 25.7 and 26.3, 38.9 and 26.7.  K 1024, N 8192: 6.1 and 8.8, 8.1 and 9.0; N 12352:
+    // 7.9 and 9.2, 11.4 and 9.4.
     if (d.M <= 16 && d.N <= 8192) return {kThin, !aligned || K % 8 != 0, 0};
     if (!direct) return {kTileAny, true, 0};
     if (best == k64two) return {kTile64Two, tail, 0};
