@@ -78,7 +78,7 @@ class Model:
         def mix(i, q, k, v, g, beta):
             q, k = (torch.nn.functional.normalize(t.float(), dim=-1) for t in (q, k))
             q, k, v = (t.to(torch.bfloat16).unflatten(0, (B, N)).contiguous() for t in (q * self.scale, k, v))
-            if self.ctx[i] is None:
+            if self.ctx[i] is None or self.ctx[i].dims.N != N:  # one tree size at a time
                 self.ctx[i] = gdn.GdnContext.for_tensors(q, v, parent)
             o = gdn.gdn_tree_verify(self.ctx[i], q, k, v, g.unflatten(0, (B, N)), beta.unflatten(0, (B, N)), parent,
                                     self.states[i])
