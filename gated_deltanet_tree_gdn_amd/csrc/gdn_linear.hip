@@ -8,10 +8,11 @@
 //  - tile_kernel: BM x BN outputs per workgroup, K in steps of 64 through LDS
 //    buffers filled by direct loads while others are multiplied.
 //
-// Measured: 1 x 12352 x 4096 18 us (101 MB of weights, partly in cache: 5.7 TB/s);
+// Measured: 1 x 12352 x 4096 18 us with the 101 MB of weights partly in cache, 26 us
+// with cold ones (3.9 TB/s); 1 x 4096 x 4096 9.7 us cold (3.5 TB/s);
 // 777 x 4096 x 4096 with bias, silu and a residual 40 us (650 TFLOP/s: one round of 224
 // tiles of 128 x 128 on 256 CUs, its loads ahead by a step); 16384 x 12352
-// x 4096 1360 us (1220 TFLOP/s).  With 256 x 256 tiles LDS carries 256 KiB per
+// x 4096 1350 us (1230 TFLOP/s).  With 256 x 256 tiles LDS carries 256 KiB per
 // step (192 read as operands, 64 written by the loads), 2,048 clocks, as many as
 // the MFMAs take: the two compete, and the kernel without its loads takes three
 // quarters of the time.  Steps of 32 (4% slower), wavefronts of 128 x 128 (spills)

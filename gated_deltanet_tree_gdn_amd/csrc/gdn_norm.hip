@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(256) gated_norm_vec_kernel(GatedNormArgs a) {
     }
 }
 
-// Heads wider than 512: one wavefront per head.
+// Heads wider than 512: one wavefront per head, element by element and o twice, which
+// bounds it: 16384 x 4 x 1024 bf16 247 us, 1.6 TB/s; 4096 x 1 x 16384 410 us.
 __global__ void __launch_bounds__(256) gated_norm_any_kernel(GatedNormArgs a) {
     const gdn_gated_norm_dims& d = a.d;
     const int64_t n = int64_t(d.T) * d.H, step = int64_t(gridDim.x) * 4;

@@ -35,7 +35,7 @@
 // = 1 and no decay up to 6e-6 (keys in a plane; 1e-6 token by token).
 //
 // Measured, H_k 16, H_v 32, d 128, bf16, half of the 13 states resumed: one of
-// 16384 tokens 540 us (prep 98, chain 442), 13 of 7919 tokens in all 253 us.
+// 16384 tokens 530 us (prep 97, chain 433), 13 of 7919 tokens in all 250 us.
 // The inputs, outputs and states are 409 MB and 238 MB; at the rate of a copy
 // (5.2 TB/s) that is 79 and 46 us.
 
@@ -198,7 +198,7 @@ __device__ __forceinline__ float exp_diff(double hi, double lo) {
 // blocks by substitution (a column per lane), the blocks below them by fp64 MFMA
 // (in fp32 their rounding is most of the error where |k|^2 is 2).  Bound by memory: it
 // writes T and M, 480 bytes per (token, value head), and reads q and k; 16384
-// tokens, H_v 32: 387 MB in 98 us, 3.9 TB/s.
+// tokens, H_v 32: 395 MB in 97 us, 4.1 TB/s.
 template <int DK>
 __global__ void __launch_bounds__(256, 3) prep_kernel(ChunkArgs c) {
     constexpr int KS = DK / 32;
@@ -590,12 +590,14 @@ __device__ __forceinline__ void walk_rows(const SeqArgs& a, int b, int hk, int h
         for (int e = 0; e < E; ++e) Sp[e] = s[e];
 }
 
-// What bounds it: a chunk takes 1.4 us (3,000 clocks) of three dependent phases,
-// each a chain of LDS reads (some 300 clocks), 6 to 12 MFMAs, the split of their
-// sums and a barrier; LDS is busy for 1,700 of the clocks, a SIMD for 640 with
-// MFMAs and 1,000 with the rest.  The chain cannot be cut along the sequence
-// (S enters every chunk), so it is cut along d_v as finely as MFMA tiles allow.
-// The same work in one wavefront per 16 columns, without barriers, took 840 us.
+// What bounds it: a chunk takes 1.7 us (3,600 clocks) of three dependent phases,
+// each a chain of LDS reads (some 300 clocks), 12 MFMAs, the split of their
+// sums and a barrier; LDS is busy for 2,000 of the clocks, a SIMD for 900 with
+// MFMAs and 1,900 with the rest, most of it splits.  The outputs' M U, which splits M and
+// U, outlasts the state update beside it by 700.  The chain cannot be cut along
+// the sequence (S enters every chunk), so it is cut along d_v as finely as MFMA
+// tiles allow.  With two parts per operand, one wavefront per 16 columns and no
+// barriers took 840 us where this split took 353.
 //
 // Eight wavefronts: 0 .. 3 carry the state from chunk to chunk, 4 .. 7 form
 // the outputs beside them.  Three barriers per chunk:
@@ -965,12 +967,14 @@ hipError_t launch_chunks(const ChunkArgs& c, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// fp32 operands would need three parts each, so those are walked token by
-// token, as are sequences of 8 tokens on average, which fill a small part of
-// their chunks.  (The lengths themselves are on the device.)  Walk and chunks,
-// H_v 32, d 128: B 1, T 8: 14 and 18 us; B 8, T 72: 25 and 37 us; B 32, T 264:
-// 73 and 114 us; B 120, T 500: 182 and 317 us; but B 1, T 64: 25 and 18 us, and
-// B 32, T 1000: 209 and 123 us.
+// fp32 q, k and v would need three parts each, so those are walked token by token,
+// as are sequences of 8 tokens on average, which fill a small part of their
+// chunks.  (The lengths themselves are on the device.)  At 8 the walk is no slower
+// even if one sequence has nearly all tokens.  Walk and chunks, H_v 32, d 128, bf16,
+// in us, by tokens per sequence on average:
+//   one long, the others of one token  B 32: 8: 113 and 124, 12: 172 and 126;  B 120: 8: 420 and 377
+//   lengths over two decades           B 32: 8: 77 and 120, 16: 127 and 123;   B 120: 8: 243 and 358
+//   one sequence                       8: 6 and 17, 64: 25 and 18
 bool use_chunks(const gdn_seq_dims& d) { return d.qkv_dtype == GDN_BF16 && d.T > 8 * int64_t(d.B); }
 
 }  // namespace

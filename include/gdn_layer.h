@@ -51,10 +51,11 @@ extern "C" {
  * sequences of one call must not share an entry.
  * ------------------------------------------------------------------------ */
 typedef struct {
-    int32_t B;         /* sequences                                              */
+    int32_t B;         /* sequences, at most 65535; B H_v at most 2^24           */
     int32_t T;         /* tokens of all sequences together (gdn_decode: ignored) */
     int32_t H_k;       /* key/query heads                                        */
-    int32_t H_v;       /* value heads (a multiple of H_k)                        */
+    int32_t H_v;       /* value heads (a multiple of H_k, at most 65535; H_v d_v
+                          at most GDN_MAX_SEQ_STRIDE)                            */
     int32_t d_k;       /* key dimension, 64 or 128                               */
     int32_t d_v;       /* value dimension, 64 or 128                             */
     int32_t qkv_dtype; /* gdn_dtype of q, k, v                                   */
@@ -62,7 +63,7 @@ typedef struct {
     int32_t n_slots;   /* entries of the state pool                              */
     int32_t qk_l2norm; /* 1: q and k are L2-normalised by the operator           */
     float q_scale;     /* factor on the output                                   */
-    float l2_eps;      /* epsilon of the L2 norm, >= 0                           */
+    float l2_eps;      /* epsilon of the L2 norm, >= 0 (0: a zero vector is 0 / 0) */
     int64_t q_stride;  /* elements between tokens of q: a multiple of 16 bytes,
                           at most GDN_MAX_SEQ_STRIDE                             */
     int64_t k_stride;  /* the same of k                                          */
