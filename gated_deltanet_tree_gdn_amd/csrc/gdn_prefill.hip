@@ -25,9 +25,9 @@
 // Precision: q, k and v are exact bf16 operands.  Every fp32 operand (S, R = V -
 // gamma K S^T, the off-diagonal part of T, U, the decayed U, M) is split into three
 // bf16 parts, 24 bits, and of a product of two such operands the six products of
-// parts above 2^-24 of it are taken.  The diagonal of T acts in fp32.  Two parts of
-// any of them cost 10 to 200 times the error of fp32 where keys reach |k|^2 = 2 and
-// nothing decays, and 20 times in outputs of ordinary inputs.
+// parts above 2^-24 of it are taken.  The diagonal of T acts in fp32.  Two parts for
+// S, T, or M and U multiply the error by 5 to 200 where keys reach |k|^2 = 2 and
+// nothing decays, and that of outputs of ordinary inputs by up to 20.
 // Sums, states and the decay are fp32, G is fp64 (a difference G_i - G_j stays exact
 // to fp32 however far the chunk has decayed), and so are the products that form T:
 // near |k|^2 = 2 their terms are larger than T.  Relative error after 2000 tokens:
@@ -593,10 +593,10 @@ __device__ __forceinline__ void walk_rows(const SeqArgs& a, int b, int hk, int h
 // What bounds it: a chunk takes 1.7 us (3,600 clocks) of three dependent phases,
 // each a chain of LDS reads (some 300 clocks), 12 MFMAs, the split of their
 // sums and a barrier; LDS is busy for 2,000 of the clocks, a SIMD for 900 with
-// MFMAs and 1,900 with the rest, most of it splits.  The outputs' M U, which splits M and
-// U, outlasts the state update beside it by 700.  The chain cannot be cut along
-// the sequence (S enters every chunk), so it is cut along d_v as finely as MFMA
-// tiles allow.  With two parts per operand, one wavefront per 16 columns and no
+// MFMAs and 1,900 with the rest, most of it splits.  The outputs' M U, which splits
+// M and U, outlasts the state update beside it by 700.  The chain cannot be cut
+// along the sequence (S enters every chunk), so it is cut along d_v as finely as
+// MFMA tiles allow.  With two parts per operand, one wavefront per 16 columns and no
 // barriers took 840 us where this split took 353.
 //
 // Eight wavefronts: 0 .. 3 carry the state from chunk to chunk, 4 .. 7 form
