@@ -366,3 +366,7 @@ def verify(q, k, v, g, beta, parent, S0, o=None, stream=None, ctx: Optional[GdnC
 # the operators around the tree verify (gdn_layer.h)
 from .layer import (LAYER_EXPORTS, gdn_add_norm, gdn_decode, gdn_gated_norm, gdn_linear,  # noqa: E402
                     gdn_prefill, gdn_prefill_workspace_bytes)
+
+# the softmax attention layers between them (gdn_attn.h)
+from .attn import (ATTN_EXPORTS, GdnKvCache, gdn_attn_decode, gdn_attn_prefill, gdn_attn_verify,  # noqa: E402
+                   gdn_attn_workspace_bytes, gdn_kv_append, gdn_kv_commit)

@@ -1,0 +1,84 @@
+// gdn_attn_internal.h -- launch interface between the C ABI of gdn_attn.h and
+// its kernels, and the division of the keys over workgroups that the
+// attention kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "gdn_attn.h"
+
+namespace gdn {
+
+struct KvAppendArgs {
+    gdn_kv_append_dims d;
+    gdn_kv_cache cache;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* q_weight;
+    const float* k_weight;
+    const float* inv_freq;
+    const int32_t* position;
+    const int32_t* slot;
+    void* q_out;
+};
+
+constexpr int kCommitCaches = 32;  // caches of one launch
+struct KvCommitArgs {
+    gdn_kv_commit_dims d;
+    gdn_kv_cache cache;  // k and v as in the arrays
+    void* k[kCommitCaches];
+    void* v[kCommitCaches];
+    const uint32_t* anc;
+    const int32_t* accepted;
+    const int32_t* table;
+    const int32_t* length;
+    int32_t* new_length;  // NULL in launches after the first
+    int32_t* seq_status;
+};
+
+enum AttnKind { kAttnDecode, kAttnPrefill, kAttnVerify };
+
+struct AttnArgs {
+    gdn_attn_dims d;
+    gdn_kv_cache cache;
+    const uint16_t* q;
+    const int32_t* cu;  // prefill
+    const uint32_t* anc;  // verify
+    const int32_t* table;
+    const int32_t* length;
+    const uint16_t* gate;
+    uint16_t* o;
+    int32_t* seq_status;
+    void* ws;
+    AttnKind kind;
+    int page_shift;
+    // Filled by attn_shape():
+    int group;       // query heads of a key head
+    int tile_rows;   // (token, head of the group) rows of a workgroup
+    int head_tiles;  // decode: tiles of 16 heads that the group is cut into, else 1
+    int spread;      // workgroups of one (key head, head tile) that the keys are divided over
+    int min_chunk;   // keys of a workgroup at least; chunks are multiples of it
+    int part_tiles;  // parts of one (key head, head tile) in the workspace
+};
+// The part of a tile's result over one chunk of keys: maxima, sums, and
+// unnormalised outputs.
+constexpr int kDecodeRows = 16, kTileRows = 128;
+
+// Fills the derived members; false if the sizes leave nothing to do.
+void attn_shape(AttnArgs& a);
+size_t attn_ws_bytes(const AttnArgs& a);
+
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
+hipError_t launch_kv_commit(const KvCommitArgs& a, int n_caches, hipStream_t stream);
+hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_tiles(const AttnArgs& a, hipStream_t stream);
+// What the two have in common: the parts of tiles whose keys were divided are
+// joined, and seq_status is written.
+hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_status(const AttnArgs& a, hipStream_t stream);
+
+}  // namespace gdn

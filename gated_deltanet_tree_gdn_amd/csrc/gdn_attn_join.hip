@@ -1,0 +1,173 @@
+// gdn_attn_join.hip -- what the attention kernels share: the sizes of a call's
+// division, the join of tiles whose keys were divided, and the verdict on a
+// call's sequences.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gdn_attn_internal.h"
+#include "gdn_attn_plan.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kJoinRows = 16;  // rows of a workgroup that joins a tile of many
+
+struct Joined {
+    f32x4 acc{0, 0, 0, 0};
+    float m = -__builtin_inff(), l = 0.0f;
+    __device__ __forceinline__ void add(const f32x4& x, float mx, float lx) {
+        const float top = fmaxf(m, mx), base = finite_max(top);
+        const float f = exp2_fast(m - base), fx = exp2_fast(mx - base);
+        acc = acc * f + x * fx;
+        l = l * f + lx * fx;
+        m = top;
+    }
+};
+
+// Parts of a tile's row, joined in the order of the keys.  Single tokens: a
+// workgroup for every row, since there are few and their parts may be hundreds;
+// the workgroup's threads take the parts in turn.  Tiles: D / 4 threads of a
+// row take its parts one after another.
+template <AttnKind KIND, int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
+    constexpr int C = D / 4, K = kThreads / C;  // threads of a row, rows (or shares of the parts) at a time
+    constexpr bool one = KIND == kAttnDecode;
+    __shared__ f32x4 share[one ? K : 1][C];
+    __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
+    const int tid = threadIdx.x, lane = tid & 63, p = tid % C, k = tid / C;
+    const int heads = a.cache.H_kv * a.head_tiles;
+    const int blocks = one ? min(a.group, kDecodeRows) : kTileRows / kJoinRows;  // workgroups of a tile
+    const int64_t wg = block_id(), grid_tiles = int64_t(gridDim.x) * gridDim.y / heads / blocks;
+    if (wg >= grid_tiles * heads * blocks) return;
+    const int block = int(wg % blocks), hh = int(wg / blocks % heads), h = hh / a.head_tiles;
+    const int c = attn_chunk<KIND>(a, lane);
+    AttnItem it;
+    for (int64_t tile = wg / blocks / heads; attn_item<KIND, true>(a, c, tile, lane, it); tile += grid_tiles) {
+        if (it.chunks > 1) {
+            const AttnSeq s = attn_seq<KIND>(a, it.b);
+            if constexpr (one) {
+                const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
+                if (row < a.group - head0) {
+                    Joined x;
+                    for (int i = k; i < it.chunks; i += K) {
+                        const float* part = part_out(a, it.part + i, hh, kDecodeRows, D);
+                        x.add(*reinterpret_cast<const f32x4*>(part + row * D + 4 * p), part[kDecodeRows * D + row],
+                              part[kDecodeRows * (D + 1) + row]);
+                    }
+                    share[k][p] = x.acc;
+                    if (p == 0) {
+                        share_m[k] = x.m;
+                        share_l[k] = x.l;
+                    }
+                    __syncthreads();
+                    if (k == 0) {
+                        for (int i = 1; i < K; ++i) x.add(share[i][p], share_m[i], share_l[i]);
+                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, x.acc, x.l);
+                    }
+                }
+            } else {
+                const int row0 = it.tile * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
+                const int last_token = (row0 + rows - 1) / a.group;
+                const int seen = KIND == kAttnPrefill ? min(max(s.prefix + last_token + 1, 0), s.keys) : s.keys;
+                const int chunks = max((seen + c - 1) / c, 1);
+                for (int r = block * kJoinRows + k; chunks > 1 && r < min((block + 1) * kJoinRows, rows); r += K) {
+                    Joined x;
+                    for (int i = 0; i < chunks; ++i) {
+                        const float* part = part_out(a, it.part + i, hh, kTileRows, D);
+                        x.add(*reinterpret_cast<const f32x4*>(part + r * D + 4 * p), part[kTileRows * D + r],
+                              part[kTileRows * (D + 1) + r]);
+                    }
+                    const int token = (row0 + r) / a.group;
+                    attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, 4 * p, x.acc, x.l);
+                }
+            }
+        }
+        if constexpr (KIND != kAttnPrefill) return;  // the grid has workgroups for every tile
+    }
+}
+
+// One workgroup per sequence reads what the attention kernels read of its
+// length, its place among the rows and its pages.
+__global__ __launch_bounds__(kThreads) void status_kernel(AttnArgs a) {
+    const int b = blockIdx.x;
+    const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, len = a.length[b];
+    int64_t keys = len;
+    bool bad = len < 0 || len > cap;
+    if (a.kind == kAttnVerify) {
+        keys += a.d.T;
+        bad |= keys > cap;
+    } else if (a.kind == kAttnPrefill) {
+        const int start = a.cu[b], end = a.cu[b + 1];
+        bad |= start < 0 || start > end || end > a.d.T || end - start > len;
+        if (start == end) keys = 0;
+    }
+    keys = keys < 0 ? 0 : keys < cap ? keys : cap;
+    for (int64_t p = threadIdx.x; p << a.page_shift < keys; p += kThreads) {
+        const int page = a.table[b * a.d.table_stride + p];
+        bad |= page < 0 || page >= a.cache.n_pages;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) a.seq_status[b] = bad ? GDN_ERR_SHAPE : 0;
+}
+
+template <AttnKind KIND>
+hipError_t launch_join(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+    switch (a.cache.d) {
+        case 64: join_kernel<KIND, 64><<<grid, kThreads, 0, stream>>>(a); break;
+        case 128: join_kernel<KIND, 128><<<grid, kThreads, 0, stream>>>(a); break;
+        default: join_kernel<KIND, 256><<<grid, kThreads, 0, stream>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
+int64_t max_tiles(const AttnArgs& a) {
+    const int64_t rows = int64_t(a.d.T) * a.group;
+    return a.kind == kAttnDecode   ? a.d.B
+           : a.kind == kAttnVerify ? a.d.B * ((rows + kTileRows - 1) / kTileRows)
+                                   : rows / kTileRows + a.d.B;
+}
+int64_t max_chunks(const AttnArgs& a) {
+    return ((int64_t(a.d.max_pages) << a.page_shift) + a.min_chunk - 1) / a.min_chunk;
+}
+
+}  // namespace
+
+void attn_shape(AttnArgs& a) {
+    constexpr int kCu = 256;
+    a.page_shift = __builtin_ctz(a.cache.page_size);
+    a.group = a.d.H_q / a.cache.H_kv;
+    const bool one = a.kind == kAttnDecode;
+    a.tile_rows = one ? kDecodeRows : kTileRows;
+    a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
+    a.min_chunk = one ? 128 : 256;
+    a.spread = std::max(1, 2 * kCu / (a.cache.H_kv * a.head_tiles));
+    const int64_t chunks = max_chunks(a);
+    // prompts may overlap (where cu_seqlens decreases), and each may then have all rows
+    const int64_t tiles = a.kind == kAttnPrefill ? a.d.B * ((int64_t(a.d.T) * a.group + kTileRows - 1) / kTileRows) : max_tiles(a);
+    a.part_tiles = chunks <= 1 ? 0 : int(std::min<int64_t>(2 * a.spread, tiles * chunks));
+}
+
+size_t attn_ws_bytes(const AttnArgs& a) {
+    const size_t part = size_t(a.tile_rows) * (a.cache.d + 2) * sizeof(float);
+    return (size_t(a.part_tiles) * a.cache.H_kv * a.head_tiles * part + 255) & ~size_t(255);
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
+    const int64_t heads = int64_t(a.cache.H_kv) * a.head_tiles;
+    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : kTileRows / kJoinRows;
+    const dim3 grid = grid_of(max_tiles(a) * heads * blocks);
+    return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, grid, stream)
+           : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, grid, stream)
+                                   : launch_join<kAttnPrefill>(a, grid, stream);
+}
+
+hipError_t launch_attn_status(const AttnArgs& a, hipStream_t stream) {
+    status_kernel<<<a.d.B, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace gdn
