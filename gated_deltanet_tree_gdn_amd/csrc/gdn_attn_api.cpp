@@ -72,6 +72,8 @@ gdn_status check_cache(const gdn_kv_cache* c) {
     GDN_TRY(check_stride(c->v_page_stride, unit, "v_page_stride"));
     GDN_TRY(check_stride(c->v_row_stride, unit, "v_row_stride"));
     GDN_TRY(check_stride(c->v_head_stride, unit, "v_head_stride"));
+    if (c->k_row_stride > GDN_MAX_SEQ_STRIDE || c->v_row_stride > GDN_MAX_SEQ_STRIDE)
+        return fail(GDN_ERR_SHAPE, "row strides of a cache must be at most 2^24");
     GDN_TRY(check_ptr(c->k, 16, "k of the cache"));
     GDN_TRY(check_ptr(c->v, 16, "v of the cache"));
     GDN_TRY(check_ptr(c->k_scale, 4, "k_scale", false));

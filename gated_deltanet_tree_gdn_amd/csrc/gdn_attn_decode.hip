@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
 
     AttnItem it;
     if (!attn_item<kAttnDecode, false>(a, c, wg / heads, lane, it)) return;
-    const AttnSeq s = attn_seq<kAttnDecode>(a, it.b);
+    const AttnSeq s = attn_seq_uniform<kAttnDecode>(a, it.b);
     const int begin = it.chunk * c, end = min(begin + c, s.keys);
     const int32_t* table = a.table + it.b * a.d.table_stride;
 

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     AttnItem it;
     for (int64_t tile = wg / blocks / heads; attn_item<KIND, true>(a, c, tile, lane, it); tile += grid_tiles) {
         if (it.chunks > 1) {
-            const AttnSeq s = attn_seq<KIND>(a, it.b);
+            const AttnSeq s = attn_seq_uniform<KIND>(a, it.b);
             if constexpr (one) {
                 const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
                 if (row < a.group - head0) {

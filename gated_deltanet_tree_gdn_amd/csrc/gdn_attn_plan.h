@@ -54,6 +54,17 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
     return s;
 }
 
+// The same of a sequence that all lanes agree on.
+template <AttnKind KIND>
+__device__ __forceinline__ AttnSeq attn_seq_uniform(const AttnArgs& a, int b) {
+    AttnSeq s = attn_seq<KIND>(a, b);
+    s.n = __builtin_amdgcn_readfirstlane(s.n);
+    s.row0 = KIND == kAttnPrefill ? __builtin_amdgcn_readfirstlane(int(s.row0)) : s.row0;
+    s.prefix = __builtin_amdgcn_readfirstlane(s.prefix);
+    s.keys = __builtin_amdgcn_readfirstlane(s.keys);
+    return s;
+}
+
 template <AttnKind KIND>
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnSeq& s) {
     if constexpr (KIND == kAttnDecode) return 1;
@@ -74,6 +85,11 @@ __device__ __forceinline__ int64_t wave_scan64(int64_t x, int lane) {  // inclus
     return x;
 }
 
+__device__ __forceinline__ int64_t read_lane64(int64_t x, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(x), lane), hi = __builtin_amdgcn_readlane(uint32_t(x >> 32), lane);
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+
 // Keys of a chunk.
 template <AttnKind KIND>
 __device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
@@ -89,7 +105,7 @@ __device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
         total = wave_sum64(total);
     }
     const int64_t c = max((total + a.spread - 1) / a.spread, int64_t(1));
-    return int(min((c + a.min_chunk - 1) / a.min_chunk * a.min_chunk, int64_t(1) << 30));
+    return __builtin_amdgcn_readfirstlane(int(min((c + a.min_chunk - 1) / a.min_chunk * a.min_chunk, int64_t(1) << 30)));
 }
 
 struct AttnItem {
@@ -120,16 +136,16 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int c, int64_t i, i
         if (here) {
             const int src = __builtin_ctzll(here);
             it.b = base + src;
-            it.chunks = __shfl(chunks, src);
-            const int64_t at = i - __shfl(first, src);
-            const int t = int(TILES ? at : at / it.chunks);
-            it.tile = t;
-            it.chunk = TILES ? 0 : int(at - int64_t(t) * it.chunks);
-            it.part = parts0 + __shfl(parts_end - parts, src) + int64_t(t) * it.chunks;
+            it.chunks = __builtin_amdgcn_readlane(chunks, src);
+            // the item's number within its sequence is below 2^31 (rows and chunks are)
+            const uint32_t at = uint32_t(i - read_lane64(first, src));
+            it.tile = TILES ? at : at / uint32_t(it.chunks);
+            it.chunk = TILES ? 0 : at - it.tile * it.chunks;
+            it.part = parts0 + read_lane64(parts_end - parts, src) + int64_t(it.tile) * it.chunks;
             return true;
         }
-        items0 += __shfl(items_end, 63);
-        parts0 += __shfl(parts_end, 63);
+        items0 += read_lane64(items_end, 63);
+        parts0 += read_lane64(parts_end, 63);
     }
     return false;
 }

@@ -21,16 +21,48 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Positions of the 16-byte piece p of row r in LDS.  K is read 16 rows of one
-// piece at a time, V transposed, 4 rows of four adjacent pieces at a time; both
-// spread over all banks.
+// The 16-byte pieces of a row in LDS are permuted by these.  K is read 16 rows
+// of one piece at a time, V transposed, 4 rows of four adjacent pieces at a
+// time; both spread over all banks.
 template <int D>
-__device__ __forceinline__ int k_piece(int r, int p) {
-    return r * (D / 8) + (p ^ (D >= 128 ? r & 15 : r >> 1 & 7));
+__device__ __forceinline__ int k_xor(int r) {
+    return D >= 128 ? r & 15 : r >> 1 & 7;
 }
 template <int D>
-__device__ __forceinline__ int v_piece(int r, int p) {
-    return r * (D / 8) + (p ^ (D >= 128 ? 4 * (r & 3) : 4 * (r >> 1 & 1)));
+__device__ __forceinline__ int v_xor(int r) {
+    return D >= 128 ? 4 * (r & 3) : 4 * (r >> 1 & 1);
+}
+
+// x, but what is computed from it is computed where it stands: the compiler
+// would otherwise form it before a loop and keep it in registers throughout.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// x *= f for accumulators that fill half of a wavefront's 512 registers, in
+// place: the other half is what vector instructions can use, and without this
+// the compiler moves all of them there and back around every use.  The first
+// instructions wait for matrix products that may still write x.
+template <int N>
+__device__ __forceinline__ void scale_acc(f32x16 (&x)[N], float f) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float t, y = x[n][i];
+            asm volatile(
+                "v_accvgpr_read_b32 %1, %0\n\t"
+                "s_nop 1\n\t"
+                "v_mul_f32 %1, %1, %2\n\t"
+                "s_nop 1\n\t"
+                "v_accvgpr_write_b32 %0, %1"
+                : "+a"(y), "=&v"(t)
+                : "v"(f));
+            x[n][i] = y;
+        }
+    asm volatile("s_nop 15" ::: "memory");
 }
 
 template <int D>
@@ -38,70 +70,132 @@ struct TileLds {
     uint4 k[2][kKeys * D / 8], v[2][kKeys * D / 8];
 };
 
-// A tile's rows on their way from memory to LDS.
-template <int D, bool F8>
-struct Stage {
-    static constexpr int E = F8 ? 16 : 8;                  // elements of a 16-byte piece
-    static constexpr int P = D / E;                        // pieces of a row
-    static constexpr int L = kKeys * P / kThreads;         // pieces of a thread
-    static constexpr int size = F8 ? 1 : 2;
-    int page[L];
-    uint4 k[L], v[L];
+// 16 bytes per lane from memory to the 1 KB of LDS at `lds`.  The compiler's own
+// forms of these make it wait for all of them before any read of LDS; here what
+// has to have arrived is what loads_barrier() waits for.  Nothing else in these
+// kernels uses m0.
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void load_to_lds(const i32x4& rsrc, int off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(lds)
+                 : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const char* at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
+}
 
-    // Pages of the tile's tokens; -1 where there is none.
-    __device__ __forceinline__ void pages(const AttnArgs& a, const int32_t* table, int t0, int end, int tid) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int t = t0 + (kThreads * i + tid) / P;
-            page[i] = -1;
-            if (t < end) page[i] = table[t >> a.page_shift];
-        }
+// Numbers of the pages from `first` on, one per lane, read from the table 64 at a time.
+struct PageWindow {
+    int first, ids, last;  // last: the last page that is read at all
+    __device__ __forceinline__ void open(int end, int shift) {
+        first = 0x7fffffff;
+        last = (end - 1) >> shift;
     }
-    __device__ __forceinline__ void load(const AttnArgs& a, const char* kp, const char* vp, int t0, int tid) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int row = (t0 + (kThreads * i + tid) / P) & (a.cache.page_size - 1);
-            k[i] = v[i] = make_uint4(0, 0, 0, 0);
-            if (page[i] >= 0 && page[i] < a.cache.n_pages) {
-                const int at = tid % P * 16;
-                k[i] = *reinterpret_cast<const uint4*>(
-                    kp + (page[i] * a.cache.k_page_stride + row * a.cache.k_row_stride) * size + at);
-                v[i] = *reinterpret_cast<const uint4*>(
-                    vp + (page[i] * a.cache.v_page_stride + row * a.cache.v_row_stride) * size + at);
-            }
+    __device__ __forceinline__ void cover(const int32_t* table, int from, int to, int lane) {
+        if (from < first || to >= first + 64) {
+            first = from;
+            ids = table[min(first + lane, last)];
         }
-    }
-    // With `check`, returns whether a value among the thread's is not finite.
-    __device__ __forceinline__ bool store(uint4* klds, uint4* vlds, int tid, bool check) const {
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int r = (kThreads * i + tid) / P, p = tid % P;
-            uint4 x[2] = {v[i]};
-            if constexpr (F8) {
-                uint4 y[2];
-                e4m3_to_bf16(k[i], y[0], y[1]);
-                klds[k_piece<D>(r, 2 * p)] = y[0];
-                klds[k_piece<D>(r, 2 * p + 1)] = y[1];
-                e4m3_to_bf16(v[i], x[0], x[1]);
-                vlds[v_piece<D>(r, 2 * p)] = x[0];
-                vlds[v_piece<D>(r, 2 * p + 1)] = x[1];
-            } else {
-                klds[k_piece<D>(r, p)] = k[i];
-                vlds[v_piece<D>(r, p)] = x[0];
-            }
-            if (!check) continue;
-#pragma unroll
-            for (int j = 0; j < (F8 ? 2 : 1); ++j) {
-                const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    odd |= (u[w] & 0x7f80u) == 0x7f80u || (u[w] & 0x7f800000u) == 0x7f800000u;
-            }
-        }
-        return odd;
     }
 };
+
+// Rows of K or V on their way from memory to LDS.  Wavefront w brings rows
+// 16 w .. 16 w + 15 of a tile.  Rows behind the last token hold what lies there
+// in the last page, rows of pages outside the pool what the first page holds;
+// both are masked.  bf16 goes straight to LDS (a load fills 64 pieces in the
+// order of the lanes, so the permutation of a row's pieces is made in the
+// address), e4m3 through registers, where it becomes bf16.
+template <int D, bool F8, bool IS_V>
+struct Stage {
+    static constexpr int P = D / (F8 ? 16 : 8);  // 16-byte pieces of a row
+    static constexpr int L = 16 * P / 64;        // loads of a wavefront
+    static constexpr int size = F8 ? 1 : 2;
+    const char* pool;  // of the key head
+    int64_t page_stride;
+    int row_stride;  // bytes
+    PageWindow window;
+    uint4 x[F8 ? L : 1];
+
+    __device__ __forceinline__ void init(const AttnArgs& a, int h, int end) {
+        const gdn_kv_cache& c = a.cache;
+        pool = static_cast<const char*>(IS_V ? c.v : c.k) + h * (IS_V ? c.v_head_stride : c.k_head_stride) * size;
+        page_stride = (IS_V ? c.v_page_stride : c.k_page_stride) * size;
+        row_stride = int(IS_V ? c.v_row_stride : c.k_row_stride) * size;
+        window.open(end, a.page_shift);
+    }
+    __device__ __forceinline__ static int perm(int r) { return F8 ? 0 : IS_V ? v_xor<D>(r) : k_xor<D>(r); }
+
+    __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
+                                         int lane) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass rejects the 16-byte forms
+        t0 += 16 * wave;
+        const int from = min(t0, end - 1) >> a.page_shift, to = min(t0 + 15, end - 1) >> a.page_shift;
+        window.cover(table, from, to, lane);
+        lds += 16 * wave * (D / 8);
+        const uint32_t to_lds = __builtin_amdgcn_readfirstlane(lds_address(lds));
+        if (a.page_shift >= 4) {  // the 16 rows lie in one page
+            int page = __builtin_amdgcn_readlane(window.ids, from - window.first);
+            if (page < 0 || page >= a.cache.n_pages) page = 0;
+            const char* base = pool + page * page_stride + int64_t(t0 & (a.cache.page_size - 1)) * row_stride;
+            const uint64_t bits = reinterpret_cast<uint64_t>(base);
+            const i32x4 rsrc{int32_t(bits), int32_t(bits >> 32 & 0xffff), 0x7fffffff, 0x00027000};
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int r = (64 * j + lane) / P;
+                const int off = r * row_stride + ((lane % P ^ perm(r)) << 4);
+                if constexpr (F8)
+                    x[j] = *reinterpret_cast<const uint4*>(base + off);
+                else
+                    load_to_lds(rsrc, off, to_lds + 1024 * j);
+            }
+        } else {
+            lane = fresh(lane);
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int r = (64 * j + lane) / P, t = t0 + r;
+                int page = __shfl(window.ids, (min(t, end - 1) >> a.page_shift) - window.first);
+                if (page < 0 || page >= a.cache.n_pages) page = 0;
+                const char* at = pool + page * page_stride + int64_t(t & (a.cache.page_size - 1)) * row_stride +
+                                 ((lane % P ^ perm(r)) << 4);
+                if constexpr (F8)
+                    x[j] = *reinterpret_cast<const uint4*>(at);
+                else
+                    load_to_lds(at, to_lds + 1024 * j);
+            }
+        }
+#endif
+    }
+    // e4m3: what load() brought, into LDS as bf16.
+    __device__ __forceinline__ void store(uint4* lds, int wave, int lane) const {
+        if constexpr (F8) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int r = 16 * wave + (64 * j + lane) / P, p = 2 * (lane % P);
+                const int perm_r = IS_V ? v_xor<D>(r) : k_xor<D>(r);
+                uint4 lo, hi;
+                e4m3_to_bf16(x[j], lo, hi);
+                lds[r * (D / 8) + (p ^ perm_r)] = lo;
+                lds[r * (D / 8) + (p + 1 ^ perm_r)] = hi;
+            }
+        }
+    }
+};
+
+// Whether any of the thread's share of a tile of V is not finite.
+template <int D>
+__device__ __forceinline__ bool any_odd(const uint4* v, int tid) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kKeys * D / 8 / kThreads; ++i) {
+        const uint4 x = v[i * kThreads + tid];
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) odd |= (u[w] & 0x7f80u) == 0x7f80u || (u[w] & 0x7f800000u) == 0x7f800000u;
+    }
+    return odd;
+}
 
 // Bits of the 32 tokens from t0 on that the query may see.
 template <AttnKind KIND>
@@ -131,22 +225,27 @@ __device__ __forceinline__ uint32_t visible(const AttnArgs& a, const AttnSeq& s,
     }
 }
 
-// V's elements that are not finite, as ones: of kind 0 NaN, 1 +inf, 2 -inf.
-__device__ __forceinline__ uint32_t marks_of(uint32_t u, int kind) {
-    uint32_t r = 0;
+// A tile of V in LDS, rewritten by the workgroup: kind 0 with zeros for what is
+// not finite, else ones where it is NaN (1), +inf (2), -inf (3) and zeros elsewhere.
+template <int D>
+__device__ __forceinline__ void rewrite(uint4* v, int kind, int tid) {
+#pragma unroll 1
+    for (int i = tid; i < kKeys * D / 8; i += kThreads) {
+        uint4 x = v[i];
+        uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-        const uint32_t x = u >> h & 0xffff;
-        const bool is = kind == 0 ? (x & 0x7fff) > 0x7f80 : x == (kind == 1 ? 0x7f80u : 0xff80u);
-        if (is) r |= 0x3f80u << h;
+        for (int w = 0; w < 4; ++w) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int at = 0; at < 32; at += 16) {
+                const uint32_t e = u[w] >> at & 0xffff;
+                const int is = (e & 0x7f80) != 0x7f80 ? 0 : (e & 0x7f) ? 1 : e == 0x7f80 ? 2 : 3;
+                r |= (kind == 0 ? (is ? 0 : e) : is == kind ? 0x3f80u : 0) << at;
+            }
+            u[w] = r;
+        }
+        v[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    return r;
-}
-// V's elements with zeros for those.
-__device__ __forceinline__ uint32_t finite_of(uint32_t u) {
-    if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-    if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
-    return u;
 }
 
 // ---------------------------------------------------------------------------
@@ -167,22 +266,19 @@ template <AttnKind KIND, int D, bool F8>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnArgs a) {
     extern __shared__ uint4 lds_raw[];
     TileLds<D>& lds = *reinterpret_cast<TileLds<D>*>(lds_raw);
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = a.cache.H_kv;
     const int64_t wg = block_id(), grid_items = int64_t(gridDim.x) * gridDim.y / heads;
     if (wg >= grid_items * heads) return;
     const int h = int(wg % heads);
-    const int c = attn_chunk<KIND>(a, lane);
-    constexpr int size = F8 ? 1 : 2;
-    const char* kp = static_cast<const char*>(a.cache.k) + h * a.cache.k_head_stride * size;
-    const char* vp = static_cast<const char*>(a.cache.v) + h * a.cache.v_head_stride * size;
+    const int c = attn_chunk<KIND>(a, threadIdx.x & 63);
     const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
     const float inf = __builtin_inff();
 
     AttnItem it;
-    for (int64_t item = wg / heads; attn_item<KIND, false>(a, c, item, lane, it); item += grid_items) {
-        const AttnSeq s = attn_seq<KIND>(a, it.b);
+    for (int64_t item = wg / heads; attn_item<KIND, false>(a, c, item, threadIdx.x & 63, it); item += grid_items) {
+        const int tid = fresh(threadIdx.x), lane = tid & 63, col = lane & 31, half = lane >> 5;
+        const AttnSeq s = attn_seq_uniform<KIND>(a, it.b);
         const int all_rows = s.n * a.group;
         const int row0 = it.tile * kTileRows, rows = min(kTileRows, all_rows - row0);
         // the last of the tile's tokens sees most
@@ -206,8 +302,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             const int page = table[p];
             missing |= page < 0 || page >= a.cache.n_pages;
         }
-        missing = __syncthreads_or(missing);
-        auto is_masked = [&](int t0) { return missing || t0 + kKeys > min(open_end, end); };
+        missing = __builtin_amdgcn_readfirstlane(__syncthreads_or(missing));
 
         bf16x8 q[D / 16];
         const uint16_t* qp = a.q + (s.row0 + token) * a.d.q_stride + int64_t(head) * D + 8 * half;
@@ -221,136 +316,198 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             for (int j = 0; j < 16; ++j) o[n][j] = 0.0f;
         float m = -inf, l = 0.0f;  // m: what the powers are taken against
 
-        Stage<D, F8> st;
-        int odd = 0;
-        if (begin < end) {
-            st.pages(a, table, begin, end, tid);
-            st.load(a, kp, vp, begin, tid);
-            st.pages(a, table, begin + kKeys, end, tid);
-            odd = __syncthreads_or(st.store(lds.k[0], lds.v[0], tid, is_masked(begin)));
-        }
-        for (int t0 = begin, buf = 0; t0 < end; t0 += kKeys, buf ^= 1) {
-            const bool more = t0 + kKeys < end;
-            if (more) {
-                st.load(a, kp, vp, t0 + kKeys, tid);
-                st.pages(a, table, t0 + 2 * kKeys, end, tid);
-            }
-            const bool masked = is_masked(t0);
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    see[j] = visible<KIND>(a, s, token, anc, t0 + 32 * j, end);
-                    if (missing) {
-                        const int t = t0 + 32 * j + col;
-                        const int page = t < end ? table[t >> a.page_shift] : -1;
-                        see[j] &= uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
-                    }
-                }
-            }
-            if (!masked || __ballot((see[0] | see[1]) != 0)) {
-                f32x16 x[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[j][i] = 0.0f;
-#pragma unroll
-                    for (int n = 0; n < D / 16; ++n)
-                        x[j] = mfma32(load_frag(lds.k[buf] + k_piece<D>(32 * j + col, 2 * n + half)), q[n], x[j]);
-                }
-                // register i of a lane: key 8 (i / 4) + 4 half + i % 4
-                float top = -inf;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (masked) {
-                        const uint32_t bits = see[j] >> (4 * half);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!(bits >> (8 * (i >> 2) + (i & 3)) & 1)) x[j][i] = -inf;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, x[j][i]);
-                }
-                // a scale of zero makes every visible score zero
-                top = fmaxf(top, __shfl_xor(top, 32));
-                top = top == -inf ? top : top * scale;
-                if (__ballot(top > m + 8.0f)) {
-                    const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
-                    m = m_new;
-                    l *= keep;
+        // register i of x[j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col`
+        auto k_frag = [&](int j, int n, int buf) {
+            const int r = 32 * j + col;
+            return load_frag(lds.k[buf] + r * (D / 8) + (2 * n + half ^ k_xor<D>(r)));
+        };
+        // k-slots 8 half .. 8 half + 7 of product k: keys 16 k + 4 half + {0 .. 3} and 8 more
+        const int vr = 4 * half + ((lane & 15) >> 2), vp = 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
+        auto v_frag = [&](int n, int k, int buf) {
+            const int r = 16 * k + vr;
+            const uint4* row = lds.v[buf] + r * (D / 8);  // row r + 8 has the same permutation
+            const char* at = reinterpret_cast<const char*>(row + (4 * n + vp ^ v_xor<D>(r))) + 8 * (lane & 1);
+            const uint2 u = read_tr16(at), w = read_tr16(at + 8 * D * 2);
+            return __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
+        };
+        const f32x16 zero{};
+        // The largest of what x adds to a row, in powers of two.
+        auto largest = [&](float top) {
+            const auto both = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, top),
+                                                               __builtin_bit_cast(uint32_t, top), false, false);
+            const uint32_t lo = both[0], hi = both[1];
+            top = fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+            return top == -inf ? top : top * scale;
+        };
+        auto raise = [&](float top) {
+            if (__ballot(top > m + 8.0f)) {
+                const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
+                m = m_new;
+                l *= keep;
+                if constexpr (D == 256) {
+                    scale_acc(o, keep);
+                } else {
 #pragma unroll
                     for (int n = 0; n < D / 32; ++n) o[n] *= keep;
                 }
+            }
+        };
+
+        if (begin < end) {
+            Stage<D, F8, false> sk;
+            Stage<D, F8, true> sv;
+            sk.init(a, h, end);
+            sv.init(a, h, end);
+            // V of the tile at t0 and K of the next one are in LDS, and those after them on their way.
+            auto arrive = [&](int t0, int buf) {
+                if (t0 + kKeys < end) sk.store(lds.k[buf ^ 1], wave, lane);
+                sv.store(lds.v[buf], wave, lane);
+                loads_barrier<0>();
+                if (t0 + 2 * kKeys < end) sk.load(a, table, lds.k[buf], t0 + 2 * kKeys, end, wave, lane);
+                if (t0 + kKeys < end) sv.load(a, table, lds.v[buf ^ 1], t0 + kKeys, end, wave, lane);
+            };
+            sk.load(a, table, lds.k[0], begin, end, wave, lane);
+            sk.store(lds.k[0], wave, lane);
+            loads_barrier<0>();
+            if (begin + kKeys < end) sk.load(a, table, lds.k[1], begin + kKeys, end, wave, lane);
+            sv.load(a, table, lds.v[0], begin, end, wave, lane);
+            constexpr int NQ = D / 8, AHEAD = 4;  // products of a tile with K (and with V), operands read ahead
+            f32x16 x[2];                          // scores of the tile at t0
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) x[i & 1] = mfma32(k_frag(i & 1, i >> 1, 0), q[i >> 1], i < 2 ? zero : x[i & 1]);
+            int t0 = begin, buf = 0;
+
+            // Tiles that every row sees all of, but the last: the scores of the
+            // next tile are formed beside the powers of this one and its maxima
+            // beside the products with V, step by step as they stand here.
+            const int open = missing ? begin : min(max(open_end, begin), end - 1);
+            float top = -inf;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
+            top = largest(top);
+            for (; t0 + kKeys <= open; t0 += kKeys, buf ^= 1) {
+                arrive(t0, buf);
+                raise(top);
                 const float base = finite_max(m);
-                bf16x8 p[4];
+                f32x16 y[2];
+                bf16x8 f[AHEAD], p[4];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) f[i] = k_frag(i & 1, i >> 1, buf ^ 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    y[i & 1] = mfma32(f[i % AHEAD], q[i >> 1], i < 2 ? zero : y[i & 1]);
+                    const int r = i + AHEAD;
+                    f[i % AHEAD] = r < NQ ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NQ) % (D / 32), (r - NQ) / (D / 32), buf);
+#pragma unroll
+                    for (int e = i * 32 / NQ; e < (i + 1) * 32 / NQ; ++e) {
+                        const float w = exp2_fast(fmaf(x[e >> 4][e & 15], scale, -base));
+                        l += w;
+                        p[e >> 3][e & 7] = static_cast<__bf16>(w);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                top = -inf;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    o[i % (D / 32)] = mfma32(f[i % AHEAD], p[i / (D / 32)], o[i % (D / 32)]);
+                    const int r = i + AHEAD;
+                    if (r < NQ) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
+                    if (i >= NQ / 2) {
+#pragma unroll
+                        for (int e = (i - NQ / 2) * 64 / NQ; e < (i - NQ / 2 + 1) * 64 / NQ; ++e)
+                            top = fmaxf(top, y[e >> 4][e & 15]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                top = largest(top);
+                x[0] = y[0];
+                x[1] = y[1];
+            }
+            for (; t0 < end; t0 += kKeys, buf ^= 1) {
+                arrive(t0, buf);
+                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+                bool odd = false;
+                if (missing || t0 + kKeys > min(open_end, end)) {
+                    odd = __builtin_amdgcn_readfirstlane(__syncthreads_or(any_odd<D>(lds.v[buf], tid)));
+                    if (odd) {
+                        rewrite<D>(lds.v[buf], 0, tid);
+                        __syncthreads();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t bits = visible<KIND>(a, s, token, anc, t0 + 32 * j, end);
+                        if (missing) {
+                            const int t = t0 + 32 * j + col;
+                            const int page = t < end ? table[t >> a.page_shift] : -1;
+                            bits &= uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
+                        }
+                        see[j] = bits >> (4 * half);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float y = exp2_fast(fmaf(x[j][i], scale, -base));
-                        if (masked && x[j][i] == -inf) y = 0.0f;
-                        l += y;
-                        p[2 * j + (i >> 3)][i & 7] = static_cast<__bf16>(y);
+                    for (int i = 0; i < 16; ++i)
+                        if (!(see[j] >> (8 * (i >> 2) + (i & 3)) & 1)) x[j][i] = -inf;
+                top = -inf;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
+                raise(largest(top));
+                const float base = finite_max(m);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bf16x8 p;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 8 * (k & 1) + i;
+                        float e = exp2_fast(fmaf(x[k >> 1][r], scale, -base));
+                        // a scale of zero turns -inf into NaN
+                        if (!(see[k >> 1] >> (8 * (r >> 2) + (r & 3)) & 1)) e = 0.0f;
+                        l += e;
+                        p[i] = static_cast<__bf16>(e);
                     }
-                // k-slots 8 half .. 8 half + 7 of product s: keys 16 s + 4 half + {0 .. 3} and 8 more
-                const int vr = 4 * half + ((lane & 15) >> 2), vp0 = 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
-                auto v_frag = [&](int n, int k) {
-                    const int r = 16 * k + vr, piece = 4 * n + vp0;
-                    const char* at0 = reinterpret_cast<const char*>(lds.v[buf] + v_piece<D>(r, piece)) + 8 * (lane & 1);
-                    const char* at1 = reinterpret_cast<const char*>(lds.v[buf] + v_piece<D>(r + 8, piece)) + 8 * (lane & 1);
-                    const uint2 u = read_tr16(at0), w = read_tr16(at1);
-                    return make_uint4(u.x, u.y, w.x, w.y);
-                };
-                if (!(masked && odd)) {
 #pragma unroll
-                    for (int n = 0; n < D / 32; ++n)
+                    for (int n = 0; n < D / 32; ++n) o[n] = mfma32(v_frag(n, k, buf), p, o[n]);
+                }
+                if (t0 + kKeys < end) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[n] = mfma32(__builtin_bit_cast(bf16x8, v_frag(n, k)), p[k], o[n]);
-                } else {
-                    bf16x8 one[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 8 * (k & 1) + i;  // register of x[k >> 1]
-                            one[k][i] = static_cast<__bf16>(
-                                (see[k >> 1] >> (4 * half) >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
-                        }
+                    for (int i = 0; i < NQ; ++i)
+                        x[i & 1] = mfma32(k_frag(i & 1, i >> 1, buf ^ 1), q[i >> 1], i < 2 ? zero : x[i & 1]);
+                }
+                if (!odd) continue;
+#pragma unroll 1
+                for (int kind = 1; kind <= 3; ++kind) {
+                    const float what = kind == 1 ? __builtin_nanf("") : kind == 2 ? inf : -inf;
+                    __syncthreads();
+                    Stage<D, F8, true> again = sv;
+                    again.load(a, table, lds.v[buf], t0, end, wave, lane);
+                    again.store(lds.v[buf], wave, lane);
+                    loads_barrier<0>();
+                    rewrite<D>(lds.v[buf], kind, tid);
+                    __syncthreads();
 #pragma unroll
                     for (int n = 0; n < D / 32; ++n) {
+                        f32x16 count;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) count[i] = 0.0f;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint4 u = v_frag(n, k);
-                            o[n] = mfma32(__builtin_bit_cast(bf16x8, make_uint4(finite_of(u.x), finite_of(u.y), finite_of(u.z),
-                                                                                finite_of(u.w))),
-                                          p[k], o[n]);
-                        }
-                        for (int kind = 0; kind < 3; ++kind) {
-                            f32x16 count;
+                            uint32_t bits = see[k >> 1];
+                            asm volatile("" : "+v"(bits));  // formed anew each time, to hold no registers for it
+                            bf16x8 one;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) count[i] = 0.0f;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint4 u = v_frag(n, k);
-                                count = mfma32(__builtin_bit_cast(bf16x8, make_uint4(marks_of(u.x, kind), marks_of(u.y, kind),
-                                                                                     marks_of(u.z, kind), marks_of(u.w, kind))),
-                                               one[k], count);
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = 8 * (k & 1) + i;
+                                one[i] = static_cast<__bf16>((bits >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
                             }
-                            const float what = kind == 0 ? __builtin_nanf("") : kind == 1 ? inf : -inf;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (count[i] > 0.0f) o[n][i] += what;
+                            count = mfma32(v_frag(n, k, buf), one, count);
                         }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (count[i] > 0.0f) o[n][i] += what;
                     }
                 }
-            }
-            if (more) {
-                const bool check = is_masked(t0 + kKeys);
-                odd = st.store(lds.k[buf ^ 1], lds.v[buf ^ 1], tid, check);
-                if (check)
-                    odd = __syncthreads_or(odd);
-                else
-                    __syncthreads();
             }
         }
 

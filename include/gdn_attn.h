@@ -44,8 +44,9 @@ extern "C" {
 /* One layer's cache: pools of pages of keys and of values.  Key j of head h
  * of row r of page p lies at k + p k_page_stride + r k_row_stride +
  * h k_head_stride + j, a value likewise; the d elements of a head are dense.
- * The strides are in elements, >= 0 and multiples of 16 bytes; any order of
- * pages, rows and heads can be described, also keys and values in one pool.
+ * The strides are in elements, >= 0 and multiples of 16 bytes, those of rows
+ * at most GDN_MAX_SEQ_STRIDE; any order of pages, rows and heads can be
+ * described, also keys and values in one pool.
  * No two (page, row, head) may share memory in a call that writes. */
 typedef struct {
     void* k;              /* 16-byte aligned                                     */

@@ -72,7 +72,7 @@ BAD_CACHE = [
     (dict(n_pages=0), "GDN_ERR_SHAPE"), (dict(page_size=0), "GDN_ERR_SHAPE"), (dict(page_size=24), "GDN_ERR_SHAPE"),
     (dict(page_size=131072), "GDN_ERR_SHAPE"), (dict(page_size=-16), "GDN_ERR_SHAPE"),
     (dict(n_pages=1 << 20, page_size=4096), "GDN_ERR_SHAPE"), (dict(H_kv=0), "GDN_ERR_SHAPE"), (dict(H_kv=65536), "GDN_ERR_SHAPE"),
-    (dict(reserved=1), "GDN_ERR_SHAPE"), (dict(k_page_stride=-8), "GDN_ERR_SHAPE"), (dict(v_row_stride=1 << 41), "GDN_ERR_SHAPE"),
+    (dict(reserved=1), "GDN_ERR_SHAPE"), (dict(k_page_stride=-8), "GDN_ERR_SHAPE"), (dict(v_row_stride=1 << 41), "GDN_ERR_SHAPE"), (dict(k_row_stride=(1 << 24) + 8), "GDN_ERR_SHAPE"),
     (dict(k_row_stride=4), "GDN_ERR_ALIGN"), (dict(v_head_stride=130), "GDN_ERR_ALIGN"), (dict(dtype=2, k_head_stride=136), "GDN_ERR_ALIGN"),
     (dict(k=None), "GDN_ERR_NULL"), (dict(v=None), "GDN_ERR_NULL"), (dict(k=FAKE + 8), "GDN_ERR_ALIGN"), (dict(v=FAKE + 2), "GDN_ERR_ALIGN"),
     (dict(k_scale=FAKE + 2), "GDN_ERR_ALIGN"), (dict(v_scale=FAKE + 1), "GDN_ERR_ALIGN"),
