@@ -139,7 +139,7 @@ gdn_status run(gdn::AttnArgs& a, size_t workspace_bytes, hipStream_t stream, con
             GDN_TRY(check_ptr(a.ws, 256, "workspace"));
         }
         hipError_t e = a.kind == gdn::kAttnDecode ? gdn::launch_attn_decode(a, stream) : gdn::launch_attn_tiles(a, stream);
-        if (e == hipSuccess && a.part_tiles > 0) e = gdn::launch_attn_join(a, stream);
+        if (e == hipSuccess && a.join) e = gdn::launch_attn_join(a, stream);
         if (e != hipSuccess) return done(e, what);
     }
     return done(a.seq_status ? gdn::launch_attn_status(a, stream) : hipSuccess, what);

@@ -14,6 +14,7 @@ namespace gdn {
 namespace {
 
 constexpr int kWaves = 4, kStep = 32;  // wavefronts of a workgroup, keys of a wavefront's step
+constexpr int kUnit = kWaves * kStep;  // keys of a unit of work
 
 // Position of the 16-byte piece p of row r of a wavefront's V tile: a
 // transposing read takes 32 bytes each of 8 rows at a time, which this spreads
@@ -24,8 +25,8 @@ __device__ __forceinline__ int v_piece(int r, int p) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup: one chunk of one sequence's keys, one key head, up to 16 of
-// its query heads.  Each wavefront takes every fourth step of 32 keys with a
+// A piece of a workgroup's range: some of one sequence's keys, one key head, up
+// to 16 of its query heads.  Each wavefront takes every fourth step of 32 keys with a
 // running maximum and sum of its own; the four are joined at the end.
 //   S^T = K Q^T   keys x heads on MFMA: K from memory straight as operand
 //   O^T += V^T P  V through the wavefront's LDS rows, read transposed; the
@@ -100,128 +101,134 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int heads = a.cache.H_kv * a.head_tiles;
-    const int64_t wg = block_id();
-    const int hh = int(wg % heads), h = hh / a.head_tiles, head0 = (hh - h * a.head_tiles) * kDecodeRows;
-    const int rows = min(a.group - head0, kDecodeRows);
-    const int64_t q_head = int64_t(h) * a.group + head0;
-    const int c = attn_chunk<kAttnDecode>(a, lane);
-    constexpr int size = F8 ? 1 : 2;
-    const char* kp = static_cast<const char*>(a.cache.k) + h * a.cache.k_head_stride * size;
-    const char* vp = static_cast<const char*>(a.cache.v) + h * a.cache.v_head_stride * size;
-    const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
+    const AttnPlan plan = attn_plan<kAttnDecode>(a, lane);
+    const int w = attn_range(plan, blockIdx.x);
+    const int64_t u0 = w * plan.per, u_end = min(u0 + plan.per, plan.units * heads);
     const float inf = __builtin_inff();
+    AttnPlace at;
+    for (int64_t u = u0; u < u_end;) {
+        const int hh = int(quotient(u, plan.units)), h = hh / a.head_tiles, head0 = (hh - h * a.head_tiles) * kDecodeRows;
+        const int64_t uh = u - hh * plan.units;
+        if (at.b < 0 || uh < at.first || uh >= at.first + at.count) attn_find<kAttnDecode, false>(a, uh, lane, at);
+        const AttnSeq s = attn_seq_uniform<kAttnDecode>(a, at.b);
+        const AttnPiece it = attn_piece<kAttnDecode>(a, s, 1, uh - at.first, u_end - u);
+        const int rows = min(a.group - head0, kDecodeRows);
+        const int64_t q_head = int64_t(h) * a.group + head0;
+        constexpr int size = F8 ? 1 : 2;
+        const char* kp = static_cast<const char*>(a.cache.k) + h * a.cache.k_head_stride * size;
+        const char* vp = static_cast<const char*>(a.cache.v) + h * a.cache.v_head_stride * size;
+        const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
+        const int begin = it.unit * kUnit, end = min(begin + it.units * kUnit, s.keys);
+        const int32_t* table = a.table + at.b * a.d.table_stride;
 
-    AttnItem it;
-    if (!attn_item<kAttnDecode, false>(a, c, wg / heads, lane, it)) return;
-    const AttnSeq s = attn_seq_uniform<kAttnDecode>(a, it.b);
-    const int begin = it.chunk * c, end = min(begin + c, s.keys);
-    const int32_t* table = a.table + it.b * a.d.table_stride;
+        bf16x8 q[D / 32];
+        const uint16_t* qp = a.q + at.b * a.d.q_stride + (q_head + min(col, rows - 1)) * D;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) q[n] = load_frag(qp + k_column<D, F8>(n, g));
 
-    bf16x8 q[D / 32];
-    const uint16_t* qp = a.q + it.b * a.d.q_stride + (q_head + min(col, rows - 1)) * D;
+        f32x4 o[D / 16];
 #pragma unroll
-    for (int n = 0; n < D / 32; ++n) q[n] = load_frag(qp + k_column<D, F8>(n, g));
+        for (int n = 0; n < D / 16; ++n) o[n] = f32x4{0, 0, 0, 0};
+        float m = -inf, l = 0.0f;
 
-    f32x4 o[D / 16];
+        Step<D, F8> cur;
+        int t0 = begin + wave * kStep;
+        if (t0 < end) cur.load(a, kp, vp, table, t0, end, lane);
+        for (; t0 < end; t0 += kWaves * kStep) {
+            cur.store_v(vlds[wave], lane);
+            const uint32_t ok = cur.ok;
+            f32x4 sc[2];
 #pragma unroll
-    for (int n = 0; n < D / 16; ++n) o[n] = f32x4{0, 0, 0, 0};
-    float m = -inf, l = 0.0f;
-
-    Step<D, F8> cur;
-    int t0 = begin + wave * kStep;
-    if (t0 < end) cur.load(a, kp, vp, table, t0, end, lane);
-    for (; t0 < end; t0 += kWaves * kStep) {
-        cur.store_v(vlds[wave], lane);
-        const uint32_t ok = cur.ok;
-        f32x4 sc[2];
+            for (int j = 0; j < 2; ++j) {
+                sc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sc[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < Step<D, F8>::KL; ++i) {
-                if constexpr (F8) {
-                    uint4 lo, hi;
-                    e4m3_to_bf16(cur.k[j][i], lo, hi);
-                    sc[j] = mfma(__builtin_bit_cast(bf16x8, lo), q[2 * i], sc[j]);
-                    sc[j] = mfma(__builtin_bit_cast(bf16x8, hi), q[2 * i + 1], sc[j]);
-                } else {
-                    sc[j] = mfma(__builtin_bit_cast(bf16x8, cur.k[j][i]), q[i], sc[j]);
+                for (int i = 0; i < Step<D, F8>::KL; ++i) {
+                    if constexpr (F8) {
+                        uint4 lo, hi;
+                        e4m3_to_bf16(cur.k[j][i], lo, hi);
+                        sc[j] = mfma(__builtin_bit_cast(bf16x8, lo), q[2 * i], sc[j]);
+                        sc[j] = mfma(__builtin_bit_cast(bf16x8, hi), q[2 * i + 1], sc[j]);
+                    } else {
+                        sc[j] = mfma(__builtin_bit_cast(bf16x8, cur.k[j][i]), q[i], sc[j]);
+                    }
                 }
             }
-        }
-        const int next = t0 + kWaves * kStep;
-        if (next < end) cur.load(a, kp, vp, table, next, end, lane);
+            const int next = t0 + kWaves * kStep;
+            if (next < end) cur.load(a, kp, vp, table, next, end, lane);
 
-        float x[8], top = -inf;
+            float x[8], top = -inf;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = sc[j >> 2][j & 3] * scale;
-            if (ok != 0xffffffffu && !(ok >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1)) x[j] = -inf;
-            top = fmaxf(top, x[j]);
-        }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m, top), base = finite_max(m_new);
-        const float keep = exp2_fast(m - base);
-        m = m_new;
-        l *= keep;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = exp2_fast(x[j] - base);
-            l += x[j];
-        }
-        bf16x8 hi, lo;
-        split8(x, hi, lo);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            const int r = 4 * g + (col >> 2), p = 2 * n + ((col >> 1) & 1);
-            const char* at0 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r, p)) + 8 * (col & 1);
-            const char* at1 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r + 16, p)) + 8 * (col & 1);
-            const uint2 u = read_tr16(at0), w = read_tr16(at1);
-            const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
-            f32x4 acc = o[n];
-            acc *= keep;
-            acc = mfma(vt, hi, acc);
-            o[n] = mfma(vt, lo, acc);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-
-    // the four wavefronts' parts, O as [head][4 elements], pieces permuted over the banks
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (lane < kDecodeRows) {
-        ml[wave][0][lane] = m;
-        ml[wave][1][lane] = l;
-    }
-    f32x4* mine = reinterpret_cast<f32x4*>(vlds[wave]);
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) mine[col * (D / 4) + ((4 * n + g) ^ (col & 7))] = o[n];
-    __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += kWaves * 64) {
-        const int r = i / (D / 4), p = i % (D / 4);
-        float top = -inf;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[w][0][r]);
-        f32x4 acc{0, 0, 0, 0};
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = exp2_fast(ml[w][0][r] - finite_max(top));
-            acc += reinterpret_cast<f32x4*>(vlds[w])[r * (D / 4) + (p ^ (r & 7))] * f;
-            sum += ml[w][1][r] * f;
-        }
-        if (it.chunks > 1) {
-            float* part = part_out(a, it.part + it.chunk, hh, kDecodeRows, D);
-            reinterpret_cast<f32x4*>(part)[i] = acc;
-            if (p == 0) {
-                part[kDecodeRows * D + r] = top;
-                part[kDecodeRows * (D + 1) + r] = sum;
+            for (int j = 0; j < 8; ++j) {
+                x[j] = sc[j >> 2][j & 3] * scale;
+                if (ok != 0xffffffffu && !(ok >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1)) x[j] = -inf;
+                top = fmaxf(top, x[j]);
             }
-        } else {
-            attn_store<D>(a, it.b, h, q_head + r, 4 * p, acc, sum);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m_new = fmaxf(m, top), base = finite_max(m_new);
+            const float keep = exp2_fast(m - base);
+            m = m_new;
+            l *= keep;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = exp2_fast(x[j] - base);
+                l += x[j];
+            }
+            bf16x8 hi, lo;
+            split8(x, hi, lo);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                const int r = 4 * g + (col >> 2), p = 2 * n + ((col >> 1) & 1);
+                const char* at0 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r, p)) + 8 * (col & 1);
+                const char* at1 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r + 16, p)) + 8 * (col & 1);
+                const uint2 u = read_tr16(lds_address(at0)), w = read_tr16(lds_address(at1));
+                const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
+                f32x4 acc = o[n];
+                acc *= keep;
+                acc = mfma(vt, hi, acc);
+                o[n] = mfma(vt, lo, acc);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
+
+        // the four wavefronts' parts, O as [head][4 elements], pieces permuted over the banks
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (lane < kDecodeRows) {
+            ml[wave][0][lane] = m;
+            ml[wave][1][lane] = l;
+        }
+        f32x4* mine = reinterpret_cast<f32x4*>(vlds[wave]);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) mine[col * (D / 4) + ((4 * n + g) ^ (col & 7))] = o[n];
+        __syncthreads();
+        for (int i = tid; i < rows * (D / 4); i += kWaves * 64) {
+            const int r = i / (D / 4), p = i % (D / 4);
+            float top = -inf;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[w][0][r]);
+            f32x4 acc{0, 0, 0, 0};
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = exp2_fast(ml[w][0][r] - finite_max(top));
+                acc += reinterpret_cast<f32x4*>(vlds[w])[r * (D / 4) + (p ^ (r & 7))] * f;
+                sum += ml[w][1][r] * f;
+            }
+            if (it.units < it.all) {
+                float* part = part_out(a, 2 * int64_t(w) + (u > u0), kDecodeRows, D);
+                reinterpret_cast<f32x4*>(part)[i] = acc;
+                if (p == 0) {
+                    part[kDecodeRows * D + r] = top;
+                    part[kDecodeRows * (D + 1) + r] = sum;
+                }
+            } else {
+                attn_store<D>(a, at.b, h, q_head + r, 4 * p, acc, sum);
+            }
+        }
+        u += it.units;
+        if (u < u_end) __syncthreads();  // the next piece overwrites what is joined here
     }
 }
 
@@ -237,9 +244,7 @@ hipError_t launch(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream) {
-    const int64_t chunks = ((int64_t(a.d.max_pages) << a.page_shift) + a.min_chunk - 1) / a.min_chunk;
-    const int64_t items = std::min(int64_t(a.spread) + a.d.B, a.d.B * std::max<int64_t>(chunks, 1));
-    const dim3 grid = grid_of(items * a.cache.H_kv * a.head_tiles);
+    const dim3 grid(a.slots);
     switch (a.cache.d) {
         case 64: return launch<64>(a, grid, stream);
         case 128: return launch<128>(a, grid, stream);

@@ -60,15 +60,14 @@ struct AttnArgs {
     int group;       // query heads of a key head
     int tile_rows;   // (token, head of the group) rows of a workgroup
     int head_tiles;  // decode: tiles of 16 heads that the group is cut into, else 1
-    int spread;      // workgroups of one (key head, head tile) that the keys are divided over
-    int min_chunk;   // keys of a workgroup at least; chunks are multiples of it
-    int part_tiles;  // parts of one (key head, head tile) in the workspace
+    int slots;       // workgroups that the units are divided over, a multiple of 8
+    int unit;        // keys of a unit
+    int min_units;   // of a workgroup
+    bool join;       // tiles may be divided
 };
-// The part of a tile's result over one chunk of keys: maxima, sums, and
-// unnormalised outputs.
-constexpr int kDecodeRows = 16, kTileRows = 128;
+constexpr int kDecodeRows = 16, kTileRows = 128;  // rows of a tile
 
-// Fills the derived members; false if the sizes leave nothing to do.
+// Fills the derived members.
 void attn_shape(AttnArgs& a);
 size_t attn_ws_bytes(const AttnArgs& a);
 

@@ -36,6 +36,7 @@ template <AttnKind KIND, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     constexpr int C = D / 4, K = kThreads / C;  // threads of a row, rows (or shares of the parts) at a time
     constexpr bool one = KIND == kAttnDecode;
+    constexpr int rows_of_part = one ? kDecodeRows : kTileRows;
     __shared__ f32x4 share[one ? K : 1][C];
     __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63, p = tid % C, k = tid / C;
@@ -44,19 +45,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     const int64_t wg = block_id(), grid_tiles = int64_t(gridDim.x) * gridDim.y / heads / blocks;
     if (wg >= grid_tiles * heads * blocks) return;
     const int block = int(wg % blocks), hh = int(wg / blocks % heads), h = hh / a.head_tiles;
-    const int c = attn_chunk<KIND>(a, lane);
-    AttnItem it;
-    for (int64_t tile = wg / blocks / heads; attn_item<KIND, true>(a, c, tile, lane, it); tile += grid_tiles) {
-        if (it.chunks > 1) {
-            const AttnSeq s = attn_seq_uniform<KIND>(a, it.b);
+    const AttnPlan plan = attn_plan<KIND>(a, lane);
+    AttnPlace at;
+    for (int64_t tile = wg / blocks / heads; attn_find<KIND, true>(a, tile, lane, at); tile += grid_tiles) {
+        const AttnSeq s = attn_seq_uniform<KIND>(a, at.b);
+        const int t = int(tile - at.first), tiles = int(at.count);
+        const int64_t g0 = hh * plan.units + at.first_unit + attn_tile_unit<KIND>(a, s, tiles, t);
+        const int64_t w0 = quotient(g0, plan.per), w1 = quotient(g0 + attn_units<KIND>(a, s, t) - 1, plan.per);
+        const int parts = int(w1 - w0) + 1;
+        // the first workgroup either starts with this tile or has it as its last
+        auto part = [&](int i) {
+            return part_out(a, i ? 2 * (w0 + i) : 2 * w0 + (g0 == w0 * plan.per ? 0 : 1), rows_of_part, D);
+        };
+        if (parts > 1) {
             if constexpr (one) {
                 const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
                 if (row < a.group - head0) {
                     Joined x;
-                    for (int i = k; i < it.chunks; i += K) {
-                        const float* part = part_out(a, it.part + i, hh, kDecodeRows, D);
-                        x.add(*reinterpret_cast<const f32x4*>(part + row * D + 4 * p), part[kDecodeRows * D + row],
-                              part[kDecodeRows * (D + 1) + row]);
+                    for (int i = k; i < parts; i += K) {
+                        const float* y = part(i);
+                        x.add(*reinterpret_cast<const f32x4*>(y + row * D + 4 * p), y[kDecodeRows * D + row],
+                              y[kDecodeRows * (D + 1) + row]);
                     }
                     share[k][p] = x.acc;
                     if (p == 0) {
@@ -70,16 +79,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
                     }
                 }
             } else {
-                const int row0 = it.tile * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
-                const int last_token = (row0 + rows - 1) / a.group;
-                const int seen = KIND == kAttnPrefill ? min(max(s.prefix + last_token + 1, 0), s.keys) : s.keys;
-                const int chunks = max((seen + c - 1) / c, 1);
-                for (int r = block * kJoinRows + k; chunks > 1 && r < min((block + 1) * kJoinRows, rows); r += K) {
+                const int row0 = t * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
+                for (int r = block * kJoinRows + k; r < min((block + 1) * kJoinRows, rows); r += K) {
                     Joined x;
-                    for (int i = 0; i < chunks; ++i) {
-                        const float* part = part_out(a, it.part + i, hh, kTileRows, D);
-                        x.add(*reinterpret_cast<const f32x4*>(part + r * D + 4 * p), part[kTileRows * D + r],
-                              part[kTileRows * (D + 1) + r]);
+                    for (int i = 0; i < parts; ++i) {
+                        const float* y = part(i);
+                        x.add(*reinterpret_cast<const f32x4*>(y + r * D + 4 * p), y[kTileRows * D + r],
+                              y[kTileRows * (D + 1) + r]);
                     }
                     const int token = (row0 + r) / a.group;
                     attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, 4 * p, x.acc, x.l);
@@ -130,10 +136,6 @@ int64_t max_tiles(const AttnArgs& a) {
            : a.kind == kAttnVerify ? a.d.B * ((rows + kTileRows - 1) / kTileRows)
                                    : rows / kTileRows + a.d.B;
 }
-int64_t max_chunks(const AttnArgs& a) {
-    return ((int64_t(a.d.max_pages) << a.page_shift) + a.min_chunk - 1) / a.min_chunk;
-}
-
 }  // namespace
 
 void attn_shape(AttnArgs& a) {
@@ -143,17 +145,19 @@ void attn_shape(AttnArgs& a) {
     const bool one = a.kind == kAttnDecode;
     a.tile_rows = one ? kDecodeRows : kTileRows;
     a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
-    a.min_chunk = one ? 128 : 256;
-    a.spread = std::max(1, 2 * kCu / (a.cache.H_kv * a.head_tiles));
-    const int64_t chunks = max_chunks(a);
-    // prompts may overlap (where cu_seqlens decreases), and each may then have all rows
-    const int64_t tiles = a.kind == kAttnPrefill ? a.d.B * ((int64_t(a.d.T) * a.group + kTileRows - 1) / kTileRows) : max_tiles(a);
-    a.part_tiles = chunks <= 1 ? 0 : int(std::min<int64_t>(2 * a.spread, tiles * chunks));
+    a.unit = one ? 128 : 64;
+    a.min_units = one ? 1 : 4;
+    const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
+    // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
+    // overlap, where cu_seqlens decreases, and each may then have all rows)
+    const int64_t tiles = one ? a.d.B : a.d.B * ((rows + kTileRows - 1) / kTileRows);
+    const int64_t units = tiles * a.cache.H_kv * a.head_tiles * ((cap + a.unit - 1) / a.unit + 2);
+    a.slots = int(std::min<int64_t>(a.cache.d == 256 ? kCu : 2 * kCu, ((units + a.min_units - 1) / a.min_units + 7) / 8 * 8));
+    a.join = cap > a.unit;  // otherwise a tile is one unit
 }
 
 size_t attn_ws_bytes(const AttnArgs& a) {
-    const size_t part = size_t(a.tile_rows) * (a.cache.d + 2) * sizeof(float);
-    return (size_t(a.part_tiles) * a.cache.H_kv * a.head_tiles * part + 255) & ~size_t(255);
+    return a.join ? size_t(2 * a.slots) * a.tile_rows * (a.cache.d + 2) * sizeof(float) : 0;
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {

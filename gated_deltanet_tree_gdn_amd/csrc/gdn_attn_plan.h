@@ -1,14 +1,17 @@
-// gdn_attn_plan.h -- which keys of which sequence a workgroup of the attention
-// kernels takes, and where it leaves its part of the result.
+// gdn_attn_plan.h -- which keys of which queries a workgroup of the attention
+// kernels takes, and where it leaves its part of a result.
 //
-// Lengths are on the device, so the division is made there, by every
-// wavefront for itself: a tile's work is its sequence's keys, the keys are cut
-// into chunks of
-//     c = max(min_chunk, sum over tiles of keys / spread)
-// (a multiple of min_chunk), and the items (tile, chunk) are numbered through
-// the sequences.  That gives at most spread + tiles items of at most c keys,
-// however uneven the lengths are, and of those that are one of several chunks
-// of their tile at most 2 spread, which is what the workspace has room for.
+// The work is numbered in units of `unit` keys of one tile of rows: through the
+// tiles of a sequence, the sequences, then the key heads.  Workgroup w takes
+// units w per .. (w + 1) per - 1, with per = max(min_units, all / slots), so the
+// workgroups that fit the GPU at once (`slots`) have the same work however
+// uneven the lengths are, and nothing has to be known on the host.  A range
+// covers any number of whole tiles, whose results are final, and at most two
+// tiles in part (one where it starts, one where it ends), whose results go to
+// parts 2 w and 2 w + 1 of the workspace and are joined by another launch.
+//
+// In a prompt the last tile sees most keys and the first fewest, so tiles are
+// taken in pairs from both ends, and every pair counts the same.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -71,6 +74,32 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnSeq& s) {
     return int((int64_t(s.n) * a.group + a.tile_rows - 1) / a.tile_rows);
 }
 
+// Keys that any row of a tile may see.
+template <AttnKind KIND>
+__device__ __forceinline__ int attn_seen(const AttnArgs& a, const AttnSeq& s, int tile) {
+    if constexpr (KIND != kAttnPrefill) return s.keys;
+    const int64_t end = min(int64_t(tile + 1) * a.tile_rows, int64_t(s.n) * a.group);  // rows
+    return max(min(int(s.prefix + (end - 1) / a.group + 1), s.keys), 0);
+}
+// A tile's units: at least one, so that rows which see nothing are written.
+template <AttnKind KIND>
+__device__ __forceinline__ int attn_units(const AttnArgs& a, const AttnSeq& s, int tile) {
+    return max((attn_seen<KIND>(a, s, tile) + a.unit - 1) / a.unit, 1);
+}
+// The units that a pair of tiles counts (prefill: at least those of any pair,
+// whose keys sum to 2 prefix + tile_rows (tiles + 1) / group + 2 at most), and
+// those of a sequence.
+template <AttnKind KIND>
+__device__ __forceinline__ int attn_pair(const AttnArgs& a, const AttnSeq& s, int tiles) {
+    if constexpr (KIND != kAttnPrefill) return attn_units<KIND>(a, s, 0);
+    const int64_t keys = 2 * int64_t(max(s.prefix, 0)) + (int64_t(tiles) + 1) * a.tile_rows / a.group + 2;
+    return int(keys / a.unit) + 2;
+}
+template <AttnKind KIND>
+__device__ __forceinline__ int64_t attn_seq_units(const AttnArgs& a, const AttnSeq& s, int tiles) {
+    return int64_t(attn_pair<KIND>(a, s, tiles)) * (KIND == kAttnPrefill ? (tiles + 1) / 2 : tiles);
+}
+
 __device__ __forceinline__ int64_t wave_sum64(int64_t x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
@@ -84,76 +113,131 @@ __device__ __forceinline__ int64_t wave_scan64(int64_t x, int lane) {  // inclus
     }
     return x;
 }
-
 __device__ __forceinline__ int64_t read_lane64(int64_t x, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(x), lane), hi = __builtin_amdgcn_readlane(uint32_t(x >> 32), lane);
     return int64_t(uint64_t(hi) << 32 | lo);
 }
 
-// Keys of a chunk.
-template <AttnKind KIND>
-__device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
-    int64_t total = 0;
-    if (a.d.B == 1) {
-        const AttnSeq s = attn_seq<KIND>(a, 0);
-        total = int64_t(attn_tiles<KIND>(a, s)) * s.keys;
-    } else {
-        for (int b = lane; b < a.d.B; b += 64) {
-            const AttnSeq s = attn_seq<KIND>(a, b);
-            total += int64_t(attn_tiles<KIND>(a, s)) * s.keys;
-        }
-        total = wave_sum64(total);
-    }
-    const int64_t c = max((total + a.spread - 1) / a.spread, int64_t(1));
-    return __builtin_amdgcn_readfirstlane(int(min((c + a.min_chunk - 1) / a.min_chunk * a.min_chunk, int64_t(1) << 30)));
+// a / b of numbers >= 0; of 32 bits, as most are, it takes a tenth of the instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((a | b) >> 32) return a / b;
+    return uint32_t(a) / uint32_t(b);
 }
 
-struct AttnItem {
-    int b, tile, chunk, chunks;
-    int64_t part;  // of the tile's first chunk in the workspace, if chunks > 1
+// The units of one key head (and head tile), those of a workgroup, and the
+// number of workgroups that have any.
+struct AttnPlan {
+    int64_t units, per;
+    int ranges;
 };
+template <AttnKind KIND>
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane) {
+    int64_t units = 0;
+    for (int b = lane; b < a.d.B; b += 64) {
+        const AttnSeq s = attn_seq<KIND>(a, b);
+        units += attn_seq_units<KIND>(a, s, attn_tiles<KIND>(a, s));
+    }
+    AttnPlan p;
+    p.units = read_lane64(a.d.B == 1 ? units : wave_sum64(units), 0);
+    const int64_t all = p.units * (a.cache.H_kv * a.head_tiles);
+    p.per = max(quotient(all + a.slots - 1, a.slots), int64_t(a.min_units));
+    p.ranges = int(quotient(all + p.per - 1, p.per));
+    return p;
+}
 
-// Item `i` (a (tile, chunk), or with TILES a whole tile); false behind the last.
+// The sequence that holds unit `u` of a key head (with TILES: that holds tile u
+// of all sequences), the first of its units (tiles) and, with TILES, units.
+struct AttnPlace {
+    int b = -1;
+    int64_t first = 0, count = 0, first_unit = 0;
+};
 template <AttnKind KIND, bool TILES>
-__device__ __forceinline__ bool attn_item(const AttnArgs& a, int c, int64_t i, int lane, AttnItem& it) {
-    int64_t items0 = 0, parts0 = 0;
+__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t u, int lane, AttnPlace& at) {
+    int64_t before = 0, units_before = 0;
     for (int base = 0; base < a.d.B; base += 64) {
         const int b = base + lane;
-        int tiles = 0, chunks = 1;
+        int64_t count = 0, units = 0;
         if (b < a.d.B) {
             const AttnSeq s = attn_seq<KIND>(a, b);
-            tiles = attn_tiles<KIND>(a, s);
-            chunks = max((s.keys + c - 1) / c, 1);
+            const int tiles = attn_tiles<KIND>(a, s);
+            units = attn_seq_units<KIND>(a, s, tiles);
+            count = TILES ? tiles : units;
         }
-        const int64_t items = int64_t(tiles) * (TILES ? 1 : chunks), parts = chunks > 1 ? int64_t(tiles) * chunks : 0;
-        int64_t items_end = items, parts_end = parts;
+        int64_t end = count, units_end = units;
         if (a.d.B > 1) {
-            items_end = wave_scan64(items, lane);
-            parts_end = wave_scan64(parts, lane);
+            end = wave_scan64(count, lane);
+            if (TILES) units_end = wave_scan64(units, lane);
         }
-        const int64_t first = items0 + items_end - items;
-        const uint64_t here = __ballot(i >= first && i < first + items);
+        const int64_t first = before + end - count;
+        const uint64_t here = __ballot(u >= first && u < first + count);
         if (here) {
             const int src = __builtin_ctzll(here);
-            it.b = base + src;
-            it.chunks = __builtin_amdgcn_readlane(chunks, src);
-            // the item's number within its sequence is below 2^31 (rows and chunks are)
-            const uint32_t at = uint32_t(i - read_lane64(first, src));
-            it.tile = TILES ? at : at / uint32_t(it.chunks);
-            it.chunk = TILES ? 0 : at - it.tile * it.chunks;
-            it.part = parts0 + read_lane64(parts_end - parts, src) + int64_t(it.tile) * it.chunks;
+            at.b = base + src;
+            at.first = read_lane64(first, src);
+            at.count = read_lane64(count, src);
+            at.first_unit = TILES ? units_before + read_lane64(units_end - units, src) : at.first;
             return true;
         }
-        items0 += read_lane64(items_end, 63);
-        parts0 += read_lane64(parts_end, 63);
+        before += read_lane64(end, 63);
+        if (TILES) units_before += read_lane64(units_end, 63);
     }
     return false;
 }
 
-// A tile's parts over chunks of keys: unnormalised outputs, then the running
-// maximum (in powers of two) and sum of every row.
-__device__ __forceinline__ float* part_out(const AttnArgs& a, int64_t part, int hh, int rows, int D) {
-    return static_cast<float*>(a.ws) + (int64_t(hh) * a.part_tiles + part) * rows * (D + 2);
+// A tile, and some of its units.
+struct AttnPiece {
+    int tile, unit, units, all;  // units from `unit` on, of all the tile's
+};
+// What of a sequence lies at its unit `off`, at most `most` units; all == 0: the
+// next `units` count nothing (a pair has fewer than it counts).
+template <AttnKind KIND>
+__device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, const AttnSeq& s, int tiles, int64_t off, int64_t most) {
+    const int pair = attn_pair<KIND>(a, s, tiles);
+    const int p = int(quotient(off, pair));
+    AttnPiece x;
+    x.unit = int(off - int64_t(p) * pair);
+    if constexpr (KIND == kAttnPrefill) {
+        x.tile = tiles - 1 - p;
+        x.all = attn_units<KIND>(a, s, x.tile);
+        if (x.unit >= x.all) {
+            x.unit -= x.all;
+            x.all = x.tile != p ? attn_units<KIND>(a, s, p) : 0;
+            const int last = pair - attn_units<KIND>(a, s, x.tile);
+            x.tile = p;
+            if (x.unit >= x.all) {
+                x.units = int(min(int64_t(last - x.unit), most));
+                x.all = 0;
+                return x;
+            }
+        }
+    } else {
+        x.tile = p;
+        x.all = pair;
+    }
+    x.units = int(min(int64_t(x.all - x.unit), most));
+    return x;
+}
+// The first unit of a tile within its sequence.
+template <AttnKind KIND>
+__device__ __forceinline__ int64_t attn_tile_unit(const AttnArgs& a, const AttnSeq& s, int tiles, int tile) {
+    const int pair = attn_pair<KIND>(a, s, tiles);
+    if constexpr (KIND != kAttnPrefill) return int64_t(pair) * tile;
+    const int other = tiles - 1 - tile;
+    if (other <= tile) return int64_t(pair) * other;
+    return int64_t(pair) * tile + attn_units<KIND>(a, s, other);
+}
+
+// Part `part` of the workspace: a tile's unnormalised outputs over some of its
+// keys, then the running maximum (in powers of two) and sum of every row.
+__device__ __forceinline__ float* part_out(const AttnArgs& a, int64_t part, int rows, int D) {
+    return static_cast<float*>(a.ws) + part * rows * (D + 2);
+}
+
+// The range of workgroup `wg` of the grid, plan.ranges if none.  Workgroups go
+// to the 8 XCDs in turn; neighbouring ranges, which share keys, go to one.
+__device__ __forceinline__ int attn_range(const AttnPlan& plan, int wg) {
+    const int per_xcd = (plan.ranges + 7) >> 3, w = (wg & 7) * per_xcd + (wg >> 3);
+    return wg >> 3 < per_xcd ? min(w, plan.ranges) : plan.ranges;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -198,10 +282,13 @@ __device__ __forceinline__ void e4m3_to_bf16(const uint4& u, uint4& lo, uint4& h
 // Four 16-bit elements of each lane, transposed over groups of 16 lanes: lane
 // 4 r + c of a group gives elements 4 c .. 4 c + 3 of row r of a 4 x 16 tile,
 // and lane i receives column i.
-__device__ __forceinline__ uint2 read_tr16(const void* lds) {
+__device__ __forceinline__ uint2 read_tr16(uint32_t lds) {
     typedef short s16x4v __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(
-        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v*)(lds)));
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         reinterpret_cast<__attribute__((address_space(3))) s16x4v*>(lds)));
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
 }
 
 }  // namespace gdn

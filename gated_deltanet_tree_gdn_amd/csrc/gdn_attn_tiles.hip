@@ -25,11 +25,11 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const
 // of one piece at a time, V transposed, 4 rows of four adjacent pieces at a
 // time; both spread over all banks.
 template <int D>
-__device__ __forceinline__ int k_xor(int r) {
+__device__ __forceinline__ constexpr int k_xor(int r) {
     return D >= 128 ? r & 15 : r >> 1 & 7;
 }
 template <int D>
-__device__ __forceinline__ int v_xor(int r) {
+__device__ __forceinline__ constexpr int v_xor(int r) {
     return D >= 128 ? 4 * (r & 3) : 4 * (r >> 1 & 1);
 }
 
@@ -40,29 +40,25 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
-// x *= f for accumulators that fill half of a wavefront's 512 registers, in
+// x = x f + g for accumulators that fill half of a wavefront's 512 registers, in
 // place: the other half is what vector instructions can use, and without this
-// the compiler moves all of them there and back around every use.  The first
-// instructions wait for matrix products that may still write x.
-template <int N>
-__device__ __forceinline__ void scale_acc(f32x16 (&x)[N], float f) {
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+// the compiler moves all of them there and back around every use.
+__device__ __forceinline__ void update_acc(f32x16& x, float f, const float (&g)[16]) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");  // matrix products may still write x
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float t, y = x[n][i];
-            asm volatile(
-                "v_accvgpr_read_b32 %1, %0\n\t"
-                "s_nop 1\n\t"
-                "v_mul_f32 %1, %1, %2\n\t"
-                "s_nop 1\n\t"
-                "v_accvgpr_write_b32 %0, %1"
-                : "+a"(y), "=&v"(t)
-                : "v"(f));
-            x[n][i] = y;
-        }
-    asm volatile("s_nop 15" ::: "memory");
+    for (int i = 0; i < 16; ++i) {
+        float t, y = x[i];
+        asm volatile(
+            "v_accvgpr_read_b32 %1, %0\n\t"
+            "s_nop 1\n\t"
+            "v_fma_f32 %1, %1, %2, %3\n\t"
+            "s_nop 1\n\t"
+            "v_accvgpr_write_b32 %0, %1"
+            : "+a"(y), "=&v"(t)
+            : "v"(f), "v"(g[i]));
+        x[i] = y;
+    }
+    asm volatile("s_nop 7" ::: "memory");
 }
 
 template <int D>
@@ -75,15 +71,13 @@ struct TileLds {
 // has to have arrived is what loads_barrier() waits for.  Nothing else in these
 // kernels uses m0.
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ void load_to_lds(const i32x4& rsrc, int off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(lds)
+__device__ __forceinline__ void load_to_lds(const i32x4& rsrc, int off, int more, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(rsrc), "s"(more),
+                 "s"(lds)
                  : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const char* at, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
 }
 
 // Numbers of the pages from `first` on, one per lane, read from the table 64 at a time.
@@ -111,45 +105,41 @@ template <int D, bool F8, bool IS_V>
 struct Stage {
     static constexpr int P = D / (F8 ? 16 : 8);  // 16-byte pieces of a row
     static constexpr int L = 16 * P / 64;        // loads of a wavefront
+    static constexpr int R = 64 / P;             // rows of a load
     static constexpr int size = F8 ? 1 : 2;
     const char* pool;  // of the key head
     int64_t page_stride;
     int row_stride;  // bytes
     PageWindow window;
+    int piece, row;  // bytes: the lane's piece of a load's first rows as permuted, and its row
     uint4 x[F8 ? L : 1];
 
-    __device__ __forceinline__ void init(const AttnArgs& a, int h, int end) {
+    __device__ __forceinline__ void init(const AttnArgs& a, int h, int end, int lane) {
         const gdn_kv_cache& c = a.cache;
         pool = static_cast<const char*>(IS_V ? c.v : c.k) + h * (IS_V ? c.v_head_stride : c.k_head_stride) * size;
         page_stride = (IS_V ? c.v_page_stride : c.k_page_stride) * size;
         row_stride = int(IS_V ? c.v_row_stride : c.k_row_stride) * size;
         window.open(end, a.page_shift);
+        piece = (lane % P ^ perm(lane / P)) << 4;
+        row = lane / P * row_stride;
     }
-    __device__ __forceinline__ static int perm(int r) { return F8 ? 0 : IS_V ? v_xor<D>(r) : k_xor<D>(r); }
+    // of row R j + l that is perm(R j) ^ perm(l)
+    __device__ __forceinline__ static constexpr int perm(int r) { return F8 ? 0 : IS_V ? v_xor<D>(r) : k_xor<D>(r); }
 
-    __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
-                                         int lane) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass rejects the 16-byte forms
+    // The loads of a tile: begin(), and then part(0) .. part(L - 1) where a page has 16 rows or more.
+    const char* base;
+    uint32_t to_lds;
+    __device__ __forceinline__ void begin(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
+                                          int lane) {
         t0 += 16 * wave;
         const int from = min(t0, end - 1) >> a.page_shift, to = min(t0 + 15, end - 1) >> a.page_shift;
         window.cover(table, from, to, lane);
-        lds += 16 * wave * (D / 8);
-        const uint32_t to_lds = __builtin_amdgcn_readfirstlane(lds_address(lds));
+        to_lds = __builtin_amdgcn_readfirstlane(lds_address(lds + 16 * wave * (D / 8)));
         if (a.page_shift >= 4) {  // the 16 rows lie in one page
+            piece = fresh(piece);
             int page = __builtin_amdgcn_readlane(window.ids, from - window.first);
             if (page < 0 || page >= a.cache.n_pages) page = 0;
-            const char* base = pool + page * page_stride + int64_t(t0 & (a.cache.page_size - 1)) * row_stride;
-            const uint64_t bits = reinterpret_cast<uint64_t>(base);
-            const i32x4 rsrc{int32_t(bits), int32_t(bits >> 32 & 0xffff), 0x7fffffff, 0x00027000};
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                const int r = (64 * j + lane) / P;
-                const int off = r * row_stride + ((lane % P ^ perm(r)) << 4);
-                if constexpr (F8)
-                    x[j] = *reinterpret_cast<const uint4*>(base + off);
-                else
-                    load_to_lds(rsrc, off, to_lds + 1024 * j);
-            }
+            base = pool + page * page_stride + int64_t(t0 & (a.cache.page_size - 1)) * row_stride;
         } else {
             lane = fresh(lane);
 #pragma unroll
@@ -165,7 +155,23 @@ struct Stage {
                     load_to_lds(at, to_lds + 1024 * j);
             }
         }
-#endif
+    }
+    __device__ __forceinline__ void part(int j) {
+        const int off = (piece ^ perm(R * j) << 4) + row, more = R * j * row_stride;
+        if constexpr (F8) {
+            x[j] = *reinterpret_cast<const uint4*>(base + more + off);
+        } else {
+            const uint64_t bits = reinterpret_cast<uint64_t>(base);
+            load_to_lds(i32x4{int32_t(bits), int32_t(bits >> 32 & 0xffff), 0x7fffffff, 0x00027000}, off, more,
+                        to_lds + 1024 * j);
+        }
+    }
+    __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
+                                         int lane) {
+        begin(a, table, lds, t0, end, wave, lane);
+        if (a.page_shift >= 4)
+#pragma unroll
+            for (int j = 0; j < L; ++j) part(j);
     }
     // e4m3: what load() brought, into LDS as bf16.
     __device__ __forceinline__ void store(uint4* lds, int wave, int lane) const {
@@ -249,9 +255,9 @@ __device__ __forceinline__ void rewrite(uint4* v, int kind, int tid) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup: one chunk of one sequence's keys, one key head, 128 rows
-// (token, query head of the group); a wavefront has 32 of the rows.  64 keys
-// at a time lie in LDS, the next 64 on their way there.
+// A piece of a workgroup's range: some keys of one key head for 128 rows (token,
+// query head of the group) of a sequence; a wavefront has 32 of the rows.  64
+// keys at a time lie in LDS, the next 64 on their way there.
 //   S^T = K Q^T    keys x rows on MFMA, Q in registers for the whole chunk
 //   O^T += V^T P   V read transposed; the lanes hold P where the product wants it
 // The running maximum is raised only where a row's scores pass it by more than
@@ -267,33 +273,33 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
     extern __shared__ uint4 lds_raw[];
     TileLds<D>& lds = *reinterpret_cast<TileLds<D>*>(lds_raw);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int heads = a.cache.H_kv;
-    const int64_t wg = block_id(), grid_items = int64_t(gridDim.x) * gridDim.y / heads;
-    if (wg >= grid_items * heads) return;
-    const int h = int(wg % heads);
-    const int c = attn_chunk<KIND>(a, threadIdx.x & 63);
-    const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
+    const AttnPlan plan = attn_plan<KIND>(a, threadIdx.x & 63);
+    const int w = attn_range(plan, blockIdx.x);
+    const int64_t u0 = w * plan.per, u_end = min(u0 + plan.per, plan.units * a.cache.H_kv);
     const float inf = __builtin_inff();
 
-    AttnItem it;
-    for (int64_t item = wg / heads; attn_item<KIND, false>(a, c, item, threadIdx.x & 63, it); item += grid_items) {
+    AttnPlace at;
+    for (int64_t u = u0; u < u_end;) {
         const int tid = fresh(threadIdx.x), lane = tid & 63, col = lane & 31, half = lane >> 5;
-        const AttnSeq s = attn_seq_uniform<KIND>(a, it.b);
+        const int h = int(quotient(u, plan.units));
+        const int64_t uh = u - h * plan.units;
+        if (at.b < 0 || uh < at.first || uh >= at.first + at.count) attn_find<KIND, false>(a, uh, lane, at);
+        const AttnSeq s = attn_seq_uniform<KIND>(a, at.b);
+        const AttnPiece it = attn_piece<KIND>(a, s, attn_tiles<KIND>(a, s), uh - at.first, u_end - u);
+        const bool first = u == u0;
+        u += it.units;
+        if (it.all == 0) continue;
+        const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
         const int all_rows = s.n * a.group;
         const int row0 = it.tile * kTileRows, rows = min(kTileRows, all_rows - row0);
-        // the last of the tile's tokens sees most
-        const int last_token = (row0 + rows - 1) / a.group;
-        const int begin = it.chunk * c;
-        const int seen = KIND == kAttnPrefill ? min(max(s.prefix + last_token + 1, 0), s.keys) : s.keys;
-        const int end = min(begin + c, seen);
-        const int chunks = max((seen + c - 1) / c, 1);  // of this tile
-        if (it.chunk >= chunks) continue;
+        const int begin = it.unit * kKeys;
+        const int end = min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile));
 
         const int my_row = min(row0 + wave * 32 + col, all_rows - 1);
         const int token = my_row / a.group, head = h * a.group + my_row - token * a.group;
         const uint32_t* anc =
-            KIND == kAttnVerify ? a.anc + (int64_t(it.b) * s.n + token) * ((a.d.T + 31) >> 5) : nullptr;
-        const int32_t* table = a.table + it.b * a.d.table_stride;
+            KIND == kAttnVerify ? a.anc + (int64_t(at.b) * s.n + token) * ((a.d.T + 31) >> 5) : nullptr;
+        const int32_t* table = a.table + at.b * a.d.table_stride;
         // tokens from here on are masked for some of the tile's rows
         const int open_end = KIND == kAttnPrefill ? s.prefix + row0 / a.group + 1 : s.prefix;
 
@@ -307,7 +313,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
         bf16x8 q[D / 16];
         const uint16_t* qp = a.q + (s.row0 + token) * a.d.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) q[n] = load_frag(qp + 16 * n);
+        for (int n = 0; n < D / 16; ++n) {
+            q[n] = load_frag(qp + 16 * n);
+            if constexpr (D == 256) asm volatile("" : "+a"(q[n]));  // beside the accumulators
+        }
 
         f32x16 o[D / 32];
 #pragma unroll
@@ -317,16 +326,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
         float m = -inf, l = 0.0f;  // m: what the powers are taken against
 
         // register i of x[j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col`
+        const uint32_t k_row = lds_address(lds.k) + col * (D * 2);
+        int k_col = (half ^ k_xor<D>(col)) << 4;
         auto k_frag = [&](int j, int n, int buf) {
-            const int r = 32 * j + col;
-            return load_frag(lds.k[buf] + r * (D / 8) + (2 * n + half ^ k_xor<D>(r)));
+            return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(
+                k_row + buf * (kKeys * D * 2) + (k_col ^ n << 5) + j * (32 * D * 2));
         };
-        // k-slots 8 half .. 8 half + 7 of product k: keys 16 k + 4 half + {0 .. 3} and 8 more
-        const int vr = 4 * half + ((lane & 15) >> 2), vp = 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
+        // k-slots 8 half .. 8 half + 7 of product k: keys 16 k + 4 half + {0 .. 3} and 8 more, whose rows have the same permutation
+        const int vr = 4 * half + ((lane & 15) >> 2);
+        const uint32_t v_row = lds_address(lds.v) + vr * (D * 2) + 8 * (lane & 1);
+        const int v_col = (2 * (lane >> 4 & 1) + ((lane & 3) >> 1) ^ v_xor<D>(vr)) << 4;
         auto v_frag = [&](int n, int k, int buf) {
-            const int r = 16 * k + vr;
-            const uint4* row = lds.v[buf] + r * (D / 8);  // row r + 8 has the same permutation
-            const char* at = reinterpret_cast<const char*>(row + (4 * n + vp ^ v_xor<D>(r))) + 8 * (lane & 1);
+            const uint32_t at = v_row + buf * (kKeys * D * 2) + (v_col ^ n << 6) + k * (16 * D * 2);
             const uint2 u = read_tr16(at), w = read_tr16(at + 8 * D * 2);
             return __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
         };
@@ -344,11 +355,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                 const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
                 m = m_new;
                 l *= keep;
-                if constexpr (D == 256) {
-                    scale_acc(o, keep);
-                } else {
 #pragma unroll
-                    for (int n = 0; n < D / 32; ++n) o[n] *= keep;
+                for (int n = 0; n < D / 32; ++n) {
+                    if constexpr (D == 256)
+                        update_acc(o[n], keep, {});
+                    else
+                        o[n] *= keep;
                 }
             }
         };
@@ -356,37 +368,49 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
         if (begin < end) {
             Stage<D, F8, false> sk;
             Stage<D, F8, true> sv;
-            sk.init(a, h, end);
-            sv.init(a, h, end);
-            // V of the tile at t0 and K of the next one are in LDS, and those after them on their way.
+            sk.init(a, h, end, lane);
+            sv.init(a, h, end, lane);
+            // V of the tile at t0 and K of the next one are in LDS; those after
+            // them may come (K behind the last tile is not used).
             auto arrive = [&](int t0, int buf) {
                 if (t0 + kKeys < end) sk.store(lds.k[buf ^ 1], wave, lane);
                 sv.store(lds.v[buf], wave, lane);
                 loads_barrier<0>();
-                if (t0 + 2 * kKeys < end) sk.load(a, table, lds.k[buf], t0 + 2 * kKeys, end, wave, lane);
-                if (t0 + kKeys < end) sv.load(a, table, lds.v[buf ^ 1], t0 + kKeys, end, wave, lane);
+                if (t0 + kKeys < end) {
+                    sk.begin(a, table, lds.k[buf], t0 + 2 * kKeys, end, wave, lane);
+                    sv.begin(a, table, lds.v[buf ^ 1], t0 + kKeys, end, wave, lane);
+                }
+            };
+            constexpr int L = Stage<D, F8, true>::L;
+            auto part = [&](int i) {
+                if (i < L)
+                    sk.part(i);
+                else
+                    sv.part(i - L);
             };
             sk.load(a, table, lds.k[0], begin, end, wave, lane);
             sk.store(lds.k[0], wave, lane);
             loads_barrier<0>();
             if (begin + kKeys < end) sk.load(a, table, lds.k[1], begin + kKeys, end, wave, lane);
             sv.load(a, table, lds.v[0], begin, end, wave, lane);
-            constexpr int NQ = D / 8, AHEAD = 4;  // products of a tile with K (and with V), operands read ahead
+            constexpr int NQ = D / 8, AHEAD = D == 128 ? 4 : 8;  // products of a tile with K (and with V), operands read ahead
             f32x16 x[2];                          // scores of the tile at t0
 #pragma unroll
             for (int i = 0; i < NQ; ++i) x[i & 1] = mfma32(k_frag(i & 1, i >> 1, 0), q[i >> 1], i < 2 ? zero : x[i & 1]);
             int t0 = begin, buf = 0;
 
-            // Tiles that every row sees all of, but the last: the scores of the
+            // Tiles that every row sees all of, but the last (pages of fewer than 16
+            // rows take the plain loop below for all): the scores of the
             // next tile are formed beside the powers of this one and its maxima
             // beside the products with V, step by step as they stand here.
-            const int open = missing ? begin : min(max(open_end, begin), end - 1);
+            const int open = missing || a.page_shift < 4 ? begin : min(max(open_end, begin), end - 1);
             float top = -inf;
 #pragma unroll
             for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
             top = largest(top);
             for (; t0 + kKeys <= open; t0 += kKeys, buf ^= 1) {
                 arrive(t0, buf);
+                k_col = fresh(k_col);
                 raise(top);
                 const float base = finite_max(m);
                 f32x16 y[2];
@@ -399,11 +423,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                     y[i & 1] = mfma32(f[i % AHEAD], q[i >> 1], i < 2 ? zero : y[i & 1]);
                     const int r = i + AHEAD;
                     f[i % AHEAD] = r < NQ ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NQ) % (D / 32), (r - NQ) / (D / 32), buf);
+                    if (i % (NQ / (2 * L)) == 0) part(i / (NQ / (2 * L)));
 #pragma unroll
                     for (int e = i * 32 / NQ; e < (i + 1) * 32 / NQ; ++e) {
-                        const float w = exp2_fast(fmaf(x[e >> 4][e & 15], scale, -base));
-                        l += w;
-                        p[e >> 3][e & 7] = static_cast<__bf16>(w);
+                        x[e >> 4][e & 15] = exp2_fast(fmaf(x[e >> 4][e & 15], scale, -base));
+                        p[e >> 3][e & 7] = static_cast<__bf16>(x[e >> 4][e & 15]);
+                        if (D < 256) l += x[e >> 4][e & 15];
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -413,6 +438,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                     o[i % (D / 32)] = mfma32(f[i % AHEAD], p[i / (D / 32)], o[i % (D / 32)]);
                     const int r = i + AHEAD;
                     if (r < NQ) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
+                    if (D == 256) l += x[i >> 4 & 1][i & 15];  // elsewhere x has no registers by now
                     if (i >= NQ / 2) {
 #pragma unroll
                         for (int e = (i - NQ / 2) * 64 / NQ; e < (i - NQ / 2 + 1) * 64 / NQ; ++e)
@@ -426,6 +452,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             }
             for (; t0 < end; t0 += kKeys, buf ^= 1) {
                 arrive(t0, buf);
+                if (t0 + kKeys < end && a.page_shift >= 4)
+#pragma unroll
+                    for (int i = 0; i < 2 * L; ++i) part(i);
                 uint32_t see[2] = {0xffffffffu, 0xffffffffu};
                 bool odd = false;
                 if (missing || t0 + kKeys > min(open_end, end)) {
@@ -503,9 +532,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                             }
                             count = mfma32(v_frag(n, k, buf), one, count);
                         }
+                        float g[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (count[i] > 0.0f) o[n][i] += what;
+                        for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
+                        if constexpr (D == 256) {
+                            update_acc(o[n], 1.0f, g);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[n][i] += g[i];
+                        }
                     }
                 }
             }
@@ -513,8 +548,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
 
         l += __shfl_xor(l, 32);
         if (wave * 32 + col < rows) {
-            if (chunks > 1) {
-                float* part = part_out(a, it.part + it.chunk, h, kTileRows, D);
+            if (it.units < it.all) {
+                float* part = part_out(a, 2 * int64_t(w) + (first ? 0 : 1), kTileRows, D);
                 const int r = wave * 32 + col;
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
@@ -535,8 +570,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                                       f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]}, l);
             }
         }
-        if constexpr (KIND != kAttnPrefill) return;  // the grid has a workgroup for every item
-        __syncthreads();
+        if (u < u_end) __syncthreads();  // the next piece overwrites LDS
     }
 }
 
@@ -555,10 +589,7 @@ hipError_t launch_one(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 
 template <AttnKind KIND>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    const int64_t rows = int64_t(a.d.T) * a.group;  // of a tree, or of all prompts
-    const int64_t tiles = KIND == kAttnVerify ? a.d.B * ((rows + kTileRows - 1) / kTileRows) : rows / kTileRows + a.d.B;
-    const int64_t chunks = ((int64_t(a.d.max_pages) << a.page_shift) + a.min_chunk - 1) / a.min_chunk;
-    const dim3 grid = grid_of(std::min(tiles + a.spread, tiles * std::max<int64_t>(chunks, 1)) * a.cache.H_kv);
+    const dim3 grid(a.slots);
     const bool f8 = a.cache.dtype == GDN_E4M3;
     switch (a.cache.d) {
         case 64: return f8 ? launch_one<KIND, 64, true>(a, grid, stream) : launch_one<KIND, 64, false>(a, grid, stream);

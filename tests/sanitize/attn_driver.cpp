@@ -19,10 +19,10 @@ static hipError_t outcome = hipSuccess;
 namespace gdn {
 void set_last_error(const std::string& msg) { last_error = msg; }
 void attn_shape(AttnArgs& a) {
-    a.part_tiles = a.d.max_pages > 8 ? 4 : 0;
+    a.join = a.d.max_pages > 8;
     a.tile_rows = 16;
 }
-size_t attn_ws_bytes(const AttnArgs& a) { return size_t(a.part_tiles) * 256; }
+size_t attn_ws_bytes(const AttnArgs& a) { return a.join ? 1024 : 0; }
 hipError_t launch_kv_append(const KvAppendArgs&, hipStream_t) { return ++launches, outcome; }
 hipError_t launch_kv_commit(const KvCommitArgs& a, int n, hipStream_t) {
     for (int i = 0; i < n; ++i) committed += a.k[i] != nullptr && a.v[i] != nullptr;

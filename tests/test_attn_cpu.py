@@ -198,12 +198,13 @@ def test_commit_rejects(lib):
 
 
 def test_workspaces_have_room_for_every_part(lib):
-    """the parts of one (key head, head tile): at most 2 spread, and none where a table has room for one chunk only"""
-    assert need(lib, "decode", dims(max_pages=8), cache()) == 0
+    """two parts for each workgroup that the GPU has room for, fewer for small calls, none where a table has room for one unit"""
+    assert need(lib, "decode", dims(max_pages=8), cache()) == need(lib, "verify", dims(max_pages=4), cache()) == 0
     assert need(lib, "decode", dims(max_pages=9), cache()) > 0
-    most = need(lib, "decode", dims(B=1000, max_pages=1 << 20), cache())
-    assert most == need(lib, "decode", dims(B=60000, max_pages=1 << 20), cache())
-    assert most == 2 * 256 * 2 * 16 * 130 * 4  # spread 512 / 2 key heads; 16 rows of 128 + 2
+    for kind, d in (("decode", dims(B=1000, max_pages=1 << 20)), ("prefill", dims(T=10 ** 6)), ("verify", dims(B=60000))):
+        rows = 16 if kind == "decode" else 128
+        assert need(lib, kind, d, cache()) == 2 * 512 * rows * 130 * 4  # rows of 128 + 2
+        assert 0 < need(lib, kind, dims(B=1, T=1, max_pages=16), cache()) < 2 * 64 * rows * 130 * 4
 
 
 def test_binding_has_no_cpu_fallback():
