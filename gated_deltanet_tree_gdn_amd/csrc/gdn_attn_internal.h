@@ -65,7 +65,10 @@ struct AttnArgs {
     int min_units;   // of a workgroup
     bool join;       // tiles may be divided
 };
-constexpr int kDecodeRows = 16, kTileRows = 128;  // rows of a tile
+// Rows of a tile: single tokens; otherwise 4 wavefronts of 64 rows, of 32 where
+// the accumulators of more do not fit the registers.
+constexpr int kDecodeRows = 16;
+constexpr int tile_rows(int d) { return d == 256 ? 128 : 256; }
 
 // Fills the derived members.
 void attn_shape(AttnArgs& a);

@@ -36,7 +36,7 @@ template <AttnKind KIND, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     constexpr int C = D / 4, K = kThreads / C;  // threads of a row, rows (or shares of the parts) at a time
     constexpr bool one = KIND == kAttnDecode;
-    constexpr int rows_of_part = one ? kDecodeRows : kTileRows;
+    constexpr int kTileRows = tile_rows(D), rows_of_part = one ? kDecodeRows : kTileRows;
     __shared__ f32x4 share[one ? K : 1][C];
     __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63, p = tid % C, k = tid / C;
@@ -133,8 +133,8 @@ hipError_t launch_join(const AttnArgs& a, const dim3& grid, hipStream_t stream) 
 int64_t max_tiles(const AttnArgs& a) {
     const int64_t rows = int64_t(a.d.T) * a.group;
     return a.kind == kAttnDecode   ? a.d.B
-           : a.kind == kAttnVerify ? a.d.B * ((rows + kTileRows - 1) / kTileRows)
-                                   : rows / kTileRows + a.d.B;
+           : a.kind == kAttnVerify ? a.d.B * ((rows + a.tile_rows - 1) / a.tile_rows)
+                                   : rows / a.tile_rows + a.d.B;
 }
 }  // namespace
 
@@ -143,16 +143,16 @@ void attn_shape(AttnArgs& a) {
     a.page_shift = __builtin_ctz(a.cache.page_size);
     a.group = a.d.H_q / a.cache.H_kv;
     const bool one = a.kind == kAttnDecode;
-    a.tile_rows = one ? kDecodeRows : kTileRows;
+    a.tile_rows = one ? kDecodeRows : tile_rows(a.cache.d);
     a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
     a.unit = one ? 128 : 64;
     a.min_units = one ? 1 : 4;
     const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
     // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
     // overlap, where cu_seqlens decreases, and each may then have all rows)
-    const int64_t tiles = one ? a.d.B : a.d.B * ((rows + kTileRows - 1) / kTileRows);
+    const int64_t tiles = one ? a.d.B : a.d.B * ((rows + a.tile_rows - 1) / a.tile_rows);
     const int64_t units = tiles * a.cache.H_kv * a.head_tiles * ((cap + a.unit - 1) / a.unit + 2);
-    a.slots = int(std::min<int64_t>(a.cache.d == 256 ? kCu : 2 * kCu, ((units + a.min_units - 1) / a.min_units + 7) / 8 * 8));
+    a.slots = int(std::min<int64_t>(one && a.cache.d < 256 ? 2 * kCu : kCu, ((units + a.min_units - 1) / a.min_units + 7) / 8 * 8));
     a.join = cap > a.unit;  // otherwise a tile is one unit
 }
 
@@ -162,7 +162,7 @@ size_t attn_ws_bytes(const AttnArgs& a) {
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
     const int64_t heads = int64_t(a.cache.H_kv) * a.head_tiles;
-    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : kTileRows / kJoinRows;
+    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows / kJoinRows;
     const dim3 grid = grid_of(max_tiles(a) * heads * blocks);
     return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, grid, stream)
            : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, grid, stream)

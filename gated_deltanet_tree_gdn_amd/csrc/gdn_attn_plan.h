@@ -118,10 +118,10 @@ __device__ __forceinline__ int64_t read_lane64(int64_t x, int lane) {
     return int64_t(uint64_t(hi) << 32 | lo);
 }
 
-// a / b of numbers >= 0; of 32 bits, as most are, it takes a tenth of the instructions.
+// a / b of numbers >= 0 that all lanes agree on; of 32 bits, as most are, it takes a tenth of the instructions.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if ((a | b) >> 32) return a / b;
-    return uint32_t(a) / uint32_t(b);
+    return __builtin_amdgcn_readfirstlane(uint32_t(a) / uint32_t(b));
 }
 
 // The units of one key head (and head tile), those of a workgroup, and the
@@ -188,6 +188,13 @@ __device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t u, int lane
 struct AttnPiece {
     int tile, unit, units, all;  // units from `unit` on, of all the tile's
 };
+__device__ __forceinline__ AttnPiece uniform(AttnPiece x) {
+    x.tile = __builtin_amdgcn_readfirstlane(x.tile);
+    x.unit = __builtin_amdgcn_readfirstlane(x.unit);
+    x.units = __builtin_amdgcn_readfirstlane(x.units);
+    x.all = __builtin_amdgcn_readfirstlane(x.all);
+    return x;
+}
 // What of a sequence lies at its unit `off`, at most `most` units; all == 0: the
 // next `units` count nothing (a pair has fewer than it counts).
 template <AttnKind KIND>
@@ -207,7 +214,7 @@ __device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, const AttnSeq
             if (x.unit >= x.all) {
                 x.units = int(min(int64_t(last - x.unit), most));
                 x.all = 0;
-                return x;
+                return uniform(x);
             }
         }
     } else {
@@ -215,7 +222,7 @@ __device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, const AttnSeq
         x.all = pair;
     }
     x.units = int(min(int64_t(x.all - x.unit), most));
-    return x;
+    return uniform(x);
 }
 // The first unit of a tile within its sequence.
 template <AttnKind KIND>

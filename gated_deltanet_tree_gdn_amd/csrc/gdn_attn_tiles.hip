@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "gdn_attn_internal.h"
 #include "gdn_attn_plan.h"
@@ -16,22 +17,33 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kKeys = 64;  // keys of a tile in LDS
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// The 16-byte pieces of a row in LDS are permuted by these.  K is read 16 rows
-// of one piece at a time, V transposed, 4 rows of four adjacent pieces at a
-// time; both spread over all banks.
+// Rows of K and V in LDS.  A load fills 1 KB in the order of the lanes, a block
+// of 512 / D rows; a few bytes after a block, and a permutation of the pieces of
+// a row by its place in the block (made in the address that a lane loads from),
+// spread over all banks what is read at a time: of K one piece of 16 rows, of V
+// four adjacent pieces of 4 rows (transposed).  Both leave constant offsets
+// between most reads of a lane.
+template <int D, bool IS_V>
+struct Layout {
+    static constexpr int kRows = 512 / D;                                  // of a block
+    static constexpr int kBlock = 1024 + (IS_V ? (D == 256 ? 128 : 0) : (D == 256 ? 32 : 64));
+    static constexpr int kTile = kKeys / kRows * kBlock;                   // bytes
+    // what the number of a row's piece is xored with: bits 0 and 1 (K), 2 and 3 (V)
+    __device__ __forceinline__ static constexpr int perm(int r) {
+        return IS_V ? 4 * (D == 256 ? r & 1 : D == 128 ? r & 3 : r >> 1 & 1) : D == 256 ? r & 1 : D == 128 ? r & 3 : r >> 1 & 3;
+    }
+    __device__ __forceinline__ static constexpr int row(int r) { return r / kRows * kBlock + r % kRows * (D * 2); }
+};
 template <int D>
-__device__ __forceinline__ constexpr int k_xor(int r) {
-    return D >= 128 ? r & 15 : r >> 1 & 7;
-}
-template <int D>
-__device__ __forceinline__ constexpr int v_xor(int r) {
-    return D >= 128 ? 4 * (r & 3) : 4 * (r >> 1 & 1);
-}
+struct TileLds {
+    static constexpr int kV = 2 * Layout<D, false>::kTile, kBytes = kV + 2 * Layout<D, true>::kTile;
+};
 
 // x, but what is computed from it is computed where it stands: the compiler
 // would otherwise form it before a loop and keep it in registers throughout.
@@ -61,11 +73,6 @@ __device__ __forceinline__ void update_acc(f32x16& x, float f, const float (&g)[
     asm volatile("s_nop 7" ::: "memory");
 }
 
-template <int D>
-struct TileLds {
-    uint4 k[2][kKeys * D / 8], v[2][kKeys * D / 8];
-};
-
 // 16 bytes per lane from memory to the 1 KB of LDS at `lds`.  The compiler's own
 // forms of these make it wait for all of them before any read of LDS; here what
 // has to have arrived is what loads_barrier() waits for.  Nothing else in these
@@ -78,6 +85,11 @@ __device__ __forceinline__ void load_to_lds(const i32x4& rsrc, int off, int more
 }
 __device__ __forceinline__ void load_to_lds(const char* at, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(lds) : "memory");
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __attribute__((address_space(3))) u32x4* lds_piece(uint32_t at) {
+    return reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at);
 }
 
 // Numbers of the pages from `first` on, one per lane, read from the table 64 at a time.
@@ -98,11 +110,11 @@ struct PageWindow {
 // Rows of K or V on their way from memory to LDS.  Wavefront w brings rows
 // 16 w .. 16 w + 15 of a tile.  Rows behind the last token hold what lies there
 // in the last page, rows of pages outside the pool what the first page holds;
-// both are masked.  bf16 goes straight to LDS (a load fills 64 pieces in the
-// order of the lanes, so the permutation of a row's pieces is made in the
-// address), e4m3 through registers, where it becomes bf16.
+// both are masked.  bf16 goes straight to LDS, e4m3 through registers, where it
+// becomes bf16.
 template <int D, bool F8, bool IS_V>
 struct Stage {
+    using To = Layout<D, IS_V>;
     static constexpr int P = D / (F8 ? 16 : 8);  // 16-byte pieces of a row
     static constexpr int L = 16 * P / 64;        // loads of a wavefront
     static constexpr int R = 64 / P;             // rows of a load
@@ -110,95 +122,126 @@ struct Stage {
     const char* pool;  // of the key head
     int64_t page_stride;
     int row_stride;  // bytes
-    PageWindow window;
-    int piece, row;  // bytes: the lane's piece of a load's first rows as permuted, and its row
+    int off;         // bytes: the lane's piece and row of a load
+    const char* base;
+    uint32_t to_lds;
     uint4 x[F8 ? L : 1];
 
-    __device__ __forceinline__ void init(const AttnArgs& a, int h, int end, int lane) {
+    __device__ __forceinline__ void init(const AttnArgs& a, int h, int lane) {
         const gdn_kv_cache& c = a.cache;
         pool = static_cast<const char*>(IS_V ? c.v : c.k) + h * (IS_V ? c.v_head_stride : c.k_head_stride) * size;
         page_stride = (IS_V ? c.v_page_stride : c.k_page_stride) * size;
         row_stride = int(IS_V ? c.v_row_stride : c.k_row_stride) * size;
-        window.open(end, a.page_shift);
-        piece = (lane % P ^ perm(lane / P)) << 4;
-        row = lane / P * row_stride;
+        off = lane / P * row_stride + ((lane % P ^ (F8 ? 0 : To::perm(lane / P))) << 4);
     }
-    // of row R j + l that is perm(R j) ^ perm(l)
-    __device__ __forceinline__ static constexpr int perm(int r) { return F8 ? 0 : IS_V ? v_xor<D>(r) : k_xor<D>(r); }
-
-    // The loads of a tile: begin(), and then part(0) .. part(L - 1) where a page has 16 rows or more.
-    const char* base;
-    uint32_t to_lds;
-    __device__ __forceinline__ void begin(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
-                                          int lane) {
-        t0 += 16 * wave;
-        const int from = min(t0, end - 1) >> a.page_shift, to = min(t0 + 15, end - 1) >> a.page_shift;
-        window.cover(table, from, to, lane);
-        to_lds = __builtin_amdgcn_readfirstlane(lds_address(lds + 16 * wave * (D / 8)));
-        if (a.page_shift >= 4) {  // the 16 rows lie in one page
-            piece = fresh(piece);
-            int page = __builtin_amdgcn_readlane(window.ids, from - window.first);
-            if (page < 0 || page >= a.cache.n_pages) page = 0;
-            base = pool + page * page_stride + int64_t(t0 & (a.cache.page_size - 1)) * row_stride;
-        } else {
-            lane = fresh(lane);
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                const int r = (64 * j + lane) / P, t = t0 + r;
-                int page = __shfl(window.ids, (min(t, end - 1) >> a.page_shift) - window.first);
-                if (page < 0 || page >= a.cache.n_pages) page = 0;
-                const char* at = pool + page * page_stride + int64_t(t & (a.cache.page_size - 1)) * row_stride +
-                                 ((lane % P ^ perm(r)) << 4);
-                if constexpr (F8)
-                    x[j] = *reinterpret_cast<const uint4*>(at);
-                else
-                    load_to_lds(at, to_lds + 1024 * j);
-            }
-        }
+    // The loads of a tile where a page has 16 rows or more, which so lie in page
+    // `page` from row `row` on: at(), and then part(0) .. part(L - 1).
+    __device__ __forceinline__ void at(uint32_t lds, int page, int row, int wave) {
+        to_lds = lds + 16 / To::kRows * To::kBlock * wave;
+        base = pool + page * page_stride + int64_t(row) * row_stride;
     }
     __device__ __forceinline__ void part(int j) {
-        const int off = (piece ^ perm(R * j) << 4) + row, more = R * j * row_stride;
+        const int more = R * j * row_stride;
         if constexpr (F8) {
             x[j] = *reinterpret_cast<const uint4*>(base + more + off);
         } else {
             const uint64_t bits = reinterpret_cast<uint64_t>(base);
             load_to_lds(i32x4{int32_t(bits), int32_t(bits >> 32 & 0xffff), 0x7fffffff, 0x00027000}, off, more,
-                        to_lds + 1024 * j);
+                        __builtin_amdgcn_readfirstlane(to_lds) + To::kBlock * j);
         }
     }
-    __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, uint4* lds, int t0, int end, int wave,
-                                         int lane) {
-        begin(a, table, lds, t0, end, wave, lane);
-        if (a.page_shift >= 4)
+    // The same for smaller pages.
+    __device__ __forceinline__ void scattered(const AttnArgs& a, const PageWindow& window, uint32_t lds, int t0, int end,
+                                              int wave, int lane) {
+        lane = fresh(lane);
+        to_lds = lds + 16 / To::kRows * To::kBlock * wave;
 #pragma unroll
-            for (int j = 0; j < L; ++j) part(j);
+        for (int j = 0; j < L; ++j) {
+            const int r = R * j + lane / P, t = t0 + 16 * wave + r;
+            int page = __shfl(window.ids, (min(t, end - 1) >> a.page_shift) - window.first);
+            if (page < 0 || page >= a.cache.n_pages) page = 0;
+            const char* from = pool + page * page_stride + int64_t(t & (a.cache.page_size - 1)) * row_stride +
+                               ((lane % P ^ (F8 ? 0 : To::perm(r))) << 4);
+            if constexpr (F8)
+                x[j] = *reinterpret_cast<const uint4*>(from);
+            else
+                load_to_lds(from, to_lds + To::kBlock * j);
+        }
     }
-    // e4m3: what load() brought, into LDS as bf16.
-    __device__ __forceinline__ void store(uint4* lds, int wave, int lane) const {
+    // e4m3: what the loads brought, into LDS as bf16.
+    __device__ __forceinline__ void store(uint32_t lds, int wave, int lane) const {
         if constexpr (F8) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                const int r = 16 * wave + (64 * j + lane) / P, p = 2 * (lane % P);
-                const int perm_r = IS_V ? v_xor<D>(r) : k_xor<D>(r);
+                const int r = 16 * wave + R * j + lane / P, p = 2 * (lane % P);
                 uint4 lo, hi;
                 e4m3_to_bf16(x[j], lo, hi);
-                lds[r * (D / 8) + (p ^ perm_r)] = lo;
-                lds[r * (D / 8) + (p + 1 ^ perm_r)] = hi;
+                *lds_piece(lds + To::row(r) + ((p ^ To::perm(r)) << 4)) = u32x4{lo.x, lo.y, lo.z, lo.w};
+                *lds_piece(lds + To::row(r) + ((p + 1 ^ To::perm(r)) << 4)) = u32x4{hi.x, hi.y, hi.z, hi.w};
             }
         }
     }
 };
 
+// The two of them, in step: K runs a tile ahead of V, whose pages are then known.
+template <int D, bool F8>
+struct Loader {
+    Stage<D, F8, false> k;
+    Stage<D, F8, true> v;
+    static constexpr int L = Stage<D, F8, false>::L;
+    PageWindow window;  // of K's tiles
+    int page, row;      // of K's last tile (pages of 16 rows or more)
+
+    __device__ __forceinline__ void init(const AttnArgs& a, int h, int end, int lane) {
+        k.init(a, h, lane);
+        v.init(a, h, lane);
+        window.open(end, a.page_shift);
+    }
+    __device__ __forceinline__ void find(const AttnArgs& a, const int32_t* table, int t0, int end, int wave, int lane) {
+        t0 += 16 * wave;
+        const int from = min(t0, end - 1) >> a.page_shift, to = min(t0 + 15, end - 1) >> a.page_shift;
+        window.cover(table, from, to, lane);
+        if (a.page_shift >= 4) {
+            page = __builtin_amdgcn_readlane(window.ids, from - window.first);
+            if (page < 0 || page >= a.cache.n_pages) page = 0;
+            row = t0 & (a.cache.page_size - 1);
+        }
+    }
+    // Part of V's tile at t0 and K's at t0 + kKeys, all of it where pages are
+    // small; the other parts follow with part().
+    __device__ __forceinline__ void begin(const AttnArgs& a, const int32_t* table, uint32_t k_lds, uint32_t v_lds, int t0,
+                                          int end, int wave, int lane) {
+        if (a.page_shift >= 4) {
+            v.at(v_lds, page, row, wave);
+            find(a, table, t0 + kKeys, end, wave, lane);
+            k.at(k_lds, page, row, wave);
+        } else {
+            find(a, table, t0, end, wave, lane);
+            v.scattered(a, window, v_lds, t0, end, wave, lane);
+            find(a, table, t0 + kKeys, end, wave, lane);
+            k.scattered(a, window, k_lds, t0 + kKeys, end, wave, lane);
+        }
+    }
+    __device__ __forceinline__ void part(int i) {
+        if (i < L)
+            k.part(i);
+        else
+            v.part(i - L);
+    }
+};
+
 // Whether any of the thread's share of a tile of V is not finite.
 template <int D>
-__device__ __forceinline__ bool any_odd(const uint4* v, int tid) {
+__device__ __forceinline__ bool any_odd(uint32_t v, int tid) {
     bool odd = false;
+#pragma unroll 2
+    for (int i = tid; i < kKeys * D / 8; i += kThreads) {
+        const u32x4 x = *lds_piece(v + (i >> 6) * Layout<D, true>::kBlock + (i & 63) * 16);
 #pragma unroll
-    for (int i = 0; i < kKeys * D / 8 / kThreads; ++i) {
-        const uint4 x = v[i * kThreads + tid];
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) odd |= (u[w] & 0x7f80u) == 0x7f80u || (u[w] & 0x7f800000u) == 0x7f800000u;
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t u = x[w];
+            odd |= (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+        }
     }
     return odd;
 }
@@ -234,44 +277,52 @@ __device__ __forceinline__ uint32_t visible(const AttnArgs& a, const AttnSeq& s,
 // A tile of V in LDS, rewritten by the workgroup: kind 0 with zeros for what is
 // not finite, else ones where it is NaN (1), +inf (2), -inf (3) and zeros elsewhere.
 template <int D>
-__device__ __forceinline__ void rewrite(uint4* v, int kind, int tid) {
+__device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 #pragma unroll 1
     for (int i = tid; i < kKeys * D / 8; i += kThreads) {
-        uint4 x = v[i];
-        uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        auto* at = lds_piece(v + (i >> 6) * Layout<D, true>::kBlock + (i & 63) * 16);
+        u32x4 x = *at;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             uint32_t r = 0;
 #pragma unroll
-            for (int at = 0; at < 32; at += 16) {
-                const uint32_t e = u[w] >> at & 0xffff;
+            for (int shift = 0; shift < 32; shift += 16) {
+                const uint32_t e = x[w] >> shift & 0xffff;
                 const int is = (e & 0x7f80) != 0x7f80 ? 0 : (e & 0x7f) ? 1 : e == 0x7f80 ? 2 : 3;
-                r |= (kind == 0 ? (is ? 0 : e) : is == kind ? 0x3f80u : 0) << at;
+                r |= (kind == 0 ? (is ? 0 : e) : is == kind ? 0x3f80u : 0) << shift;
             }
-            u[w] = r;
+            x[w] = r;
         }
-        v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        *at = x;
     }
 }
 
 // ---------------------------------------------------------------------------
-// A piece of a workgroup's range: some keys of one key head for 128 rows (token,
-// query head of the group) of a sequence; a wavefront has 32 of the rows.  64
-// keys at a time lie in LDS, the next 64 on their way there.
-//   S^T = K Q^T    keys x rows on MFMA, Q in registers for the whole chunk
+// A piece of a workgroup's range: some keys of one key head for a tile of rows
+// (token, query head of the group) of a sequence; a wavefront has RB blocks of
+// 32 of the rows, so that an operand read from LDS serves RB products.  64 keys
+// at a time lie in LDS, the next 64 on their way there.
+//   S^T = K Q^T    keys x rows on MFMA, Q in registers for the whole piece
 //   O^T += V^T P   V read transposed; the lanes hold P where the product wants it
 // The running maximum is raised only where a row's scores pass it by more than
 // 2^8: P then stays below 2^8, which costs no precision in floating point, and
-// O is rarely rescaled.  P is rounded to bf16 for the product (its sum is not):
-// 2^-9 of every weight, as much as the output's own rounding.
+// O is rarely rescaled.  P is rounded to bf16 for the product, 2^-9 of every
+// weight, as much as the output's own rounding; the sum is that of the rounded
+// weights.
 // A masked key has P = 0, but 0 times an infinity or NaN of its value would not
 // be 0: a tile with masked keys and such values is multiplied with zeros in
 // their place, and the rows that do see them get them from products of marks.
+// A wavefront has a SIMD's registers to itself and issues in order, so the main
+// loop stands in the order in which it is to run: beside every product what
+// the vector unit can do meanwhile.
 // ---------------------------------------------------------------------------
 template <AttnKind KIND, int D, bool F8>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
+    constexpr int RB = tile_rows(D) / 128, kRows = 128 * RB;
+    using KL = Layout<D, false>;
+    using VL = Layout<D, true>;
     extern __shared__ uint4 lds_raw[];
-    TileLds<D>& lds = *reinterpret_cast<TileLds<D>*>(lds_raw);
+    const uint32_t lds_k = __builtin_amdgcn_readfirstlane(lds_address(lds_raw)), lds_v = lds_k + TileLds<D>::kV;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AttnPlan plan = attn_plan<KIND>(a, threadIdx.x & 63);
     const int w = attn_range(plan, blockIdx.x);
@@ -291,17 +342,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
         if (it.all == 0) continue;
         const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
         const int all_rows = s.n * a.group;
-        const int row0 = it.tile * kTileRows, rows = min(kTileRows, all_rows - row0);
+        const int row0 = it.tile * kRows, rows = min(kRows, all_rows - row0);
         const int begin = it.unit * kKeys;
-        const int end = min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile));
-
-        const int my_row = min(row0 + wave * 32 + col, all_rows - 1);
-        const int token = my_row / a.group, head = h * a.group + my_row - token * a.group;
-        const uint32_t* anc =
-            KIND == kAttnVerify ? a.anc + (int64_t(at.b) * s.n + token) * ((a.d.T + 31) >> 5) : nullptr;
+        const int end = __builtin_amdgcn_readfirstlane(min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile)));
         const int32_t* table = a.table + at.b * a.d.table_stride;
         // tokens from here on are masked for some of the tile's rows
-        const int open_end = KIND == kAttnPrefill ? s.prefix + row0 / a.group + 1 : s.prefix;
+        const int open_end = KIND == kAttnPrefill ? __builtin_amdgcn_readfirstlane(s.prefix + row0 / a.group + 1) : s.prefix;
 
         bool missing = false;  // pages outside the pool
         for (int p = (begin >> a.page_shift) + tid; begin < end && p <= (end - 1) >> a.page_shift; p += kThreads) {
@@ -310,36 +356,49 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
         }
         missing = __builtin_amdgcn_readfirstlane(__syncthreads_or(missing));
 
-        bf16x8 q[D / 16];
-        const uint16_t* qp = a.q + (s.row0 + token) * a.d.q_stride + int64_t(head) * D + 8 * half;
+        int token[RB], head[RB];
+        bf16x8 q[RB][D / 16];
+        f32x16 o[RB][D / 32];
+        float m[RB], l[RB];  // m: what the powers are taken against
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            q[n] = load_frag(qp + 16 * n);
-            if constexpr (D == 256) asm volatile("" : "+a"(q[n]));  // beside the accumulators
+        for (int b = 0; b < RB; ++b) {
+            const int row = min(row0 + (wave * RB + b) * 32 + col, all_rows - 1);
+            token[b] = row / a.group;
+            head[b] = h * a.group + row - token[b] * a.group;
+            const uint16_t* qp = a.q + (s.row0 + token[b]) * a.d.q_stride + int64_t(head[b]) * D + 8 * half;
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                q[b][n] = load_frag(qp + 16 * n);
+                if constexpr (D == 256) asm volatile("" : "+a"(q[b][n]));  // beside the accumulators
+            }
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[b][n][j] = 0.0f;
+            m[b] = -inf;
+            l[b] = 0.0f;
         }
 
-        f32x16 o[D / 32];
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[n][j] = 0.0f;
-        float m = -inf, l = 0.0f;  // m: what the powers are taken against
-
-        // register i of x[j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col`
-        const uint32_t k_row = lds_address(lds.k) + col * (D * 2);
-        int k_col = (half ^ k_xor<D>(col)) << 4;
+        // Register i of a score x[b][j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col` of block b.
+        // K: piece 2 n + half of row 32 j + col; its permutation's higher bit swaps neighbouring n.
+        const int k_swap = KL::perm(col) >> 1, k_piece = (half ^ (KL::perm(col) & 1)) << 4;
+        const uint32_t k_even = lds_k + KL::row(col) + k_piece + 32 * k_swap, k_odd = k_even - 64 * k_swap;
         auto k_frag = [&](int j, int n, int buf) {
             return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(
-                k_row + buf * (kKeys * D * 2) + (k_col ^ n << 5) + j * (32 * D * 2));
+                (n & 1 ? k_odd : k_even) + buf * KL::kTile + 32 / KL::kRows * KL::kBlock * j + 32 * n);
         };
-        // k-slots 8 half .. 8 half + 7 of product k: keys 16 k + 4 half + {0 .. 3} and 8 more, whose rows have the same permutation
-        const int vr = 4 * half + ((lane & 15) >> 2);
-        const uint32_t v_row = lds_address(lds.v) + vr * (D * 2) + 8 * (lane & 1);
-        const int v_col = (2 * (lane >> 4 & 1) + ((lane & 3) >> 1) ^ v_xor<D>(vr)) << 4;
+        // V: k-slots 8 half .. 8 half + 7 of product k are keys 16 k + 4 half + {0 .. 3} and 8 more, whose rows have the
+        // same permutation; it swaps the 64 bytes of product n with those of n ^ v_swap.
+        const int vr = 4 * half + ((lane & 15) >> 2), v_swap = VL::perm(vr) >> 2;
+        const uint32_t v_row = lds_v + VL::row(vr) + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
+        constexpr int VN = D == 128 ? 4 : 2;  // v_swap < VN
+        uint32_t v_at[VN];
+#pragma unroll
+        for (int n = 0; n < VN; ++n) v_at[n] = v_row + 64 * (n ^ v_swap);
         auto v_frag = [&](int n, int k, int buf) {
-            const uint32_t at = v_row + buf * (kKeys * D * 2) + (v_col ^ n << 6) + k * (16 * D * 2);
-            const uint2 u = read_tr16(at), w = read_tr16(at + 8 * D * 2);
-            return __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
+            const uint32_t from = v_at[n % VN] + buf * VL::kTile + n / VN * VN * 64 + 16 / VL::kRows * VL::kBlock * k;
+            const uint2 x = read_tr16(from), y = read_tr16(from + VL::row(8));
+            return __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
         };
         const f32x16 zero{};
         // The largest of what x adds to a row, in powers of two.
@@ -350,224 +409,282 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             top = fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
             return top == -inf ? top : top * scale;
         };
-        auto raise = [&](float top) {
-            if (__ballot(top > m + 8.0f)) {
-                const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
-                m = m_new;
-                l *= keep;
+        auto raise = [&](int b, float top) {
+            if (__ballot(top > m[b] + 8.0f)) {
+                const float m_new = fmaxf(m[b], top), keep = exp2_fast(m[b] - finite_max(m_new));
+                m[b] = m_new;
+                l[b] *= keep;
 #pragma unroll
-                for (int n = 0; n < D / 32; ++n) {
-                    if constexpr (D == 256)
-                        update_acc(o[n], keep, {});
-                    else
-                        o[n] *= keep;
-                }
+                for (int n = 0; n < D / 32; ++n) update_acc(o[b][n], keep, {});
             }
         };
 
         if (begin < end) {
-            Stage<D, F8, false> sk;
-            Stage<D, F8, true> sv;
-            sk.init(a, h, end, lane);
-            sv.init(a, h, end, lane);
-            // V of the tile at t0 and K of the next one are in LDS; those after
-            // them may come (K behind the last tile is not used).
-            auto arrive = [&](int t0, int buf) {
-                if (t0 + kKeys < end) sk.store(lds.k[buf ^ 1], wave, lane);
-                sv.store(lds.v[buf], wave, lane);
-                loads_barrier<0>();
-                if (t0 + kKeys < end) {
-                    sk.begin(a, table, lds.k[buf], t0 + 2 * kKeys, end, wave, lane);
-                    sv.begin(a, table, lds.v[buf ^ 1], t0 + kKeys, end, wave, lane);
-                }
-            };
-            constexpr int L = Stage<D, F8, true>::L;
-            auto part = [&](int i) {
-                if (i < L)
-                    sk.part(i);
-                else
-                    sv.part(i - L);
-            };
-            sk.load(a, table, lds.k[0], begin, end, wave, lane);
-            sk.store(lds.k[0], wave, lane);
+            Loader<D, F8> load;
+            constexpr int L2 = 2 * load.L;
+            load.init(a, h, end, lane);
+            load.find(a, table, begin, end, wave, lane);
+            if (a.page_shift >= 4) {
+                load.k.at(lds_k, load.page, load.row, wave);
+#pragma unroll
+                for (int i = 0; i < load.L; ++i) load.k.part(i);
+            } else {
+                load.k.scattered(a, load.window, lds_k, begin, end, wave, lane);
+            }
+            load.k.store(lds_k, wave, lane);
             loads_barrier<0>();
-            if (begin + kKeys < end) sk.load(a, table, lds.k[1], begin + kKeys, end, wave, lane);
-            sv.load(a, table, lds.v[0], begin, end, wave, lane);
-            constexpr int NQ = D / 8, AHEAD = D == 128 ? 4 : 8;  // products of a tile with K (and with V), operands read ahead
-            f32x16 x[2];                          // scores of the tile at t0
+            // K of the tile behind the last is not used: it repeats what there is
+            load.begin(a, table, lds_k + KL::kTile, lds_v, begin, end, wave, lane);
+            if (a.page_shift >= 4)
 #pragma unroll
-            for (int i = 0; i < NQ; ++i) x[i & 1] = mfma32(k_frag(i & 1, i >> 1, 0), q[i >> 1], i < 2 ? zero : x[i & 1]);
-            int t0 = begin, buf = 0;
+                for (int i = 0; i < L2; ++i) load.part(i);
+            // V of the tile at t0 and K of the next one are in LDS; those after them may come.
+            auto arrive = [&](int t0, int buf) {
+                load.k.store(lds_k + (buf ^ 1) * KL::kTile, wave, lane);
+                load.v.store(lds_v + buf * VL::kTile, wave, lane);
+                loads_barrier<0>();
+                if (t0 + kKeys < end)
+                    load.begin(a, table, lds_k + buf * KL::kTile, lds_v + (buf ^ 1) * VL::kTile, t0 + kKeys, end, wave, lane);
+            };
+            // products of a tile with K, and with V; operands read ahead
+            constexpr int NS = D / 8, AHEAD = 8 / RB;
+            f32x16 x[RB][2];  // scores of the tile at t0
+            float top[RB];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const bf16x8 f = k_frag(i & 1, i >> 1, 0);
+#pragma unroll
+                for (int b = 0; b < RB; ++b) x[b][i & 1] = mfma32(f, q[b][i >> 1], i < 2 ? zero : x[b][i & 1]);
+            }
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                top[b] = -inf;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top[b] = fmaxf(top[b], x[b][i >> 4][i & 15]);
+                top[b] = largest(top[b]);
+            }
 
-            // Tiles that every row sees all of, but the last (pages of fewer than 16
-            // rows take the plain loop below for all): the scores of the
-            // next tile are formed beside the powers of this one and its maxima
-            // beside the products with V, step by step as they stand here.
-            const int open = missing || a.page_shift < 4 ? begin : min(max(open_end, begin), end - 1);
-            float top = -inf;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
-            top = largest(top);
-            for (; t0 + kKeys <= open; t0 += kKeys, buf ^= 1) {
+            // A tile that every row sees all of, and that is not the last: the
+            // scores y of the next tile beside the powers of this one's x, and
+            // its maxima beside the products with V.
+            auto turn = [&](f32x16 (&x)[RB][2], f32x16 (&y)[RB][2], int t0, auto buf) {
                 arrive(t0, buf);
-                k_col = fresh(k_col);
-                raise(top);
-                const float base = finite_max(m);
-                f32x16 y[2];
-                bf16x8 f[AHEAD], p[4];
+                float base[RB];
+                bf16x8 f[AHEAD], p[RB][4];
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    raise(b, top[b]);
+                    base[b] = finite_max(m[b]);
+                    top[b] = -inf;
+                }
+                // powers that are formed up to step i: 20 of 32 beside K, the others
+                // beside the first half of V, in time for the product that wants them
+                auto formed = [](int i) { return i <= NS ? i * 20 / NS : i >= NS + NS / 2 ? 32 : 20 + (i - NS) * 24 / NS; };
+                auto powers = [&](int i) {
+#pragma unroll
+                    for (int e = formed(i); e < formed(i + 1); ++e)
+#pragma unroll
+                        for (int b = 0; b < RB; ++b) {
+                            p[b][e >> 3][e & 7] = static_cast<__bf16>(exp2_fast(fmaf(x[b][e >> 4][e & 15], scale, -base[b])));
+                            if (e & 1) {
+                                const bf16x2 two{p[b][e >> 3][(e & 7) - 1], p[b][e >> 3][e & 7]}, one{1.0f, 1.0f};
+                                l[b] = __builtin_amdgcn_fdot2_f32_bf16(two, one, l[b], false);
+                            }
+                        }
+                };
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) f[i] = k_frag(i & 1, i >> 1, buf ^ 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    y[i & 1] = mfma32(f[i % AHEAD], q[i >> 1], i < 2 ? zero : y[i & 1]);
-                    const int r = i + AHEAD;
-                    f[i % AHEAD] = r < NQ ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NQ) % (D / 32), (r - NQ) / (D / 32), buf);
-                    if (i % (NQ / (2 * L)) == 0) part(i / (NQ / (2 * L)));
+                for (int i = 0; i < NS; ++i) {
 #pragma unroll
-                    for (int e = i * 32 / NQ; e < (i + 1) * 32 / NQ; ++e) {
-                        x[e >> 4][e & 15] = exp2_fast(fmaf(x[e >> 4][e & 15], scale, -base));
-                        p[e >> 3][e & 7] = static_cast<__bf16>(x[e >> 4][e & 15]);
-                        if (D < 256) l += x[e >> 4][e & 15];
+                    for (int b = 0; b < RB; ++b) y[b][i & 1] = mfma32(f[i % AHEAD], q[b][i >> 1], i < 2 ? zero : y[b][i & 1]);
+                    const int r = i + AHEAD;
+                    f[i % AHEAD] = r < NS ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NS) % (D / 32), (r - NS) / (D / 32), buf);
+                    if (i % (NS / L2) == 0) load.part(i / (NS / L2));
+                    powers(i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const int n = i % (D / 32), k = i / (D / 32), r = i + AHEAD;
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) o[b][n] = mfma32(f[i % AHEAD], p[b][k], o[b][n]);
+                    if (r < NS) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
+                    powers(NS + i);
+                    if (i >= NS / 2) {
+#pragma unroll
+                        for (int e = (i - NS / 2) * 64 / NS; e < (i - NS / 2 + 1) * 64 / NS; ++e)
+#pragma unroll
+                            for (int b = 0; b < RB; ++b) top[b] = fmaxf(top[b], y[b][e >> 4][e & 15]);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                top = -inf;
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    o[i % (D / 32)] = mfma32(f[i % AHEAD], p[i / (D / 32)], o[i % (D / 32)]);
-                    const int r = i + AHEAD;
-                    if (r < NQ) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
-                    if (D == 256) l += x[i >> 4 & 1][i & 15];  // elsewhere x has no registers by now
-                    if (i >= NQ / 2) {
-#pragma unroll
-                        for (int e = (i - NQ / 2) * 64 / NQ; e < (i - NQ / 2 + 1) * 64 / NQ; ++e)
-                            top = fmaxf(top, y[e >> 4][e & 15]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int b = 0; b < RB; ++b) top[b] = largest(top[b]);
+            };
+            int t0 = begin, buf = 0;
+            // (pages of fewer than 16 rows take the plain loop below for all tiles)
+            const int open = missing || a.page_shift < 4 ? begin : min(max(open_end, begin), end - 1);
+            {
+                f32x16 y[RB][2];
+                for (; t0 + 2 * kKeys <= open; t0 += 2 * kKeys) {
+                    turn(x, y, t0, std::integral_constant<int, 0>());
+                    turn(y, x, t0 + kKeys, std::integral_constant<int, 1>());
                 }
-                top = largest(top);
-                x[0] = y[0];
-                x[1] = y[1];
+                if (t0 + kKeys <= open) {
+                    turn(x, y, t0, std::integral_constant<int, 0>());
+#pragma unroll
+                    for (int b = 0; b < RB; ++b)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) x[b][j] = y[b][j];
+                    t0 += kKeys;
+                    buf = 1;
+                }
             }
+
+            // Other tiles, step by step.
+#pragma unroll 1
             for (; t0 < end; t0 += kKeys, buf ^= 1) {
                 arrive(t0, buf);
                 if (t0 + kKeys < end && a.page_shift >= 4)
 #pragma unroll
-                    for (int i = 0; i < 2 * L; ++i) part(i);
-                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+                    for (int i = 0; i < L2; ++i) load.part(i);
+                uint32_t see[RB][2];
                 bool odd = false;
-                if (missing || t0 + kKeys > min(open_end, end)) {
-                    odd = __builtin_amdgcn_readfirstlane(__syncthreads_or(any_odd<D>(lds.v[buf], tid)));
+                const bool masked = missing || t0 + kKeys > min(open_end, end);
+                if (masked) {
+                    odd = __builtin_amdgcn_readfirstlane(__syncthreads_or(any_odd<D>(lds_v + buf * VL::kTile, tid)));
                     if (odd) {
-                        rewrite<D>(lds.v[buf], 0, tid);
+                        rewrite<D>(lds_v + buf * VL::kTile, 0, tid);
                         __syncthreads();
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t bits = visible<KIND>(a, s, token, anc, t0 + 32 * j, end);
-                        if (missing) {
-                            const int t = t0 + 32 * j + col;
-                            const int page = t < end ? table[t >> a.page_shift] : -1;
-                            bits &= uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
-                        }
-                        see[j] = bits >> (4 * half);
-                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t there = 0xffffffffu;
+                    if (missing) {
+                        const int t = t0 + 32 * j + col;
+                        const int page = t < end ? table[t >> a.page_shift] : -1;
+                        there = uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
+                    }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!(see[j] >> (8 * (i >> 2) + (i & 3)) & 1)) x[j][i] = -inf;
-                top = -inf;
+                    for (int b = 0; b < RB; ++b) {
+                        uint32_t bits = there;
+                        if (masked)
+                            bits &= visible<KIND>(a, s, token[b],
+                                                  KIND == kAttnVerify
+                                                      ? a.anc + (int64_t(at.b) * s.n + token[b]) * ((a.d.T + 31) >> 5)
+                                                      : nullptr,
+                                                  t0 + 32 * j, end);
+                        see[b][j] = bits >> (4 * half);
+                    }
+                }
+                bf16x8 p[RB][4];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
-                raise(largest(top));
-                const float base = finite_max(m);
+                for (int b = 0; b < RB; ++b) {
+                    float most = -inf;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    bf16x8 p;
+                    for (int i = 0; i < 32; ++i) {
+                        if (!(see[b][i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) x[b][i >> 4][i & 15] = -inf;
+                        most = fmaxf(most, x[b][i >> 4][i & 15]);
+                    }
+                    raise(b, largest(most));
+                    const float base = finite_max(m[b]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 8 * (k & 1) + i;
-                        float e = exp2_fast(fmaf(x[k >> 1][r], scale, -base));
+                    for (int i = 0; i < 32; ++i) {
+                        float e = exp2_fast(fmaf(x[b][i >> 4][i & 15], scale, -base));
                         // a scale of zero turns -inf into NaN
-                        if (!(see[k >> 1] >> (8 * (r >> 2) + (r & 3)) & 1)) e = 0.0f;
-                        l += e;
-                        p[i] = static_cast<__bf16>(e);
+                        if (!(see[b][i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) e = 0.0f;
+                        p[b][i >> 3][i & 7] = static_cast<__bf16>(e);
+                        l[b] += static_cast<float>(p[b][i >> 3][i & 7]);
                     }
-#pragma unroll
-                    for (int n = 0; n < D / 32; ++n) o[n] = mfma32(v_frag(n, k, buf), p, o[n]);
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int n = 0; n < D / 32; ++n) {
+                        const bf16x8 f = v_frag(n, k, buf);
+#pragma unroll
+                        for (int b = 0; b < RB; ++b) o[b][n] = mfma32(f, p[b][k], o[b][n]);
+                    }
                 if (t0 + kKeys < end) {
 #pragma unroll
-                    for (int i = 0; i < NQ; ++i)
-                        x[i & 1] = mfma32(k_frag(i & 1, i >> 1, buf ^ 1), q[i >> 1], i < 2 ? zero : x[i & 1]);
+                    for (int i = 0; i < NS; ++i) {
+                        const bf16x8 f = k_frag(i & 1, i >> 1, buf ^ 1);
+#pragma unroll
+                        for (int b = 0; b < RB; ++b) x[b][i & 1] = mfma32(f, q[b][i >> 1], i < 2 ? zero : x[b][i & 1]);
+                    }
                 }
                 if (!odd) continue;
 #pragma unroll 1
                 for (int kind = 1; kind <= 3; ++kind) {
                     const float what = kind == 1 ? __builtin_nanf("") : kind == 2 ? inf : -inf;
+                    const uint32_t to = lds_v + buf * VL::kTile;
                     __syncthreads();
-                    Stage<D, F8, true> again = sv;
-                    again.load(a, table, lds.v[buf], t0, end, wave, lane);
-                    again.store(lds.v[buf], wave, lane);
-                    loads_barrier<0>();
-                    rewrite<D>(lds.v[buf], kind, tid);
-                    __syncthreads();
+                    Loader<D, F8> again = load;
+                    again.find(a, table, t0, end, wave, lane);
+                    if (a.page_shift >= 4) {
+                        again.v.at(to, again.page, again.row, wave);
 #pragma unroll
-                    for (int n = 0; n < D / 32; ++n) {
-                        f32x16 count;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) count[i] = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t bits = see[k >> 1];
-                            asm volatile("" : "+v"(bits));  // formed anew each time, to hold no registers for it
-                            bf16x8 one;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int r = 8 * (k & 1) + i;
-                                one[i] = static_cast<__bf16>((bits >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
-                            }
-                            count = mfma32(v_frag(n, k, buf), one, count);
-                        }
-                        float g[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
-                        if constexpr (D == 256) {
-                            update_acc(o[n], 1.0f, g);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[n][i] += g[i];
-                        }
+                        for (int i = 0; i < load.L; ++i) again.v.part(i);
+                    } else {
+                        again.v.scattered(a, again.window, to, t0, end, wave, lane);
                     }
+                    again.v.store(to, wave, lane);
+                    loads_barrier<0>();
+                    rewrite<D>(to, kind, tid);
+                    __syncthreads();
+#pragma unroll
+                    for (int b = 0; b < RB; ++b)
+#pragma unroll
+                        for (int n = 0; n < D / 32; ++n) {
+                            f32x16 count = zero;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t bits = see[b][k >> 1];
+                                asm volatile("" : "+v"(bits));  // formed anew each time, to hold no registers for it
+                                bf16x8 one;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int r = 8 * (k & 1) + i;
+                                    one[i] = static_cast<__bf16>((bits >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
+                                }
+                                count = mfma32(v_frag(n, k, buf), one, count);
+                            }
+                            float g[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
+                            update_acc(o[b][n], 1.0f, g);
+                        }
                 }
             }
         }
 
-        l += __shfl_xor(l, 32);
-        if (wave * 32 + col < rows) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            l[b] += __shfl_xor(l[b], 32);
+            const int r = (wave * RB + b) * 32 + col;
+            if (r >= rows) continue;
             if (it.units < it.all) {
-                float* part = part_out(a, 2 * int64_t(w) + (first ? 0 : 1), kTileRows, D);
-                const int r = wave * 32 + col;
+                float* part = part_out(a, 2 * int64_t(w) + (first ? 0 : 1), kRows, D);
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         *reinterpret_cast<f32x4*>(part + r * D + 32 * n + 8 * i + 4 * half) =
-                            f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
+                            f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]};
                 if (half == 0) {
-                    part[kTileRows * D + r] = m;
-                    part[kTileRows * (D + 1) + r] = l;
+                    part[kRows * D + r] = m[b];
+                    part[kRows * (D + 1) + r] = l[b];
                 }
             } else {
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        attn_store<D>(a, s.row0 + token, h, head, 32 * n + 8 * i + 4 * half,
-                                      f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]}, l);
+                        attn_store<D>(a, s.row0 + token[b], h, head[b], 32 * n + 8 * i + 4 * half,
+                                      f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]}, l[b]);
             }
         }
         if (u < u_end) __syncthreads();  // the next piece overwrites LDS
@@ -577,7 +694,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
 template <AttnKind KIND, int D, bool F8>
 hipError_t launch_one(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
     const auto kernel = tiles_kernel<KIND, D, F8>;
-    constexpr int bytes = sizeof(TileLds<D>);
+    constexpr int bytes = TileLds<D>::kBytes;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
