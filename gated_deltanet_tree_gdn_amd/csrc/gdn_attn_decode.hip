@@ -102,7 +102,8 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
     const int col = lane & 15, g = lane >> 4;
     const int heads = a.cache.H_kv * a.head_tiles;
     const AttnPlan plan = attn_plan<kAttnDecode>(a, lane);
-    const int w = attn_range(plan, blockIdx.x);
+    const int w = attn_range(a, plan, blockIdx.x);
+    if (w < 0) return;
     const int64_t u0 = w * plan.per, u_end = min(u0 + plan.per, plan.units * heads);
     const float inf = __builtin_inff();
     AttnPlace at;
@@ -244,7 +245,7 @@ hipError_t launch(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid(a.slots);
+    const dim3 grid((a.teams + 7) / 8 * 8);
     switch (a.cache.d) {
         case 64: return launch<64>(a, grid, stream);
         case 128: return launch<128>(a, grid, stream);

@@ -60,7 +60,8 @@ struct AttnArgs {
     int group;       // query heads of a key head
     int tile_rows;   // (token, head of the group) rows of a workgroup
     int head_tiles;  // decode: tiles of 16 heads that the group is cut into, else 1
-    int slots;       // workgroups that the units are divided over, a multiple of 8
+    int team;        // workgroups side by side: the tiles of a tree, otherwise 1
+    int teams;       // that the units are divided over
     int unit;        // keys of a unit
     int min_units;   // of a workgroup
     bool join;       // tiles may be divided
@@ -68,7 +69,7 @@ struct AttnArgs {
 // Rows of a tile: single tokens; otherwise 4 wavefronts of 64 rows, of 32 where
 // the accumulators of more do not fit the registers.
 constexpr int kDecodeRows = 16;
-constexpr int tile_rows(int d) { return d == 256 ? 128 : 256; }
+constexpr int tile_rows(int d) { return d == 256 ? 128 : 128; }
 
 // Fills the derived members.
 void attn_shape(AttnArgs& a);

@@ -41,10 +41,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63, p = tid % C, k = tid / C;
     const int heads = a.cache.H_kv * a.head_tiles;
-    const int blocks = one ? min(a.group, kDecodeRows) : kTileRows / kJoinRows;  // workgroups of a tile
+    const int blocks = (one ? min(a.group, kDecodeRows) : kTileRows / kJoinRows) * a.team;  // workgroups of a tile (or team)
     const int64_t wg = block_id(), grid_tiles = int64_t(gridDim.x) * gridDim.y / heads / blocks;
     if (wg >= grid_tiles * heads * blocks) return;
-    const int block = int(wg % blocks), hh = int(wg / blocks % heads), h = hh / a.head_tiles;
+    const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team, hh = int(wg / blocks % heads), h = hh / a.head_tiles;
     const AttnPlan plan = attn_plan<KIND>(a, lane);
     AttnPlace at;
     for (int64_t tile = wg / blocks / heads; attn_find<KIND, true>(a, tile, lane, at); tile += grid_tiles) {
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
         const int parts = int(w1 - w0) + 1;
         // the first workgroup either starts with this tile or has it as its last
         auto part = [&](int i) {
-            return part_out(a, i ? 2 * (w0 + i) : 2 * w0 + (g0 == w0 * plan.per ? 0 : 1), rows_of_part, D);
+            return part_out(a, 2 * ((w0 + i) * a.team + mate) + (i == 0 && g0 != w0 * plan.per), rows_of_part, D);
         };
         if (parts > 1) {
             if constexpr (one) {
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
                     }
                 }
             } else {
-                const int row0 = t * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
+                const int row0 = (KIND == kAttnVerify ? mate : t) * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
                 for (int r = block * kJoinRows + k; r < min((block + 1) * kJoinRows, rows); r += K) {
                     Joined x;
                     for (int i = 0; i < parts; ++i) {
@@ -133,7 +133,7 @@ hipError_t launch_join(const AttnArgs& a, const dim3& grid, hipStream_t stream) 
 int64_t max_tiles(const AttnArgs& a) {
     const int64_t rows = int64_t(a.d.T) * a.group;
     return a.kind == kAttnDecode   ? a.d.B
-           : a.kind == kAttnVerify ? a.d.B * ((rows + a.tile_rows - 1) / a.tile_rows)
+           : a.kind == kAttnVerify ? a.d.B
                                    : rows / a.tile_rows + a.d.B;
 }
 }  // namespace
@@ -150,19 +150,22 @@ void attn_shape(AttnArgs& a) {
     const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
     // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
     // overlap, where cu_seqlens decreases, and each may then have all rows)
-    const int64_t tiles = one ? a.d.B : a.d.B * ((rows + a.tile_rows - 1) / a.tile_rows);
-    const int64_t units = tiles * a.cache.H_kv * a.head_tiles * ((cap + a.unit - 1) / a.unit + 2);
-    a.slots = int(std::min<int64_t>(one && a.cache.d < 256 ? 2 * kCu : kCu, ((units + a.min_units - 1) / a.min_units + 7) / 8 * 8));
-    a.join = cap > a.unit;  // otherwise a tile is one unit
+    const int64_t tiles = (rows + a.tile_rows - 1) / a.tile_rows;
+    const int64_t units = (a.kind == kAttnPrefill ? tiles : 1) * a.d.B * a.cache.H_kv * a.head_tiles *
+                          ((cap + a.unit - 1) / a.unit + 2);
+    a.team = a.kind == kAttnVerify ? int(tiles) : 1;
+    a.teams = int(std::max<int64_t>(
+        1, std::min<int64_t>((a.cache.d < 256 ? 2 * kCu : kCu) / a.team, (units + a.min_units - 1) / a.min_units)));
+    a.join = a.teams > 1 && cap > a.unit;  // otherwise a tile is one unit
 }
 
 size_t attn_ws_bytes(const AttnArgs& a) {
-    return a.join ? size_t(2 * a.slots) * a.tile_rows * (a.cache.d + 2) * sizeof(float) : 0;
+    return a.join ? size_t(2 * a.teams) * a.team * a.tile_rows * (a.cache.d + 2) * sizeof(float) : 0;
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
     const int64_t heads = int64_t(a.cache.H_kv) * a.head_tiles;
-    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows / kJoinRows;
+    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows / kJoinRows * a.team;
     const dim3 grid = grid_of(max_tiles(a) * heads * blocks);
     return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, grid, stream)
            : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, grid, stream)

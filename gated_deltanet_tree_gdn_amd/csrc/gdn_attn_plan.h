@@ -11,7 +11,9 @@
 // parts 2 w and 2 w + 1 of the workspace and are joined by another launch.
 //
 // In a prompt the last tile sees most keys and the first fewest, so tiles are
-// taken in pairs from both ends, and every pair counts the same.
+// taken in pairs from both ends, and every pair counts the same.  The tiles of a
+// tree all see the same keys: a team of as many workgroups takes them side by
+// side, as one unit, so that the keys come from memory once.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -70,7 +72,7 @@ __device__ __forceinline__ AttnSeq attn_seq_uniform(const AttnArgs& a, int b) {
 
 template <AttnKind KIND>
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnSeq& s) {
-    if constexpr (KIND == kAttnDecode) return 1;
+    if constexpr (KIND != kAttnPrefill) return 1;  // a tree: each workgroup of a team has one
     return int((int64_t(s.n) * a.group + a.tile_rows - 1) / a.tile_rows);
 }
 
@@ -124,8 +126,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return __builtin_amdgcn_readfirstlane(uint32_t(a) / uint32_t(b));
 }
 
-// The units of one key head (and head tile), those of a workgroup, and the
-// number of workgroups that have any.
+// The units of one key head (and head tile), those of a workgroup (team), and
+// the number of workgroups (teams) that have any.
 struct AttnPlan {
     int64_t units, per;
     int ranges;
@@ -140,7 +142,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane) {
     AttnPlan p;
     p.units = read_lane64(a.d.B == 1 ? units : wave_sum64(units), 0);
     const int64_t all = p.units * (a.cache.H_kv * a.head_tiles);
-    p.per = max(quotient(all + a.slots - 1, a.slots), int64_t(a.min_units));
+    p.per = max(quotient(all + a.teams - 1, a.teams), int64_t(a.min_units));
     p.ranges = int(quotient(all + p.per - 1, p.per));
     return p;
 }
@@ -240,11 +242,12 @@ __device__ __forceinline__ float* part_out(const AttnArgs& a, int64_t part, int 
     return static_cast<float*>(a.ws) + part * rows * (D + 2);
 }
 
-// The range of workgroup `wg` of the grid, plan.ranges if none.  Workgroups go
-// to the 8 XCDs in turn; neighbouring ranges, which share keys, go to one.
-__device__ __forceinline__ int attn_range(const AttnPlan& plan, int wg) {
-    const int per_xcd = (plan.ranges + 7) >> 3, w = (wg & 7) * per_xcd + (wg >> 3);
-    return wg >> 3 < per_xcd ? min(w, plan.ranges) : plan.ranges;
+// The number of workgroup `wg` of the grid, range times team plus place in the
+// team; -1 if it has no range.  Workgroups go to the 8 XCDs in turn; teams stay
+// on one, and so do neighbouring ranges, which share keys.
+__device__ __forceinline__ int attn_range(const AttnArgs& a, const AttnPlan& plan, int wg) {
+    const int per_xcd = ((plan.ranges + 7) >> 3) * a.team, w = (wg & 7) * per_xcd + (wg >> 3);
+    return wg >> 3 < per_xcd && w < plan.ranges * a.team ? w : -1;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -146,7 +146,8 @@ struct Stage {
             x[j] = *reinterpret_cast<const uint4*>(base + more + off);
         } else {
             const uint64_t bits = reinterpret_cast<uint64_t>(base);
-            load_to_lds(i32x4{int32_t(bits), int32_t(bits >> 32 & 0xffff), 0x7fffffff, 0x00027000}, off, more,
+            const int lo = __builtin_amdgcn_readfirstlane(int(bits)), hi = __builtin_amdgcn_readfirstlane(int(bits >> 32 & 0xffff));
+            load_to_lds(i32x4{lo, hi, 0x7fffffff, 0x00027000}, off, __builtin_amdgcn_readfirstlane(more),
                         __builtin_amdgcn_readfirstlane(to_lds) + To::kBlock * j);
         }
     }
@@ -207,8 +208,8 @@ struct Loader {
             row = t0 & (a.cache.page_size - 1);
         }
     }
-    // Part of V's tile at t0 and K's at t0 + kKeys, all of it where pages are
-    // small; the other parts follow with part().
+    // V's tile at t0 and K's at t0 + kKeys: all of it where pages are small,
+    // otherwise the loads follow with k.part() and v.part().
     __device__ __forceinline__ void begin(const AttnArgs& a, const int32_t* table, uint32_t k_lds, uint32_t v_lds, int t0,
                                           int end, int wave, int lane) {
         if (a.page_shift >= 4) {
@@ -221,12 +222,6 @@ struct Loader {
             find(a, table, t0 + kKeys, end, wave, lane);
             k.scattered(a, window, k_lds, t0 + kKeys, end, wave, lane);
         }
-    }
-    __device__ __forceinline__ void part(int i) {
-        if (i < L)
-            k.part(i);
-        else
-            v.part(i - L);
     }
 };
 
@@ -317,7 +312,7 @@ __device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 // the vector unit can do meanwhile.
 // ---------------------------------------------------------------------------
 template <AttnKind KIND, int D, bool F8>
-__global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnArgs a) {
     constexpr int RB = tile_rows(D) / 128, kRows = 128 * RB;
     using KL = Layout<D, false>;
     using VL = Layout<D, true>;
@@ -325,8 +320,10 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
     const uint32_t lds_k = __builtin_amdgcn_readfirstlane(lds_address(lds_raw)), lds_v = lds_k + TileLds<D>::kV;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AttnPlan plan = attn_plan<KIND>(a, threadIdx.x & 63);
-    const int w = attn_range(plan, blockIdx.x);
-    const int64_t u0 = w * plan.per, u_end = min(u0 + plan.per, plan.units * a.cache.H_kv);
+    const int w = attn_range(a, plan, blockIdx.x);
+    if (w < 0) return;
+    const int team = __builtin_amdgcn_readfirstlane(w / a.team), mate = w - team * a.team;
+    const int64_t u0 = team * plan.per, u_end = min(u0 + plan.per, plan.units * a.cache.H_kv);
     const float inf = __builtin_inff();
 
     AttnPlace at;
@@ -342,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
         if (it.all == 0) continue;
         const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
         const int all_rows = s.n * a.group;
-        const int row0 = it.tile * kRows, rows = min(kRows, all_rows - row0);
+        const int row0 = (KIND == kAttnVerify ? mate : it.tile) * kRows, rows = min(kRows, all_rows - row0);
         const int begin = it.unit * kKeys;
         const int end = __builtin_amdgcn_readfirstlane(min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile)));
         const int32_t* table = a.table + at.b * a.d.table_stride;
@@ -415,19 +412,31 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
                 m[b] = m_new;
                 l[b] *= keep;
 #pragma unroll
-                for (int n = 0; n < D / 32; ++n) update_acc(o[b][n], keep, {});
+                for (int n = 0; n < D / 32; ++n) {
+                    if constexpr (D == 256)
+                        update_acc(o[b][n], keep, {});
+                    else
+                        o[b][n] *= keep;
+                }
             }
         };
 
         if (begin < end) {
             Loader<D, F8> load;
-            constexpr int L2 = 2 * load.L;
+            constexpr int L = load.L;
+            auto rest = [&] {  // of the loads of one tile, at once
+                if (a.page_shift < 4) return;
+#pragma unroll
+                for (int i = 0; i < L; ++i) load.k.part(i);
+#pragma unroll
+                for (int i = 0; i < L; ++i) load.v.part(i);
+            };
             load.init(a, h, end, lane);
             load.find(a, table, begin, end, wave, lane);
             if (a.page_shift >= 4) {
                 load.k.at(lds_k, load.page, load.row, wave);
 #pragma unroll
-                for (int i = 0; i < load.L; ++i) load.k.part(i);
+                for (int i = 0; i < L; ++i) load.k.part(i);
             } else {
                 load.k.scattered(a, load.window, lds_k, begin, end, wave, lane);
             }
@@ -435,19 +444,18 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
             loads_barrier<0>();
             // K of the tile behind the last is not used: it repeats what there is
             load.begin(a, table, lds_k + KL::kTile, lds_v, begin, end, wave, lane);
-            if (a.page_shift >= 4)
-#pragma unroll
-                for (int i = 0; i < L2; ++i) load.part(i);
-            // V of the tile at t0 and K of the next one are in LDS; those after them may come.
-            auto arrive = [&](int t0, int buf) {
+            rest();
+            // K of the tile after t0 and, but for the last PENDING loads, V of that
+            // at t0 are in LDS; those after them may come.
+            auto arrive = [&](int t0, int buf, auto pending) {
                 load.k.store(lds_k + (buf ^ 1) * KL::kTile, wave, lane);
                 load.v.store(lds_v + buf * VL::kTile, wave, lane);
-                loads_barrier<0>();
+                loads_barrier<pending>();
                 if (t0 + kKeys < end)
                     load.begin(a, table, lds_k + buf * KL::kTile, lds_v + (buf ^ 1) * VL::kTile, t0 + kKeys, end, wave, lane);
             };
             // products of a tile with K, and with V; operands read ahead
-            constexpr int NS = D / 8, AHEAD = 8 / RB;
+            constexpr int NS = D / 8, AHEAD = D == 256 ? 8 : 4;
             f32x16 x[RB][2];  // scores of the tile at t0
             float top[RB];
 #pragma unroll
@@ -466,9 +474,13 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
 
             // A tile that every row sees all of, and that is not the last: the
             // scores y of the next tile beside the powers of this one's x, and
-            // its maxima beside the products with V.
+            // its maxima beside the products with V.  Loads have a whole turn to
+            // arrive: K's are issued beside the products with K and waited for
+            // before those of the next turn, V's likewise (e4m3, which waits in
+            // registers, has V's beside the products with V as well, where x no
+            // longer needs them, and stores both at once).
             auto turn = [&](f32x16 (&x)[RB][2], f32x16 (&y)[RB][2], int t0, auto buf) {
-                arrive(t0, buf);
+                arrive(t0, buf, std::integral_constant<int, F8 ? 0 : L>());
                 float base[RB];
                 bf16x8 f[AHEAD], p[RB][4];
 #pragma unroll
@@ -500,8 +512,9 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
 #pragma unroll
                     for (int b = 0; b < RB; ++b) y[b][i & 1] = mfma32(f[i % AHEAD], q[b][i >> 1], i < 2 ? zero : y[b][i & 1]);
                     const int r = i + AHEAD;
+                    if (!F8 && r == NS) loads_barrier<L>();  // V is there
                     f[i % AHEAD] = r < NS ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NS) % (D / 32), (r - NS) / (D / 32), buf);
-                    if (i % (NS / L2) == 0) load.part(i / (NS / L2));
+                    if (i < L) load.k.part(i);
                     powers(i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -510,6 +523,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
                     const int n = i % (D / 32), k = i / (D / 32), r = i + AHEAD;
 #pragma unroll
                     for (int b = 0; b < RB; ++b) o[b][n] = mfma32(f[i % AHEAD], p[b][k], o[b][n]);
+                    if (const int j = F8 ? i - NS / 2 : i; j >= 0 && j < L) load.v.part(j);
                     if (r < NS) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
                     powers(NS + i);
                     if (i >= NS / 2) {
@@ -546,10 +560,8 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
             // Other tiles, step by step.
 #pragma unroll 1
             for (; t0 < end; t0 += kKeys, buf ^= 1) {
-                arrive(t0, buf);
-                if (t0 + kKeys < end && a.page_shift >= 4)
-#pragma unroll
-                    for (int i = 0; i < L2; ++i) load.part(i);
+                arrive(t0, buf, std::integral_constant<int, 0>());
+                if (t0 + kKeys < end) rest();
                 uint32_t see[RB][2];
                 bool odd = false;
                 const bool masked = missing || t0 + kKeys > min(open_end, end);
@@ -627,7 +639,7 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
                     if (a.page_shift >= 4) {
                         again.v.at(to, again.page, again.row, wave);
 #pragma unroll
-                        for (int i = 0; i < load.L; ++i) again.v.part(i);
+                        for (int i = 0; i < L; ++i) again.v.part(i);
                     } else {
                         again.v.scattered(a, again.window, to, t0, end, wave, lane);
                     }
@@ -655,7 +667,12 @@ __global__ __launch_bounds__(kThreads, 1) void tiles_kernel(AttnArgs a) {
                             float g[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
-                            update_acc(o[b][n], 1.0f, g);
+                            if constexpr (D == 256) {
+                                update_acc(o[b][n], 1.0f, g);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[b][n][i] += g[i];
+                            }
                         }
                 }
             }
@@ -706,7 +723,7 @@ hipError_t launch_one(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 
 template <AttnKind KIND>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid(a.slots);
+    const dim3 grid((a.teams + 7) / 8 * 8 * a.team);
     const bool f8 = a.cache.dtype == GDN_E4M3;
     switch (a.cache.d) {
         case 64: return f8 ? launch_one<KIND, 64, true>(a, grid, stream) : launch_one<KIND, 64, false>(a, grid, stream);

@@ -205,6 +205,9 @@ def test_workspaces_have_room_for_every_part(lib):
         rows = 16 if kind == "decode" else 128
         assert need(lib, kind, d, cache()) == 2 * 512 * rows * 130 * 4  # rows of 128 + 2
         assert 0 < need(lib, kind, dims(B=1, T=1, max_pages=16), cache()) < 2 * 64 * rows * 130 * 4
+    # trees of 5 tiles: teams of 5; more tiles than fit at once: whole tiles only
+    assert need(lib, "verify", dims(B=100, T=160), cache()) == 2 * (512 // 5) * 5 * 128 * 130 * 4
+    assert need(lib, "verify", dims(T=256, H_q=2 * 300, q_stride=76800), cache()) == 0
 
 
 def test_binding_has_no_cpu_fallback():
