@@ -100,19 +100,16 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
     __shared__ float ml[kWaves][2][kDecodeRows];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
-    const int heads = a.cache.H_kv * a.head_tiles;
-    const AttnPlan plan = attn_plan<kAttnDecode>(a, lane);
-    const int w = attn_range(a, plan, blockIdx.x);
-    if (w < 0) return;
-    const int64_t u0 = w * plan.per, u_end = min(u0 + plan.per, plan.units * heads);
     const float inf = __builtin_inff();
+    AttnRange range;
     AttnPlace at;
-    for (int64_t u = u0; u < u_end;) {
-        const int hh = int(quotient(u, plan.units)), h = hh / a.head_tiles, head0 = (hh - h * a.head_tiles) * kDecodeRows;
-        const int64_t uh = u - hh * plan.units;
-        if (at.b < 0 || uh < at.first || uh >= at.first + at.count) attn_find<kAttnDecode, false>(a, uh, lane, at);
-        const AttnSeq s = attn_seq_uniform<kAttnDecode>(a, at.b);
-        const AttnPiece it = attn_piece<kAttnDecode>(a, s, 1, uh - at.first, u_end - u);
+    if (!attn_begin<kAttnDecode>(a, blockIdx.x, lane, range, at)) return;
+    for (int64_t u = range.u; u < range.end;) {
+        const int hh = int(quotient(u, range.units)), h = hh / a.head_tiles, head0 = (hh - h * a.head_tiles) * kDecodeRows;
+        const int64_t uh = u - hh * range.units;
+        if (uh < at.first || uh >= at.first + at.count) attn_find<kAttnDecode, false>(a, uh, lane, at);
+        const AttnSeq& s = at.s;
+        const AttnPiece it = attn_piece<kAttnDecode>(a, s, 1, uh - at.first, range.end - u);
         const int rows = min(a.group - head0, kDecodeRows);
         const int64_t q_head = int64_t(h) * a.group + head0;
         constexpr int size = F8 ? 1 : 2;
@@ -218,7 +215,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
                 sum += ml[w][1][r] * f;
             }
             if (it.units < it.all) {
-                float* part = part_out(a, 2 * int64_t(w) + (u > u0), kDecodeRows, D);
+                float* part = part_out(a, 2 * int64_t(range.w) + (u > range.u), kDecodeRows, D);
                 reinterpret_cast<f32x4*>(part)[i] = acc;
                 if (p == 0) {
                     part[kDecodeRows * D + r] = top;
@@ -229,7 +226,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
             }
         }
         u += it.units;
-        if (u < u_end) __syncthreads();  // the next piece overwrites what is joined here
+        if (u < range.end) __syncthreads();  // the next piece overwrites what is joined here
     }
 }
 

@@ -14,7 +14,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJoinRows = 16;  // rows of a workgroup that joins a tile of many
+constexpr int kJoinPieces = 2;  // of 4 elements, of a thread that joins tiles
 
 struct Joined {
     f32x4 acc{0, 0, 0, 0};
@@ -28,27 +28,34 @@ struct Joined {
     }
 };
 
-// Parts of a tile's row, joined in the order of the keys.  Single tokens: a
+// Parts of a tile's rows, joined in the order of the keys.  Single tokens: a
 // workgroup for every row, since there are few and their parts may be hundreds;
-// the workgroup's threads take the parts in turn.  Tiles: D / 4 threads of a
-// row take its parts one after another.
+// the workgroup's threads take the parts in turn.  Tiles: every thread has
+// kJoinPieces pieces of 4 elements, in the order in which the parts hold them.
 template <AttnKind KIND, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
-    constexpr int C = D / 4, K = kThreads / C;  // threads of a row, rows (or shares of the parts) at a time
+    constexpr int C = D / 4, K = kThreads / C;  // threads of a row, shares of the parts
     constexpr bool one = KIND == kAttnDecode;
     constexpr int kTileRows = tile_rows(D), rows_of_part = one ? kDecodeRows : kTileRows;
     __shared__ f32x4 share[one ? K : 1][C];
     __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
-    const int tid = threadIdx.x, lane = tid & 63, p = tid % C, k = tid / C;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int heads = a.cache.H_kv * a.head_tiles;
-    const int blocks = (one ? min(a.group, kDecodeRows) : kTileRows / kJoinRows) * a.team;  // workgroups of a tile (or team)
+    // workgroups of a tile (or team)
+    const int blocks = (one ? min(a.group, kDecodeRows) : kTileRows * C / (kThreads * kJoinPieces)) * a.team;
     const int64_t wg = block_id(), grid_tiles = int64_t(gridDim.x) * gridDim.y / heads / blocks;
     if (wg >= grid_tiles * heads * blocks) return;
-    const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team, hh = int(wg / blocks % heads), h = hh / a.head_tiles;
-    const AttnPlan plan = attn_plan<KIND>(a, lane);
+    const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team, hh = int(wg / blocks % heads);
+    const int h = hh / a.head_tiles;
+    AttnLane<KIND> x;
+    const AttnPlan plan = attn_plan<KIND>(a, lane, x);
     AttnPlace at;
-    for (int64_t tile = wg / blocks / heads; attn_find<KIND, true>(a, tile, lane, at); tile += grid_tiles) {
-        const AttnSeq s = attn_seq_uniform<KIND>(a, at.b);
+    for (int64_t tile = wg / blocks / heads;; tile += grid_tiles) {
+        int64_t before = 0, units_before = 0;
+        if (!attn_find_here<KIND, true>(a, x, 0, tile, lane, before, units_before, at) &&
+            (a.d.B <= 64 || !attn_find<KIND, true>(a, tile, lane, at)))
+            return;
+        const AttnSeq s = at.s;
         const int t = int(tile - at.first), tiles = int(at.count);
         const int64_t g0 = hh * plan.units + at.first_unit + attn_tile_unit<KIND>(a, s, tiles, t);
         const int64_t w0 = quotient(g0, plan.per), w1 = quotient(g0 + attn_units<KIND>(a, s, t) - 1, plan.per);
@@ -59,36 +66,41 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
         };
         if (parts > 1) {
             if constexpr (one) {
+                const int p = tid % C, k = tid / C;
                 const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
                 if (row < a.group - head0) {
-                    Joined x;
+                    Joined y;
                     for (int i = k; i < parts; i += K) {
-                        const float* y = part(i);
-                        x.add(*reinterpret_cast<const f32x4*>(y + row * D + 4 * p), y[kDecodeRows * D + row],
-                              y[kDecodeRows * (D + 1) + row]);
+                        const float* z = part(i);
+                        y.add(*reinterpret_cast<const f32x4*>(z + row * D + 4 * p), z[kDecodeRows * D + row],
+                              z[kDecodeRows * (D + 1) + row]);
                     }
-                    share[k][p] = x.acc;
+                    share[k][p] = y.acc;
                     if (p == 0) {
-                        share_m[k] = x.m;
-                        share_l[k] = x.l;
+                        share_m[k] = y.m;
+                        share_l[k] = y.l;
                     }
                     __syncthreads();
                     if (k == 0) {
-                        for (int i = 1; i < K; ++i) x.add(share[i][p], share_m[i], share_l[i]);
-                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, x.acc, x.l);
+                        for (int i = 1; i < K; ++i) y.add(share[i][p], share_m[i], share_l[i]);
+                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, y.acc, y.l);
                     }
                 }
             } else {
                 const int row0 = (KIND == kAttnVerify ? mate : t) * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
-                for (int r = block * kJoinRows + k; r < min((block + 1) * kJoinRows, rows); r += K) {
-                    Joined x;
+#pragma unroll
+                for (int j = 0; j < kJoinPieces; ++j) {
+                    const int e = (block * kJoinPieces + j) * kThreads + tid;  // 32 rows have 32 C pieces
+                    const int r = e / (32 * C) * 32 + (e & 31), d = e / 64 % (C / 2) * 8 + (e >> 5 & 1) * 4;
+                    if (r >= rows) continue;
+                    Joined y;
+#pragma unroll 4
                     for (int i = 0; i < parts; ++i) {
-                        const float* y = part(i);
-                        x.add(*reinterpret_cast<const f32x4*>(y + r * D + 4 * p), y[kTileRows * D + r],
-                              y[kTileRows * (D + 1) + r]);
+                        const float* z = part(i);
+                        y.add(reinterpret_cast<const f32x4*>(z)[e], z[kTileRows * D + r], z[kTileRows * (D + 1) + r]);
                     }
                     const int token = (row0 + r) / a.group;
-                    attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, 4 * p, x.acc, x.l);
+                    attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, d, y.acc, y.l);
                 }
             }
         }
@@ -165,7 +177,7 @@ size_t attn_ws_bytes(const AttnArgs& a) {
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
     const int64_t heads = int64_t(a.cache.H_kv) * a.head_tiles;
-    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows / kJoinRows * a.team;
+    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows * (a.cache.d / 4) / (kThreads * kJoinPieces) * a.team;
     const dim3 grid = grid_of(max_tiles(a) * heads * blocks);
     return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, grid, stream)
            : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, grid, stream)

@@ -59,17 +59,6 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
     return s;
 }
 
-// The same of a sequence that all lanes agree on.
-template <AttnKind KIND>
-__device__ __forceinline__ AttnSeq attn_seq_uniform(const AttnArgs& a, int b) {
-    AttnSeq s = attn_seq<KIND>(a, b);
-    s.n = __builtin_amdgcn_readfirstlane(s.n);
-    s.row0 = KIND == kAttnPrefill ? __builtin_amdgcn_readfirstlane(int(s.row0)) : s.row0;
-    s.prefix = __builtin_amdgcn_readfirstlane(s.prefix);
-    s.keys = __builtin_amdgcn_readfirstlane(s.keys);
-    return s;
-}
-
 template <AttnKind KIND>
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnSeq& s) {
     if constexpr (KIND != kAttnPrefill) return 1;  // a tree: each workgroup of a team has one
@@ -132,12 +121,79 @@ struct AttnPlan {
     int64_t units, per;
     int ranges;
 };
+// A sequence that all lanes agree on, the first of its units (join: tiles, and
+// units) within the key head, and how many it has.
+struct AttnPlace {
+    int b = -1;
+    int64_t first = 0, count = 0, first_unit = 0;
+    AttnSeq s;
+};
+// What a lane knows of 64 sequences in a row.
 template <AttnKind KIND>
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane) {
+struct AttnLane {
+    AttnSeq s{0, 0, 0, 0};
+    int tiles = 0;
     int64_t units = 0;
-    for (int b = lane; b < a.d.B; b += 64) {
-        const AttnSeq s = attn_seq<KIND>(a, b);
-        units += attn_seq_units<KIND>(a, s, attn_tiles<KIND>(a, s));
+    __device__ __forceinline__ void read(const AttnArgs& a, int b) {
+        s = AttnSeq{0, 0, 0, 0};
+        tiles = 0;
+        units = 0;
+        if (b < a.d.B) {
+            s = attn_seq<KIND>(a, b);
+            tiles = attn_tiles<KIND>(a, s);
+            units = attn_seq_units<KIND>(a, s, tiles);
+        }
+    }
+};
+// The sequence among those from `base` on that holds unit `u` (with TILES: tile
+// u); otherwise the numbers before the next ones.
+template <AttnKind KIND, bool TILES>
+__device__ __forceinline__ bool attn_find_here(const AttnArgs& a, const AttnLane<KIND>& x, int base, int64_t u, int lane,
+                                               int64_t& before, int64_t& units_before, AttnPlace& at) {
+    const int64_t count = TILES ? x.tiles : x.units;
+    int64_t end = count, units_end = x.units;
+    if (a.d.B > 1) {
+        end = wave_scan64(count, lane);
+        if (TILES) units_end = wave_scan64(x.units, lane);
+    }
+    const int64_t first = before + end - count;
+    const uint64_t here = __ballot(u >= first && u < first + count);
+    if (here) {
+        const int src = __builtin_ctzll(here);
+        at.b = base + src;
+        at.first = read_lane64(first, src);
+        at.count = read_lane64(count, src);
+        at.first_unit = TILES ? units_before + read_lane64(units_end - x.units, src) : at.first;
+        at.s.n = __builtin_amdgcn_readlane(x.s.n, src);
+        at.s.row0 = read_lane64(x.s.row0, src);
+        at.s.prefix = __builtin_amdgcn_readlane(x.s.prefix, src);
+        at.s.keys = __builtin_amdgcn_readlane(x.s.keys, src);
+        return true;
+    }
+    before += read_lane64(end, 63);
+    if (TILES) units_before += read_lane64(units_end, 63);
+    return false;
+}
+template <AttnKind KIND, bool TILES>
+__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t u, int lane, AttnPlace& at) {
+    int64_t before = 0, units_before = 0;
+    for (int base = 0; base < a.d.B; base += 64) {
+        AttnLane<KIND> x;
+        x.read(a, base + lane);
+        if (attn_find_here<KIND, TILES>(a, x, base, u, lane, before, units_before, at)) return true;
+    }
+    return false;
+}
+
+// The plan; `x`: what the lanes have read of the first 64 sequences.
+template <AttnKind KIND>
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane, AttnLane<KIND>& x) {
+    x.read(a, lane);
+    int64_t units = x.units;
+    for (int b = lane + 64; b < a.d.B; b += 64) {
+        AttnLane<KIND> y;
+        y.read(a, b);
+        units += y.units;
     }
     AttnPlan p;
     p.units = read_lane64(a.d.B == 1 ? units : wave_sum64(units), 0);
@@ -147,43 +203,33 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane) {
     return p;
 }
 
-// The sequence that holds unit `u` of a key head (with TILES: that holds tile u
-// of all sequences), the first of its units (tiles) and, with TILES, units.
-struct AttnPlace {
-    int b = -1;
-    int64_t first = 0, count = 0, first_unit = 0;
+// The number of workgroup `wg` of the grid, range times team plus place in the
+// team; -1 if it has no range.  Workgroups go to the 8 XCDs in turn; teams stay
+// on one, and so do neighbouring ranges, which share keys.
+__device__ __forceinline__ int attn_range(const AttnArgs& a, const AttnPlan& plan, int wg) {
+    const int per_xcd = ((plan.ranges + 7) >> 3) * a.team, w = (wg & 7) * per_xcd + (wg >> 3);
+    return wg >> 3 < per_xcd && w < plan.ranges * a.team ? w : -1;
+}
+// A workgroup's range, and the place of its first unit.
+struct AttnRange {
+    int w, team, mate;  // its number, its team and its place there
+    int64_t u, end, units;
 };
-template <AttnKind KIND, bool TILES>
-__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t u, int lane, AttnPlace& at) {
+template <AttnKind KIND>
+__device__ __forceinline__ bool attn_begin(const AttnArgs& a, int wg, int lane, AttnRange& r, AttnPlace& at) {
+    AttnLane<KIND> x;
+    const AttnPlan plan = attn_plan<KIND>(a, lane, x);
+    r.w = attn_range(a, plan, wg);
+    if (r.w < 0) return false;
+    r.team = a.team == 1 ? r.w : __builtin_amdgcn_readfirstlane(r.w / a.team);
+    r.mate = r.w - r.team * a.team;
+    r.units = plan.units;
+    r.u = r.team * plan.per;
+    r.end = min(r.u + plan.per, plan.units * (a.cache.H_kv * a.head_tiles));
+    const int64_t uh = r.u - quotient(r.u, plan.units) * plan.units;
     int64_t before = 0, units_before = 0;
-    for (int base = 0; base < a.d.B; base += 64) {
-        const int b = base + lane;
-        int64_t count = 0, units = 0;
-        if (b < a.d.B) {
-            const AttnSeq s = attn_seq<KIND>(a, b);
-            const int tiles = attn_tiles<KIND>(a, s);
-            units = attn_seq_units<KIND>(a, s, tiles);
-            count = TILES ? tiles : units;
-        }
-        int64_t end = count, units_end = units;
-        if (a.d.B > 1) {
-            end = wave_scan64(count, lane);
-            if (TILES) units_end = wave_scan64(units, lane);
-        }
-        const int64_t first = before + end - count;
-        const uint64_t here = __ballot(u >= first && u < first + count);
-        if (here) {
-            const int src = __builtin_ctzll(here);
-            at.b = base + src;
-            at.first = read_lane64(first, src);
-            at.count = read_lane64(count, src);
-            at.first_unit = TILES ? units_before + read_lane64(units_end - units, src) : at.first;
-            return true;
-        }
-        before += read_lane64(end, 63);
-        if (TILES) units_before += read_lane64(units_end, 63);
-    }
-    return false;
+    if (!attn_find_here<KIND, false>(a, x, 0, uh, lane, before, units_before, at)) attn_find<KIND, false>(a, uh, lane, at);
+    return true;
 }
 
 // A tile, and some of its units.
@@ -237,17 +283,10 @@ __device__ __forceinline__ int64_t attn_tile_unit(const AttnArgs& a, const AttnS
 }
 
 // Part `part` of the workspace: a tile's unnormalised outputs over some of its
-// keys, then the running maximum (in powers of two) and sum of every row.
+// keys (in the order that suits the kernel that writes them), then the running
+// maximum (in powers of two) and sum of every row.
 __device__ __forceinline__ float* part_out(const AttnArgs& a, int64_t part, int rows, int D) {
     return static_cast<float*>(a.ws) + part * rows * (D + 2);
-}
-
-// The number of workgroup `wg` of the grid, range times team plus place in the
-// team; -1 if it has no range.  Workgroups go to the 8 XCDs in turn; teams stay
-// on one, and so do neighbouring ranges, which share keys.
-__device__ __forceinline__ int attn_range(const AttnArgs& a, const AttnPlan& plan, int wg) {
-    const int per_xcd = ((plan.ranges + 7) >> 3) * a.team, w = (wg & 7) * per_xcd + (wg >> 3);
-    return wg >> 3 < per_xcd && w < plan.ranges * a.team ? w : -1;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

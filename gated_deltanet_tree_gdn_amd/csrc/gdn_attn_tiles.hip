@@ -319,39 +319,29 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
     extern __shared__ uint4 lds_raw[];
     const uint32_t lds_k = __builtin_amdgcn_readfirstlane(lds_address(lds_raw)), lds_v = lds_k + TileLds<D>::kV;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const AttnPlan plan = attn_plan<KIND>(a, threadIdx.x & 63);
-    const int w = attn_range(a, plan, blockIdx.x);
-    if (w < 0) return;
-    const int team = __builtin_amdgcn_readfirstlane(w / a.team), mate = w - team * a.team;
-    const int64_t u0 = team * plan.per, u_end = min(u0 + plan.per, plan.units * a.cache.H_kv);
     const float inf = __builtin_inff();
 
+    AttnRange range;
     AttnPlace at;
-    for (int64_t u = u0; u < u_end;) {
+    if (!attn_begin<KIND>(a, blockIdx.x, threadIdx.x & 63, range, at)) return;
+    for (int64_t u = range.u; u < range.end;) {
         const int tid = fresh(threadIdx.x), lane = tid & 63, col = lane & 31, half = lane >> 5;
-        const int h = int(quotient(u, plan.units));
-        const int64_t uh = u - h * plan.units;
-        if (at.b < 0 || uh < at.first || uh >= at.first + at.count) attn_find<KIND, false>(a, uh, lane, at);
-        const AttnSeq s = attn_seq_uniform<KIND>(a, at.b);
-        const AttnPiece it = attn_piece<KIND>(a, s, attn_tiles<KIND>(a, s), uh - at.first, u_end - u);
-        const bool first = u == u0;
+        const int h = int(quotient(u, range.units));
+        const int64_t uh = u - h * range.units;
+        if (uh < at.first || uh >= at.first + at.count) attn_find<KIND, false>(a, uh, lane, at);
+        const AttnSeq s = at.s;
+        const AttnPiece it = attn_piece<KIND>(a, s, attn_tiles<KIND>(a, s), uh - at.first, range.end - u);
+        const bool first = u == range.u;
         u += it.units;
         if (it.all == 0) continue;
         const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
         const int all_rows = s.n * a.group;
-        const int row0 = (KIND == kAttnVerify ? mate : it.tile) * kRows, rows = min(kRows, all_rows - row0);
+        const int row0 = (KIND == kAttnVerify ? range.mate : it.tile) * kRows, rows = min(kRows, all_rows - row0);
         const int begin = it.unit * kKeys;
         const int end = __builtin_amdgcn_readfirstlane(min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile)));
         const int32_t* table = a.table + at.b * a.d.table_stride;
         // tokens from here on are masked for some of the tile's rows
         const int open_end = KIND == kAttnPrefill ? __builtin_amdgcn_readfirstlane(s.prefix + row0 / a.group + 1) : s.prefix;
-
-        bool missing = false;  // pages outside the pool
-        for (int p = (begin >> a.page_shift) + tid; begin < end && p <= (end - 1) >> a.page_shift; p += kThreads) {
-            const int page = table[p];
-            missing |= page < 0 || page >= a.cache.n_pages;
-        }
-        missing = __builtin_amdgcn_readfirstlane(__syncthreads_or(missing));
 
         int token[RB], head[RB];
         bf16x8 q[RB][D / 16];
@@ -440,8 +430,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             } else {
                 load.k.scattered(a, load.window, lds_k, begin, end, wave, lane);
             }
+            bool missing = false;  // pages outside the pool
+            for (int p = (begin >> a.page_shift) + tid; p <= (end - 1) >> a.page_shift; p += kThreads) {
+                const int page = table[p];
+                missing |= page < 0 || page >= a.cache.n_pages;
+            }
             load.k.store(lds_k, wave, lane);
-            loads_barrier<0>();
+            wait_count<0>();
+            missing = __builtin_amdgcn_readfirstlane(__syncthreads_or(missing));
             // K of the tile behind the last is not used: it repeats what there is
             load.begin(a, table, lds_k + KL::kTile, lds_v, begin, end, wave, lane);
             rest();
@@ -684,13 +680,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
             const int r = (wave * RB + b) * 32 + col;
             if (r >= rows) continue;
             if (it.units < it.all) {
-                float* part = part_out(a, 2 * int64_t(w) + (first ? 0 : 1), kRows, D);
+                // 4 elements of each lane at a time, as they lie in the registers
+                float* part = part_out(a, 2 * int64_t(range.w) + (first ? 0 : 1), kRows, D);
+                f32x4* out = reinterpret_cast<f32x4*>(part) + (wave * RB + b) * (D / 4 * 32) + lane;
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<f32x4*>(part + r * D + 32 * n + 8 * i + 4 * half) =
-                            f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]};
+                        out[(4 * n + i) * 64] = f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]};
                 if (half == 0) {
                     part[kRows * D + r] = m[b];
                     part[kRows * (D + 1) + r] = l[b];
@@ -704,7 +701,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnA
                                       f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]}, l[b]);
             }
         }
-        if (u < u_end) __syncthreads();  // the next piece overwrites LDS
+        if (u < range.end) __syncthreads();  // the next piece overwrites LDS
     }
 }
 
