@@ -13,8 +13,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kWaves = 4, kStep = 32;  // wavefronts of a workgroup, keys of a wavefront's step
-constexpr int kUnit = kWaves * kStep;  // keys of a unit of work
+constexpr int kWaves = 4, kStep = 32;  // wavefronts of a workgroup, keys that one takes at a time
+constexpr int kUnit = kDecodeUnit;
 
 // Position of the 16-byte piece p of row r of a wavefront's V tile: a
 // transposing read takes 32 bytes each of 8 rows at a time, which this spreads
@@ -26,38 +26,42 @@ __device__ __forceinline__ int v_piece(int r, int p) {
 
 // ---------------------------------------------------------------------------
 // A piece of a workgroup's range: some of one sequence's keys, one key head, up
-// to 16 of its query heads.  Each wavefront takes every fourth step of 32 keys with a
-// running maximum and sum of its own; the four are joined at the end.
+// to 16 of its query heads.  Each wavefront takes a quarter of the keys, 32 at a
+// time, with a running maximum and sum of its own; the four are joined at the end.
 //   S^T = K Q^T   keys x heads on MFMA: K from memory straight as operand
 //   O^T += V^T P  V through the wavefront's LDS rows, read transposed; the
 //                 lanes hold P where the product wants it, since the k-slots
 //                 of both operands may carry keys in any order
 // P goes in as two bf16 (16 bits together), so that only the result is
-// rounded to bf16.
+// rounded to bf16.  What bounds it is memory: a step's loads are under way while
+// the step before is worked on, 64 KB or more of each CU.
 // ---------------------------------------------------------------------------
 template <int D, bool F8>
 struct Step {
+    static constexpr int T = kStep / 16;             // tiles of 16 keys
     static constexpr int E = F8 ? 16 : 8;            // elements of a 16-byte piece
     static constexpr int KL = D / (4 * E);           // loads of a K row's quarter
     static constexpr int VL = kStep * D / E / 64;    // loads of the V tile per lane
     static constexpr int VP = D / E;                 // pieces of a V row
-    uint4 k[2][KL], v[VL];
+    uint4 k[T][KL], v[VL];
     uint32_t ok;  // keys that are there
 
-    __device__ __forceinline__ void load(const AttnArgs& a, const char* kp, const char* vp, const int32_t* table, int t0,
-                                         int end, int lane) {
+    static constexpr uint32_t kAll = ~uint32_t(0);
+
+    __device__ __forceinline__ void load(const AttnArgs& a, PageWindow& window, const char* kp, const char* vp,
+                                         const int32_t* table, int t0, int end, int lane) {
         constexpr int size = F8 ? 1 : 2;
-        const int t = t0 + (lane & 31);
-        int page = -1;
-        if (t < end) page = table[t >> a.page_shift];
-        const bool there = page >= 0 && page < a.cache.n_pages;
+        const int t = t0 + (lane & (kStep - 1));
+        window.cover(table, t0 >> a.page_shift, (min(t0 + kStep, end) - 1) >> a.page_shift, lane);
+        const int page = __shfl(window.ids, (min(t, end - 1) >> a.page_shift) - window.first);
+        const bool there = t < end && page >= 0 && page < a.cache.n_pages;
         ok = uint32_t(__ballot(there));
         const int row = t & (a.cache.page_size - 1);
         // absent keys read the pool's first row
         const int64_t ko = there ? (page * a.cache.k_page_stride + row * a.cache.k_row_stride) * size : 0;
         const int64_t vo = there ? (page * a.cache.v_page_stride + row * a.cache.v_row_stride) * size : 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < T; ++j) {
             const char* p = kp + __shfl(ko, 16 * j + (lane & 15)) + (lane >> 4) * 16;
 #pragma unroll
             for (int i = 0; i < KL; ++i) k[j][i] = *reinterpret_cast<const uint4*>(p + i * 64);
@@ -75,7 +79,7 @@ struct Step {
         for (int i = 0; i < VL; ++i) {
             const int r = (64 * i + lane) / VP, p = lane % VP;
             uint4 x = v[i];
-            if (ok != 0xffffffffu && !(ok >> r & 1)) x = make_uint4(0, 0, 0, 0);
+            if (ok != kAll && !(ok >> r & 1)) x = make_uint4(0, 0, 0, 0);
             if constexpr (F8) {
                 uint4 lo, hi;
                 e4m3_to_bf16(x, lo, hi);
@@ -95,7 +99,8 @@ __device__ __forceinline__ int k_column(int n, int g) {
 }
 
 template <int D, bool F8>
-__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWaves * 64, decode_per_cu(D, F8)) void decode_kernel(AttnArgs a) {
+    constexpr int T = kStep / 16;
     __shared__ uint4 vlds[kWaves][kStep * D / 8];  // V by wavefront, then the wavefronts' O in fp32
     __shared__ float ml[kWaves][2][kDecodeRows];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -129,15 +134,20 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
         for (int n = 0; n < D / 16; ++n) o[n] = f32x4{0, 0, 0, 0};
         float m = -inf, l = 0.0f;
 
+        // the piece's steps in four runs of neighbours, so that a wavefront's pages are neighbours too
+        const int steps = (end - begin + kStep - 1) / kStep, run = (steps + kWaves - 1) / kWaves;
+        int t0 = begin + wave * run * kStep;
+        const int stop = __builtin_amdgcn_readfirstlane(min(t0 + run * kStep, end));
         Step<D, F8> cur;
-        int t0 = begin + wave * kStep;
-        if (t0 < end) cur.load(a, kp, vp, table, t0, end, lane);
-        for (; t0 < end; t0 += kWaves * kStep) {
+        PageWindow window;
+        window.open(end, a.page_shift);
+        if (t0 < stop) cur.load(a, window, kp, vp, table, t0, stop, lane);
+        for (; t0 < stop; t0 += kStep) {
             cur.store_v(vlds[wave], lane);
             const uint32_t ok = cur.ok;
-            f32x4 sc[2];
+            f32x4 sc[T];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < T; ++j) {
                 sc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < Step<D, F8>::KL; ++i) {
@@ -151,14 +161,13 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
                     }
                 }
             }
-            const int next = t0 + kWaves * kStep;
-            if (next < end) cur.load(a, kp, vp, table, next, end, lane);
+            if (t0 + kStep < stop) cur.load(a, window, kp, vp, table, t0 + kStep, stop, lane);
 
-            float x[8], top = -inf;
+            float x[4 * T], top = -inf;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4 * T; ++j) {
                 x[j] = sc[j >> 2][j & 3] * scale;
-                if (ok != 0xffffffffu && !(ok >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1)) x[j] = -inf;
+                if (ok != Step<D, F8>::kAll && !(ok >> (16 * (j >> 2) + 4 * g + (j & 3)) & 1)) x[j] = -inf;
                 top = fmaxf(top, x[j]);
             }
             top = fmaxf(top, __shfl_xor(top, 16));
@@ -168,24 +177,23 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void decode_kernel(A
             m = m_new;
             l *= keep;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4 * T; ++j) {
                 x[j] = exp2_fast(x[j] - base);
                 l += x[j];
             }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) o[n] *= keep;
             bf16x8 hi, lo;
             split8(x, hi, lo);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
                 const int r = 4 * g + (col >> 2), p = 2 * n + ((col >> 1) & 1);
                 const char* at0 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r, p)) + 8 * (col & 1);
                 const char* at1 = reinterpret_cast<const char*>(vlds[wave] + v_piece<D>(r + 16, p)) + 8 * (col & 1);
-                const uint2 u = read_tr16(lds_address(at0)), w = read_tr16(lds_address(at1));
-                const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, w.x, w.y));
-                f32x4 acc = o[n];
-                acc *= keep;
-                acc = mfma(vt, hi, acc);
-                o[n] = mfma(vt, lo, acc);
+                const uint2 y0 = read_tr16(lds_address(at0)), y1 = read_tr16(lds_address(at1));
+                const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(y0.x, y0.y, y1.x, y1.y));
+                o[n] = mfma(vt, lo, mfma(vt, hi, o[n]));
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }

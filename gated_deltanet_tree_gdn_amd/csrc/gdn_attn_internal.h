@@ -62,14 +62,17 @@ struct AttnArgs {
     int head_tiles;  // decode: tiles of 16 heads that the group is cut into, else 1
     int team;        // workgroups side by side: the tiles of a tree, otherwise 1
     int teams;       // that the units are divided over
-    int unit;        // keys of a unit
+    int unit_shift;  // keys of a unit, as a power of two
     int min_units;   // of a workgroup
     bool join;       // tiles may be divided
 };
-// Rows of a tile: single tokens; otherwise 4 wavefronts of 64 rows, of 32 where
-// the accumulators of more do not fit the registers.
-constexpr int kDecodeRows = 16;
-constexpr int tile_rows(int d) { return d == 256 ? 128 : 128; }
+constexpr int kDecodeRows = 16, kTileRows = 128;  // rows of a tile
+// Workgroups of 4 wavefronts that a CU's registers have room for: what a
+// wavefront of the single-token kernel holds goes by the bytes of a key, and the
+// fewer those are, the more wavefronts it takes to hide a step's latencies.
+constexpr int decode_per_cu(int d, bool e4m3) { return d == 256 ? 1 : d == 128 ? 2 : e4m3 ? 4 : 3; }
+constexpr int tiles_per_cu(int d) { return d == 256 ? 1 : 2; }
+constexpr int kDecodeUnit = 128, kTilesUnit = 64;  // keys of a unit
 
 // Fills the derived members.
 void attn_shape(AttnArgs& a);

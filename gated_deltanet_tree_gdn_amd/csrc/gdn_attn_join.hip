@@ -34,11 +34,11 @@ struct Joined {
 // kJoinPieces pieces of 4 elements, in the order in which the parts hold them.
 template <AttnKind KIND, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
-    constexpr int C = D / 4, K = kThreads / C;  // threads of a row, shares of the parts
+    constexpr int C = D / 4, K = kThreads / C;  // threads of a row, shares of the parts (single tokens)
     constexpr bool one = KIND == kAttnDecode;
-    constexpr int kTileRows = tile_rows(D), rows_of_part = one ? kDecodeRows : kTileRows;
+    constexpr int rows_of_part = one ? kDecodeRows : kTileRows;
     __shared__ f32x4 share[one ? K : 1][C];
-    __shared__ float share_m[one ? K : 1], share_l[one ? K : 1];
+    __shared__ float share_m[4], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int heads = a.cache.H_kv * a.head_tiles;
     // workgroups of a tile (or team)
@@ -66,24 +66,35 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
         };
         if (parts > 1) {
             if constexpr (one) {
-                const int p = tid % C, k = tid / C;
+                // maxima first, so that the parts' outputs are loads that wait for nothing but their weights
                 const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
                 if (row < a.group - head0) {
-                    Joined y;
+                    float top = -__builtin_inff();
+                    for (int i = tid; i < parts; i += kThreads) top = fmaxf(top, part(i)[kDecodeRows * D + row]);
+#pragma unroll
+                    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+                    if (lane == 0) share_m[tid >> 6] = top;
+                    __syncthreads();
+                    top = finite_max(fmaxf(fmaxf(share_m[0], share_m[1]), fmaxf(share_m[2], share_m[3])));
+                    const int p = tid % C, k = tid / C;
+                    f32x4 acc{0, 0, 0, 0};
+                    float sum = 0.0f;
+#pragma unroll 4
                     for (int i = k; i < parts; i += K) {
                         const float* z = part(i);
-                        y.add(*reinterpret_cast<const f32x4*>(z + row * D + 4 * p), z[kDecodeRows * D + row],
-                              z[kDecodeRows * (D + 1) + row]);
+                        const float f = exp2_fast(z[kDecodeRows * D + row] - top);
+                        acc += *reinterpret_cast<const f32x4*>(z + row * D + 4 * p) * f;
+                        sum += z[kDecodeRows * (D + 1) + row] * f;
                     }
-                    share[k][p] = y.acc;
-                    if (p == 0) {
-                        share_m[k] = y.m;
-                        share_l[k] = y.l;
-                    }
+                    share[k][p] = acc;
+                    if (p == 0) share_l[k] = sum;
                     __syncthreads();
                     if (k == 0) {
-                        for (int i = 1; i < K; ++i) y.add(share[i][p], share_m[i], share_l[i]);
-                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, y.acc, y.l);
+                        for (int i = 1; i < K; ++i) {
+                            acc += share[i][p];
+                            sum += share_l[i];
+                        }
+                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, acc, sum);
                     }
                 }
             } else {
@@ -155,20 +166,22 @@ void attn_shape(AttnArgs& a) {
     a.page_shift = __builtin_ctz(a.cache.page_size);
     a.group = a.d.H_q / a.cache.H_kv;
     const bool one = a.kind == kAttnDecode;
-    a.tile_rows = one ? kDecodeRows : tile_rows(a.cache.d);
+    a.tile_rows = one ? kDecodeRows : kTileRows;
     a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
-    a.unit = one ? 128 : 64;
+    const int unit = one ? kDecodeUnit : kTilesUnit;
+    a.unit_shift = __builtin_ctz(unit);
     a.min_units = one ? 1 : 4;
     const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
     // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
     // overlap, where cu_seqlens decreases, and each may then have all rows)
     const int64_t tiles = (rows + a.tile_rows - 1) / a.tile_rows;
     const int64_t units = (a.kind == kAttnPrefill ? tiles : 1) * a.d.B * a.cache.H_kv * a.head_tiles *
-                          ((cap + a.unit - 1) / a.unit + 2);
+                          ((cap + unit - 1) / unit + 2);
     a.team = a.kind == kAttnVerify ? int(tiles) : 1;
     a.teams = int(std::max<int64_t>(
-        1, std::min<int64_t>((a.cache.d < 256 ? 2 * kCu : kCu) / a.team, (units + a.min_units - 1) / a.min_units)));
-    a.join = a.teams > 1 && cap > a.unit;  // otherwise a tile is one unit
+        1, std::min<int64_t>(kCu * (one ? decode_per_cu(a.cache.d, a.cache.dtype == GDN_E4M3) : tiles_per_cu(a.cache.d)) / a.team,
+                             (units + a.min_units - 1) / a.min_units)));
+    a.join = a.teams > 1 && cap > unit;  // otherwise a tile is one unit
 }
 
 size_t attn_ws_bytes(const AttnArgs& a) {

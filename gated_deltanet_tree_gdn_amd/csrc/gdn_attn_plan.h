@@ -1,10 +1,10 @@
 // gdn_attn_plan.h -- which keys of which queries a workgroup of the attention
 // kernels takes, and where it leaves its part of a result.
 //
-// The work is numbered in units of `unit` keys of one tile of rows: through the
+// The work is numbered in units of some keys of one tile of rows: through the
 // tiles of a sequence, the sequences, then the key heads.  Workgroup w takes
-// units w per .. (w + 1) per - 1, with per = max(min_units, all / slots), so the
-// workgroups that fit the GPU at once (`slots`) have the same work however
+// units w per .. (w + 1) per - 1, with per = max(min_units, all / teams), so the
+// workgroups that fit the GPU at once (`teams`) have the same work however
 // uneven the lengths are, and nothing has to be known on the host.  A range
 // covers any number of whole tiles, whose results are final, and at most two
 // tiles in part (one where it starts, one where it ends), whose results go to
@@ -75,7 +75,7 @@ __device__ __forceinline__ int attn_seen(const AttnArgs& a, const AttnSeq& s, in
 // A tile's units: at least one, so that rows which see nothing are written.
 template <AttnKind KIND>
 __device__ __forceinline__ int attn_units(const AttnArgs& a, const AttnSeq& s, int tile) {
-    return max((attn_seen<KIND>(a, s, tile) + a.unit - 1) / a.unit, 1);
+    return max((attn_seen<KIND>(a, s, tile) + (1 << a.unit_shift) - 1) >> a.unit_shift, 1);
 }
 // The units that a pair of tiles counts (prefill: at least those of any pair,
 // whose keys sum to 2 prefix + tile_rows (tiles + 1) / group + 2 at most), and
@@ -84,7 +84,7 @@ template <AttnKind KIND>
 __device__ __forceinline__ int attn_pair(const AttnArgs& a, const AttnSeq& s, int tiles) {
     if constexpr (KIND != kAttnPrefill) return attn_units<KIND>(a, s, 0);
     const int64_t keys = 2 * int64_t(max(s.prefix, 0)) + (int64_t(tiles) + 1) * a.tile_rows / a.group + 2;
-    return int(keys / a.unit) + 2;
+    return int(keys >> a.unit_shift) + 2;
 }
 template <AttnKind KIND>
 __device__ __forceinline__ int64_t attn_seq_units(const AttnArgs& a, const AttnSeq& s, int tiles) {
@@ -288,6 +288,21 @@ __device__ __forceinline__ int64_t attn_tile_unit(const AttnArgs& a, const AttnS
 __device__ __forceinline__ float* part_out(const AttnArgs& a, int64_t part, int rows, int D) {
     return static_cast<float*>(a.ws) + part * rows * (D + 2);
 }
+
+// Numbers of the pages from `first` on, one per lane, read from the table 64 at a time.
+struct PageWindow {
+    int first, ids, last;  // last: the last page that is read at all
+    __device__ __forceinline__ void open(int end, int shift) {
+        first = 0x7fffffff;
+        last = (end - 1) >> shift;
+    }
+    __device__ __forceinline__ void cover(const int32_t* table, int from, int to, int lane) {
+        if (from < first || to >= first + 64) {
+            first = from;
+            ids = table[min(first + lane, last)];
+        }
+    }
+};
 
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -14,7 +14,7 @@ namespace gdn {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kKeys = 64;  // keys of a tile in LDS
+constexpr int kKeys = kTilesUnit;  // keys of a tile in LDS
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -91,21 +91,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ __attribute__((address_space(3))) u32x4* lds_piece(uint32_t at) {
     return reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at);
 }
-
-// Numbers of the pages from `first` on, one per lane, read from the table 64 at a time.
-struct PageWindow {
-    int first, ids, last;  // last: the last page that is read at all
-    __device__ __forceinline__ void open(int end, int shift) {
-        first = 0x7fffffff;
-        last = (end - 1) >> shift;
-    }
-    __device__ __forceinline__ void cover(const int32_t* table, int from, int to, int lane) {
-        if (from < first || to >= first + 64) {
-            first = from;
-            ids = table[min(first + lane, last)];
-        }
-    }
-};
 
 // Rows of K or V on their way from memory to LDS.  Wavefront w brings rows
 // 16 w .. 16 w + 15 of a tile.  Rows behind the last token hold what lies there
@@ -312,8 +297,8 @@ __device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 // the vector unit can do meanwhile.
 // ---------------------------------------------------------------------------
 template <AttnKind KIND, int D, bool F8>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void tiles_kernel(AttnArgs a) {
-    constexpr int RB = tile_rows(D) / 128, kRows = 128 * RB;
+__global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnArgs a) {
+    constexpr int RB = 1, kRows = kTileRows * RB;
     using KL = Layout<D, false>;
     using VL = Layout<D, true>;
     extern __shared__ uint4 lds_raw[];

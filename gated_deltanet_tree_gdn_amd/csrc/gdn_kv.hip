@@ -28,6 +28,30 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8]) {
     return make_uint2(a, b);
 }
 
+// 8 elements of any alignment as they lie in memory.
+struct Raw {
+    typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+    u32x4 a, b;
+    __device__ __forceinline__ void load(const void* p, int dtype, int64_t i) {
+        const char* at = static_cast<const char*>(p) + i * (dtype == GDN_BF16 ? 2 : 4);
+        a = *reinterpret_cast<const u32x4u*>(at);
+        if (dtype != GDN_BF16) b = *reinterpret_cast<const u32x4u*>(at + 16);
+    }
+    __device__ __forceinline__ void unpack(int dtype, float (&x)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t u = a[j], v = b[j];
+            if (dtype == GDN_BF16) {
+                x[2 * j] = bf16_lo(u);
+                x[2 * j + 1] = bf16_hi(u);
+            } else {
+                x[j] = __builtin_bit_cast(float, u);
+                x[4 + j] = __builtin_bit_cast(float, v);
+            }
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // gdn_kv_append.  A head's d elements lie 8 to a lane in d / 8 adjacent lanes,
 // so its norm is a sum over lanes, and a pair of neighbours turns within a
@@ -35,24 +59,37 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8]) {
 // and sines of a token are formed once by the first rot / 2 threads of each
 // workgroup: the angle position * inv_freq is exact to 2^-53 in fp64, reduced
 // there to a fraction of a turn, and from then on fp32 is enough for outputs
-// of 8 bits.  A workgroup takes `passes` times 256 / (d / 8) heads of one token.
+// of 8 bits.  A workgroup takes `passes` times 256 / (d / 8) heads of one token;
+// the elements of a pass are on their way while the one before (the first:
+// while the angles) is worked on.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int passes, int groups) {
+__global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int passes, int groups, int page_shift) {
     constexpr int L = D / 8, PER = kThreads / L;  // lanes of a head, heads of a pass
     __shared__ float cs[128], sn[128];
     __shared__ alignas(16) float rows[kThreads * 8];
     const int tid = threadIdx.x;
     const int64_t wg = block_id();
-    const int64_t t = wg / groups;
+    const int64_t t = groups == 1 ? wg : wg / groups;
     if (t >= a.d.T) return;
-    const int group = int(wg % groups);
+    const int group = int(wg - t * groups);
     const int H_q = a.d.H_q, H_kv = a.cache.H_kv, heads = H_q + 2 * H_kv;
     const int half = a.d.rot >> 1;
-    const int32_t slot = a.slot[t];
-    const int32_t n_slots = a.cache.n_pages * a.cache.page_size;
-    const bool stored = slot >= 0 && slot < n_slots;
+    const int e = 8 * (tid % L);
 
+    Raw next;
+    auto fetch = [&](int p) {
+        const int head = (group * passes + p) * PER + tid / L;
+        if (head >= heads) return;
+        const bool is_q = head < H_q, is_v = head >= H_q + H_kv;
+        const int h = is_q ? head : is_v ? head - H_q - H_kv : head - H_q;
+        const void* src = is_q ? a.q : is_v ? a.v : a.k;
+        const int64_t ts = is_q ? a.d.q_stride : is_v ? a.d.v_stride : a.d.k_stride;
+        const int64_t hs = is_q ? a.d.q_head_stride : is_v ? a.d.v_head_stride : a.d.k_head_stride;
+        next.load(src, a.d.in_dtype, t * ts + h * hs + e);
+    };
+    fetch(0);
+    const int32_t slot = a.slot[t];
     if (tid < half) {
         double turn = double(a.position[t]) * double(a.inv_freq[tid]) * 0.15915494309189533577;
         turn -= rint(turn);
@@ -61,25 +98,19 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int pa
         cs[tid] = c;
         sn[tid] = s;
     }
-    __syncthreads();
+    const bool stored = slot >= 0 && slot < a.cache.n_pages << page_shift;
+    const int page = slot >> page_shift, page_row = slot & (a.cache.page_size - 1);
+    if (half > 0) __syncthreads();
 
-    const int e = 8 * (tid % L);
     float* mine = rows + (tid / L) * D;
     for (int p = 0; p < passes; ++p) {
         const int head = (group * passes + p) * PER + tid / L;
         const bool live = head < heads;
         const bool is_q = head < H_q, is_v = head >= H_q + H_kv;
         const int h = is_q ? head : is_v ? head - H_q - H_kv : head - H_q;
-        float x[8];
-        if (live) {
-            const void* src = is_q ? a.q : is_v ? a.v : a.k;
-            const int64_t ts = is_q ? a.d.q_stride : is_v ? a.d.v_stride : a.d.k_stride;
-            const int64_t hs = is_q ? a.d.q_head_stride : is_v ? a.d.v_head_stride : a.d.k_head_stride;
-            load8(src, a.d.in_dtype, t * ts + h * hs + e, x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-        }
+        float x[8] = {};
+        if (live) next.unpack(a.d.in_dtype, x);
+        if (p + 1 < passes) fetch(p + 1);
         const float* w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
         float sum = 0.0f;
 #pragma unroll
@@ -127,15 +158,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int pa
         if (is_q) {
             store8(a.q_out, GDN_BF16, (t * H_q + h) * int64_t(D) + e, x);
         } else if (stored) {
-            const int page = slot / a.cache.page_size, row = slot % a.cache.page_size;
             const float* scale = is_v ? a.cache.v_scale : a.cache.k_scale;
             if (scale) {
                 const float s = scale[h];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] /= s;
             }
-            const int64_t at = is_v ? page * a.cache.v_page_stride + row * a.cache.v_row_stride + h * a.cache.v_head_stride
-                                    : page * a.cache.k_page_stride + row * a.cache.k_row_stride + h * a.cache.k_head_stride;
+            const int64_t at =
+                is_v ? page * a.cache.v_page_stride + page_row * a.cache.v_row_stride + h * a.cache.v_head_stride
+                     : page * a.cache.k_page_stride + page_row * a.cache.k_row_stride + h * a.cache.k_head_stride;
             char* pool = static_cast<char*>(is_v ? a.cache.v : a.cache.k);
             if (a.cache.dtype == GDN_BF16)
                 store8(pool, GDN_BF16, at + e, x);
@@ -240,11 +271,12 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream) {
     // few tokens: a workgroup for every pass; many: the angles once per token
     const int passes = a.d.T < 1024 ? 1 : all;
     const int groups = (all + passes - 1) / passes;
+    const int shift = __builtin_ctz(a.cache.page_size);
     const dim3 grid = grid_of(int64_t(a.d.T) * groups);
     switch (a.cache.d) {
-        case 64: append_kernel<64><<<grid, kThreads, 0, stream>>>(a, passes, groups); break;
-        case 128: append_kernel<128><<<grid, kThreads, 0, stream>>>(a, passes, groups); break;
-        default: append_kernel<256><<<grid, kThreads, 0, stream>>>(a, passes, groups); break;
+        case 64: append_kernel<64><<<grid, kThreads, 0, stream>>>(a, passes, groups, shift); break;
+        case 128: append_kernel<128><<<grid, kThreads, 0, stream>>>(a, passes, groups, shift); break;
+        default: append_kernel<256><<<grid, kThreads, 0, stream>>>(a, passes, groups, shift); break;
     }
     return hipGetLastError();
 }
