@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_per_cu(D, F8)) void decode_kern
     for (int64_t u = range.u; u < range.end;) {
         const int hh = int(quotient(u, range.units)), h = hh / a.head_tiles, head0 = (hh - h * a.head_tiles) * kDecodeRows;
         const int64_t uh = u - hh * range.units;
-        if (uh < at.first || uh >= at.first + at.count) attn_find<kAttnDecode, false>(a, uh, lane, at);
+        attn_next<kAttnDecode>(a, uh, lane, at);
         const AttnSeq& s = at.s;
         const AttnPiece it = attn_piece<kAttnDecode>(a, s, 1, uh - at.first, range.end - u);
         const int rows = min(a.group - head0, kDecodeRows);

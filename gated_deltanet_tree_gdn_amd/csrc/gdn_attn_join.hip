@@ -16,6 +16,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kJoinPieces = 2;  // of 4 elements, of a thread that joins tiles
 
+// Workgroups that join a tile (or team).
+__host__ __device__ inline int join_blocks(const AttnArgs& a) {
+    const int rows = a.group < kDecodeRows ? a.group : kDecodeRows;
+    return a.kind == kAttnDecode ? rows : kTileRows * (a.cache.d / 4) / (kThreads * kJoinPieces) * a.team;
+}
+
 struct Joined {
     f32x4 acc{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0.0f;
@@ -28,12 +34,15 @@ struct Joined {
     }
 };
 
-// Parts of a tile's rows, joined in the order of the keys.  Single tokens: a
-// workgroup for every row, since there are few and their parts may be hundreds;
-// the workgroup's threads take the parts in turn.  Tiles: every thread has
-// kJoinPieces pieces of 4 elements, in the order in which the parts hold them.
-template <AttnKind KIND, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
+// Parts of a tile's rows, joined in the order of the keys.  Where BY_TILE, there
+// are workgroups for every tile (which is all of a sequence, as a prompt's are
+// not), otherwise for every end of a range within a tile, of which the first
+// joins it: whichever are fewer, since each of them has to find its place.  Single tokens: a workgroup for every row, since
+// there are few and their parts may be hundreds; the workgroup's threads take
+// the parts in turn.  Tiles: every thread has kJoinPieces pieces of 4 elements,
+// in the order in which the parts hold them.
+template <AttnKind KIND, int D, bool BY_TILE>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int64_t workgroups) {
     constexpr int C = D / 4, K = kThreads / C;  // threads of a row, shares of the parts (single tokens)
     constexpr bool one = KIND == kAttnDecode;
     constexpr int rows_of_part = one ? kDecodeRows : kTileRows;
@@ -41,81 +50,89 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     __shared__ float share_m[4], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int heads = a.cache.H_kv * a.head_tiles;
-    // workgroups of a tile (or team)
-    const int blocks = (one ? min(a.group, kDecodeRows) : kTileRows * C / (kThreads * kJoinPieces)) * a.team;
-    const int64_t wg = block_id(), grid_tiles = int64_t(gridDim.x) * gridDim.y / heads / blocks;
-    if (wg >= grid_tiles * heads * blocks) return;
-    const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team, hh = int(wg / blocks % heads);
-    const int h = hh / a.head_tiles;
+    const int blocks = join_blocks(a);
+    const int64_t wg = block_id();
+    if (wg >= workgroups) return;
+    const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team;
     AttnLane<KIND> x;
     const AttnPlan plan = attn_plan<KIND>(a, lane, x);
     AttnPlace at;
-    for (int64_t tile = wg / blocks / heads;; tile += grid_tiles) {
-        int64_t before = 0, units_before = 0;
-        if (!attn_find_here<KIND, true>(a, x, 0, tile, lane, before, units_before, at) &&
-            (a.d.B <= 64 || !attn_find<KIND, true>(a, tile, lane, at)))
-            return;
-        const AttnSeq s = at.s;
-        const int t = int(tile - at.first), tiles = int(at.count);
-        const int64_t g0 = hh * plan.units + at.first_unit + attn_tile_unit<KIND>(a, s, tiles, t);
-        const int64_t w0 = quotient(g0, plan.per), w1 = quotient(g0 + attn_units<KIND>(a, s, t) - 1, plan.per);
-        const int parts = int(w1 - w0) + 1;
-        // the first workgroup either starts with this tile or has it as its last
-        auto part = [&](int i) {
-            return part_out(a, 2 * ((w0 + i) * a.team + mate) + (i == 0 && g0 != w0 * plan.per), rows_of_part, D);
-        };
-        if (parts > 1) {
-            if constexpr (one) {
-                // maxima first, so that the parts' outputs are loads that wait for nothing but their weights
-                const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
-                if (row < a.group - head0) {
-                    float top = -__builtin_inff();
-                    for (int i = tid; i < parts; i += kThreads) top = fmaxf(top, part(i)[kDecodeRows * D + row]);
+    int hh, t = 0;
+    int64_t g0, before = 0;  // g0: the tile's first unit
+    if constexpr (BY_TILE) {
+        const int b = int(wg / blocks / heads);
+        hh = int(wg / blocks % heads);
+        if (!attn_find_here<KIND, true>(a, x, 0, b, lane, before, at)) attn_find<KIND, true>(a, 64, before, b, lane, at);
+        g0 = hh * plan.units + at.first;
+    } else {
+        const int64_t w = wg / blocks + 1;
+        if (w >= plan.ranges) return;
+        const int64_t g = w * plan.per;
+        hh = int(quotient(g, plan.units));
+        const int64_t uh = g - hh * plan.units;
+        if (!attn_find_here<KIND, false>(a, x, 0, uh, lane, before, at)) attn_find<KIND, false>(a, 64, before, uh, lane, at);
+        const AttnPiece it = attn_piece<KIND>(a, at.s, attn_tiles<KIND>(a, at.s), uh - at.first, 1);
+        if (it.all == 0 || it.unit == 0 || it.unit > plan.per) return;
+        t = it.tile;
+        g0 = g - it.unit;
+    }
+    const AttnSeq s = at.s;
+    const int h = hh / a.head_tiles;
+    const int64_t w0 = quotient(g0, plan.per), w1 = quotient(g0 + attn_units<KIND>(a, s, t) - 1, plan.per);
+    const int parts = int(w1 - w0) + 1;
+    if (parts == 1) return;
+    // the first workgroup either starts with this tile or has it as its last
+    auto part = [&](int i) {
+        return part_out(a, 2 * ((w0 + i) * a.team + mate) + (i == 0 && g0 != w0 * plan.per), rows_of_part, D);
+    };
+    if constexpr (one) {
+        // maxima first, so that the parts' outputs are loads that wait for nothing but their weights
+        const int head0 = (hh - h * a.head_tiles) * kDecodeRows, row = block;
+        if (row < a.group - head0) {
+            float top = -__builtin_inff();
+            for (int i = tid; i < parts; i += kThreads) top = fmaxf(top, part(i)[kDecodeRows * D + row]);
 #pragma unroll
-                    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-                    if (lane == 0) share_m[tid >> 6] = top;
-                    __syncthreads();
-                    top = finite_max(fmaxf(fmaxf(share_m[0], share_m[1]), fmaxf(share_m[2], share_m[3])));
-                    const int p = tid % C, k = tid / C;
-                    f32x4 acc{0, 0, 0, 0};
-                    float sum = 0.0f;
+            for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+            if (lane == 0) share_m[tid >> 6] = top;
+            __syncthreads();
+            top = finite_max(fmaxf(fmaxf(share_m[0], share_m[1]), fmaxf(share_m[2], share_m[3])));
+            const int p = tid % C, k = tid / C;
+            f32x4 acc{0, 0, 0, 0};
+            float sum = 0.0f;
 #pragma unroll 4
-                    for (int i = k; i < parts; i += K) {
-                        const float* z = part(i);
-                        const float f = exp2_fast(z[kDecodeRows * D + row] - top);
-                        acc += *reinterpret_cast<const f32x4*>(z + row * D + 4 * p) * f;
-                        sum += z[kDecodeRows * (D + 1) + row] * f;
-                    }
-                    share[k][p] = acc;
-                    if (p == 0) share_l[k] = sum;
-                    __syncthreads();
-                    if (k == 0) {
-                        for (int i = 1; i < K; ++i) {
-                            acc += share[i][p];
-                            sum += share_l[i];
-                        }
-                        attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, acc, sum);
-                    }
+            for (int i = k; i < parts; i += K) {
+                const float* z = part(i);
+                const float f = exp2_fast(z[kDecodeRows * D + row] - top);
+                acc += *reinterpret_cast<const f32x4*>(z + row * D + 4 * p) * f;
+                sum += z[kDecodeRows * (D + 1) + row] * f;
+            }
+            share[k][p] = acc;
+            if (p == 0) share_l[k] = sum;
+            __syncthreads();
+            if (k == 0) {
+                for (int i = 1; i < K; ++i) {
+                    acc += share[i][p];
+                    sum += share_l[i];
                 }
-            } else {
-                const int row0 = (KIND == kAttnVerify ? mate : t) * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
-#pragma unroll
-                for (int j = 0; j < kJoinPieces; ++j) {
-                    const int e = (block * kJoinPieces + j) * kThreads + tid;  // 32 rows have 32 C pieces
-                    const int r = e / (32 * C) * 32 + (e & 31), d = e / 64 % (C / 2) * 8 + (e >> 5 & 1) * 4;
-                    if (r >= rows) continue;
-                    Joined y;
-#pragma unroll 4
-                    for (int i = 0; i < parts; ++i) {
-                        const float* z = part(i);
-                        y.add(reinterpret_cast<const f32x4*>(z)[e], z[kTileRows * D + r], z[kTileRows * (D + 1) + r]);
-                    }
-                    const int token = (row0 + r) / a.group;
-                    attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, d, y.acc, y.l);
-                }
+                attn_store<D>(a, s.row0, h, int64_t(h) * a.group + head0 + row, 4 * p, acc, sum);
             }
         }
-        if constexpr (KIND != kAttnPrefill) return;  // the grid has workgroups for every tile
+    } else {
+        const int row0 = (KIND == kAttnVerify ? mate : t) * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
+#pragma unroll
+        for (int j = 0; j < kJoinPieces; ++j) {
+            const int e = (block * kJoinPieces + j) * kThreads + tid;  // 32 rows have 32 C pieces
+            const int r = e / (32 * C) * 32 + (e & 31), d = e / 64 % (C / 2) * 8 + (e >> 5 & 1) * 4;
+            if (r >= rows) continue;
+            Joined y;
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const float* z = part(i);
+                y.add(reinterpret_cast<const f32x4*>(z)[e], z[kTileRows * D + r], z[kTileRows * (D + 1) + r]);
+            }
+            const int token = (row0 + r) / a.group;
+            attn_store<D>(a, s.row0 + token, h, int64_t(h) * a.group + row0 + r - token * a.group, d, y.acc, y.l);
+        }
     }
 }
 
@@ -143,22 +160,24 @@ __global__ __launch_bounds__(kThreads) void status_kernel(AttnArgs a) {
     if (threadIdx.x == 0) a.seq_status[b] = bad ? GDN_ERR_SHAPE : 0;
 }
 
-template <AttnKind KIND>
-hipError_t launch_join(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
+template <AttnKind KIND, bool BY_TILE>
+hipError_t launch_join(const AttnArgs& a, int64_t workgroups, hipStream_t stream) {
+    const dim3 grid = grid_of(workgroups);
     switch (a.cache.d) {
-        case 64: join_kernel<KIND, 64><<<grid, kThreads, 0, stream>>>(a); break;
-        case 128: join_kernel<KIND, 128><<<grid, kThreads, 0, stream>>>(a); break;
-        default: join_kernel<KIND, 256><<<grid, kThreads, 0, stream>>>(a); break;
+        case 64: join_kernel<KIND, 64, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
+        case 128: join_kernel<KIND, 128, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
+        default: join_kernel<KIND, 256, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
     }
     return hipGetLastError();
 }
-
-int64_t max_tiles(const AttnArgs& a) {
-    const int64_t rows = int64_t(a.d.T) * a.group;
-    return a.kind == kAttnDecode   ? a.d.B
-           : a.kind == kAttnVerify ? a.d.B
-                                   : rows / a.tile_rows + a.d.B;
+template <AttnKind KIND>
+hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
+    const int64_t tiles = int64_t(a.d.B) * a.cache.H_kv * a.head_tiles, ends = a.teams - 1;
+    if constexpr (KIND != kAttnPrefill)  // how many tiles prompts have is not known here
+        if (tiles <= ends) return launch_join<KIND, true>(a, tiles * join_blocks(a), stream);
+    return launch_join<KIND, false>(a, ends * join_blocks(a), stream);
 }
+
 }  // namespace
 
 void attn_shape(AttnArgs& a) {
@@ -189,12 +208,9 @@ size_t attn_ws_bytes(const AttnArgs& a) {
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
-    const int64_t heads = int64_t(a.cache.H_kv) * a.head_tiles;
-    const int blocks = a.kind == kAttnDecode ? std::min(a.group, kDecodeRows) : a.tile_rows * (a.cache.d / 4) / (kThreads * kJoinPieces) * a.team;
-    const dim3 grid = grid_of(max_tiles(a) * heads * blocks);
-    return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, grid, stream)
-           : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, grid, stream)
-                                   : launch_join<kAttnPrefill>(a, grid, stream);
+    return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, stream)
+           : a.kind == kAttnVerify ? launch_join<kAttnVerify>(a, stream)
+                                   : launch_join<kAttnPrefill>(a, stream);
 }
 
 hipError_t launch_attn_status(const AttnArgs& a, hipStream_t stream) {

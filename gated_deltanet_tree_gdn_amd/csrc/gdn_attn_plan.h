@@ -121,49 +121,42 @@ struct AttnPlan {
     int64_t units, per;
     int ranges;
 };
-// A sequence that all lanes agree on, the first of its units (join: tiles, and
-// units) within the key head, and how many it has.
+// A sequence that all lanes agree on, its first unit within the key head, and
+// how many it has; and the first of the 64 sequences that it was found among,
+// with the units before them.
 struct AttnPlace {
-    int b = -1;
-    int64_t first = 0, count = 0, first_unit = 0;
+    int b = -1, base = 0;
+    int64_t first = 0, count = 0, before = 0;
     AttnSeq s;
 };
 // What a lane knows of 64 sequences in a row.
 template <AttnKind KIND>
 struct AttnLane {
     AttnSeq s{0, 0, 0, 0};
-    int tiles = 0;
     int64_t units = 0;
     __device__ __forceinline__ void read(const AttnArgs& a, int b) {
         s = AttnSeq{0, 0, 0, 0};
-        tiles = 0;
         units = 0;
         if (b < a.d.B) {
             s = attn_seq<KIND>(a, b);
-            tiles = attn_tiles<KIND>(a, s);
-            units = attn_seq_units<KIND>(a, s, tiles);
+            units = attn_seq_units<KIND>(a, s, attn_tiles<KIND>(a, s));
         }
     }
 };
-// The sequence among those from `base` on that holds unit `u` (with TILES: tile
-// u); otherwise the numbers before the next ones.
-template <AttnKind KIND, bool TILES>
+// The sequence among those from `base` on that holds unit `u` (BY_NUMBER: that
+// is sequence u); otherwise the units before the next ones.
+template <AttnKind KIND, bool BY_NUMBER>
 __device__ __forceinline__ bool attn_find_here(const AttnArgs& a, const AttnLane<KIND>& x, int base, int64_t u, int lane,
-                                               int64_t& before, int64_t& units_before, AttnPlace& at) {
-    const int64_t count = TILES ? x.tiles : x.units;
-    int64_t end = count, units_end = x.units;
-    if (a.d.B > 1) {
-        end = wave_scan64(count, lane);
-        if (TILES) units_end = wave_scan64(x.units, lane);
-    }
-    const int64_t first = before + end - count;
-    const uint64_t here = __ballot(u >= first && u < first + count);
+                                               int64_t& before, AttnPlace& at) {
+    const int64_t end = a.d.B > 1 ? wave_scan64(x.units, lane) : x.units, first = before + end - x.units;
+    const uint64_t here = __ballot(BY_NUMBER ? base + lane == u : u >= first && u < first + x.units);
     if (here) {
         const int src = __builtin_ctzll(here);
         at.b = base + src;
+        at.base = base;
+        at.before = before;
         at.first = read_lane64(first, src);
-        at.count = read_lane64(count, src);
-        at.first_unit = TILES ? units_before + read_lane64(units_end - x.units, src) : at.first;
+        at.count = read_lane64(x.units, src);
         at.s.n = __builtin_amdgcn_readlane(x.s.n, src);
         at.s.row0 = read_lane64(x.s.row0, src);
         at.s.prefix = __builtin_amdgcn_readlane(x.s.prefix, src);
@@ -171,18 +164,22 @@ __device__ __forceinline__ bool attn_find_here(const AttnArgs& a, const AttnLane
         return true;
     }
     before += read_lane64(end, 63);
-    if (TILES) units_before += read_lane64(units_end, 63);
     return false;
 }
-template <AttnKind KIND, bool TILES>
-__device__ __forceinline__ bool attn_find(const AttnArgs& a, int64_t u, int lane, AttnPlace& at) {
-    int64_t before = 0, units_before = 0;
-    for (int base = 0; base < a.d.B; base += 64) {
+template <AttnKind KIND, bool BY_NUMBER>
+__device__ __forceinline__ void attn_find(const AttnArgs& a, int base, int64_t before, int64_t u, int lane, AttnPlace& at) {
+    for (; base < a.d.B; base += 64) {
         AttnLane<KIND> x;
         x.read(a, base + lane);
-        if (attn_find_here<KIND, TILES>(a, x, base, u, lane, before, units_before, at)) return true;
+        if (attn_find_here<KIND, BY_NUMBER>(a, x, base, u, lane, before, at)) return;
     }
-    return false;
+}
+// The place of a later unit of the same workgroup, from where the last one was.
+template <AttnKind KIND>
+__device__ __forceinline__ void attn_next(const AttnArgs& a, int64_t u, int lane, AttnPlace& at) {
+    if (u >= at.first && u < at.first + at.count) return;
+    const bool on = u >= at.before;  // not in the next key head
+    attn_find<KIND, false>(a, on ? at.base : 0, on ? at.before : 0, u, lane, at);
 }
 
 // The plan; `x`: what the lanes have read of the first 64 sequences.
@@ -190,6 +187,7 @@ template <AttnKind KIND>
 __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane, AttnLane<KIND>& x) {
     x.read(a, lane);
     int64_t units = x.units;
+#pragma unroll 4
     for (int b = lane + 64; b < a.d.B; b += 64) {
         AttnLane<KIND> y;
         y.read(a, b);
@@ -227,8 +225,8 @@ __device__ __forceinline__ bool attn_begin(const AttnArgs& a, int wg, int lane, 
     r.u = r.team * plan.per;
     r.end = min(r.u + plan.per, plan.units * (a.cache.H_kv * a.head_tiles));
     const int64_t uh = r.u - quotient(r.u, plan.units) * plan.units;
-    int64_t before = 0, units_before = 0;
-    if (!attn_find_here<KIND, false>(a, x, 0, uh, lane, before, units_before, at)) attn_find<KIND, false>(a, uh, lane, at);
+    int64_t before = 0;
+    if (!attn_find_here<KIND, false>(a, x, 0, uh, lane, before, at)) attn_find<KIND, false>(a, 64, before, uh, lane, at);
     return true;
 }
 
@@ -272,16 +270,6 @@ __device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, const AttnSeq
     x.units = int(min(int64_t(x.all - x.unit), most));
     return uniform(x);
 }
-// The first unit of a tile within its sequence.
-template <AttnKind KIND>
-__device__ __forceinline__ int64_t attn_tile_unit(const AttnArgs& a, const AttnSeq& s, int tiles, int tile) {
-    const int pair = attn_pair<KIND>(a, s, tiles);
-    if constexpr (KIND != kAttnPrefill) return int64_t(pair) * tile;
-    const int other = tiles - 1 - tile;
-    if (other <= tile) return int64_t(pair) * other;
-    return int64_t(pair) * tile + attn_units<KIND>(a, s, other);
-}
-
 // Part `part` of the workspace: a tile's unnormalised outputs over some of its
 // keys (in the order that suits the kernel that writes them), then the running
 // maximum (in powers of two) and sum of every row.

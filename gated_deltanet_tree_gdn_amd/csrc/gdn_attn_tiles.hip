@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
         const int tid = fresh(threadIdx.x), lane = tid & 63, col = lane & 31, half = lane >> 5;
         const int h = int(quotient(u, range.units));
         const int64_t uh = u - h * range.units;
-        if (uh < at.first || uh >= at.first + at.count) attn_find<KIND, false>(a, uh, lane, at);
+        attn_next<KIND>(a, uh, lane, at);
         const AttnSeq s = at.s;
         const AttnPiece it = attn_piece<KIND>(a, s, attn_tiles<KIND>(a, s), uh - at.first, range.end - u);
         const bool first = u == range.u;
