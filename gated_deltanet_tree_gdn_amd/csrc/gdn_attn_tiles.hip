@@ -279,26 +279,24 @@ __device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 
 // ---------------------------------------------------------------------------
 // A piece of a workgroup's range: some keys of one key head for a tile of rows
-// (token, query head of the group) of a sequence; a wavefront has RB blocks of
-// 32 of the rows, so that an operand read from LDS serves RB products.  64 keys
-// at a time lie in LDS, the next 64 on their way there.
+// (token, query head of the group) of a sequence, 32 of them a wavefront's.  64
+// keys at a time lie in LDS, the next 64 on their way there.
 //   S^T = K Q^T    keys x rows on MFMA, Q in registers for the whole piece
 //   O^T += V^T P   V read transposed; the lanes hold P where the product wants it
 // The running maximum is raised only where a row's scores pass it by more than
 // 2^8: P then stays below 2^8, which costs no precision in floating point, and
-// O is rarely rescaled.  P is rounded to bf16 for the product, 2^-9 of every
+// O is rarely rescaled.  P is rounded to bf16 for the product, at most 2^-8 of a
 // weight, as much as the output's own rounding; the sum is that of the rounded
 // weights.
 // A masked key has P = 0, but 0 times an infinity or NaN of its value would not
 // be 0: a tile with masked keys and such values is multiplied with zeros in
 // their place, and the rows that do see them get them from products of marks.
-// A wavefront has a SIMD's registers to itself and issues in order, so the main
-// loop stands in the order in which it is to run: beside every product what
-// the vector unit can do meanwhile.
+// A SIMD has registers for one wavefront (d = 256) or two, and a wavefront issues
+// in order, so the main loop stands in the order in which it is to run: beside
+// every product what the vector unit can do meanwhile.
 // ---------------------------------------------------------------------------
 template <AttnKind KIND, int D, bool F8>
 __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnArgs a) {
-    constexpr int RB = 1, kRows = kTileRows * RB;
     using KL = Layout<D, false>;
     using VL = Layout<D, true>;
     extern __shared__ uint4 lds_raw[];
@@ -321,37 +319,30 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
         if (it.all == 0) continue;
         const float scale = a.d.scale * kLog2e * (a.cache.k_scale ? a.cache.k_scale[h] : 1.0f);
         const int all_rows = s.n * a.group;
-        const int row0 = (KIND == kAttnVerify ? range.mate : it.tile) * kRows, rows = min(kRows, all_rows - row0);
+        const int row0 = (KIND == kAttnVerify ? range.mate : it.tile) * kTileRows, rows = min(kTileRows, all_rows - row0);
         const int begin = it.unit * kKeys;
         const int end = __builtin_amdgcn_readfirstlane(min(begin + it.units * kKeys, attn_seen<KIND>(a, s, it.tile)));
         const int32_t* table = a.table + at.b * a.d.table_stride;
         // tokens from here on are masked for some of the tile's rows
         const int open_end = KIND == kAttnPrefill ? __builtin_amdgcn_readfirstlane(s.prefix + row0 / a.group + 1) : s.prefix;
 
-        int token[RB], head[RB];
-        bf16x8 q[RB][D / 16];
-        f32x16 o[RB][D / 32];
-        float m[RB], l[RB];  // m: what the powers are taken against
+        const int row = min(row0 + wave * 32 + col, all_rows - 1), token = row / a.group;
+        const int head = h * a.group + row - token * a.group;
+        bf16x8 q[D / 16];
+        f32x16 o[D / 32];
+        float m = -inf, l = 0.0f;  // m: what the powers are taken against
+        const uint16_t* qp = a.q + (s.row0 + token) * a.d.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            const int row = min(row0 + (wave * RB + b) * 32 + col, all_rows - 1);
-            token[b] = row / a.group;
-            head[b] = h * a.group + row - token[b] * a.group;
-            const uint16_t* qp = a.q + (s.row0 + token[b]) * a.d.q_stride + int64_t(head[b]) * D + 8 * half;
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                q[b][n] = load_frag(qp + 16 * n);
-                if constexpr (D == 256) asm volatile("" : "+a"(q[b][n]));  // beside the accumulators
-            }
-#pragma unroll
-            for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[b][n][j] = 0.0f;
-            m[b] = -inf;
-            l[b] = 0.0f;
+        for (int n = 0; n < D / 16; ++n) {
+            q[n] = load_frag(qp + 16 * n);
+            if constexpr (D == 256) asm volatile("" : "+a"(q[n]));  // beside the accumulators
         }
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[n][j] = 0.0f;
 
-        // Register i of a score x[b][j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col` of block b.
+        // Register i of a score x[j]: key 32 j + 8 (i / 4) + 4 half + i % 4 of the tile, row `col` of the wavefront's.
         // K: piece 2 n + half of row 32 j + col; its permutation's higher bit swaps neighbouring n.
         const int k_swap = KL::perm(col) >> 1, k_piece = (half ^ (KL::perm(col) & 1)) << 4;
         const uint32_t k_even = lds_k + KL::row(col) + k_piece + 32 * k_swap, k_odd = k_even - 64 * k_swap;
@@ -381,17 +372,17 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             top = fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
             return top == -inf ? top : top * scale;
         };
-        auto raise = [&](int b, float top) {
-            if (__ballot(top > m[b] + 8.0f)) {
-                const float m_new = fmaxf(m[b], top), keep = exp2_fast(m[b] - finite_max(m_new));
-                m[b] = m_new;
-                l[b] *= keep;
+        auto raise = [&](float top) {
+            if (__ballot(top > m + 8.0f)) {
+                const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
+                m = m_new;
+                l *= keep;
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n) {
                     if constexpr (D == 256)
-                        update_acc(o[b][n], keep, {});
+                        update_acc(o[n], keep, {});
                     else
-                        o[b][n] *= keep;
+                        o[n] *= keep;
                 }
             }
         };
@@ -437,21 +428,16 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             };
             // products of a tile with K, and with V; operands read ahead
             constexpr int NS = D / 8, AHEAD = D == 256 ? 8 : 4;
-            f32x16 x[RB][2];  // scores of the tile at t0
-            float top[RB];
+            f32x16 x[2];  // scores of the tile at t0
+            float top = -inf;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 const bf16x8 f = k_frag(i & 1, i >> 1, 0);
-#pragma unroll
-                for (int b = 0; b < RB; ++b) x[b][i & 1] = mfma32(f, q[b][i >> 1], i < 2 ? zero : x[b][i & 1]);
+                x[i & 1] = mfma32(f, q[i >> 1], i < 2 ? zero : x[i & 1]);
             }
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                top[b] = -inf;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) top[b] = fmaxf(top[b], x[b][i >> 4][i & 15]);
-                top[b] = largest(top[b]);
-            }
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i >> 4][i & 15]);
+            top = largest(top);
 
             // A tile that every row sees all of, and that is not the last: the
             // scores y of the next tile beside the powers of this one's x, and
@@ -460,38 +446,31 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             // before those of the next turn, V's likewise (e4m3, which waits in
             // registers, has V's beside the products with V as well, where x no
             // longer needs them, and stores both at once).
-            auto turn = [&](f32x16 (&x)[RB][2], f32x16 (&y)[RB][2], int t0, auto buf) {
+            auto turn = [&](f32x16 (&x)[2], f32x16 (&y)[2], int t0, auto buf) {
                 arrive(t0, buf, std::integral_constant<int, F8 ? 0 : L>());
-                float base[RB];
-                bf16x8 f[AHEAD], p[RB][4];
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    raise(b, top[b]);
-                    base[b] = finite_max(m[b]);
-                    top[b] = -inf;
-                }
+                bf16x8 f[AHEAD], p[4];
+                raise(top);
+                const float base = finite_max(m);
+                top = -inf;
                 // powers that are formed up to step i: 20 of 32 beside K, the others
                 // beside the first half of V, in time for the product that wants them
                 auto formed = [](int i) { return i <= NS ? i * 20 / NS : i >= NS + NS / 2 ? 32 : 20 + (i - NS) * 24 / NS; };
                 auto powers = [&](int i) {
 #pragma unroll
-                    for (int e = formed(i); e < formed(i + 1); ++e)
-#pragma unroll
-                        for (int b = 0; b < RB; ++b) {
-                            p[b][e >> 3][e & 7] = static_cast<__bf16>(exp2_fast(fmaf(x[b][e >> 4][e & 15], scale, -base[b])));
-                            if (e & 1) {
-                                const bf16x2 two{p[b][e >> 3][(e & 7) - 1], p[b][e >> 3][e & 7]}, one{1.0f, 1.0f};
-                                l[b] = __builtin_amdgcn_fdot2_f32_bf16(two, one, l[b], false);
-                            }
+                    for (int e = formed(i); e < formed(i + 1); ++e) {
+                        p[e >> 3][e & 7] = static_cast<__bf16>(exp2_fast(fmaf(x[e >> 4][e & 15], scale, -base)));
+                        if (e & 1) {
+                            const bf16x2 two{p[e >> 3][(e & 7) - 1], p[e >> 3][e & 7]}, one{1.0f, 1.0f};
+                            l = __builtin_amdgcn_fdot2_f32_bf16(two, one, l, false);
                         }
+                    }
                 };
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) f[i] = k_frag(i & 1, i >> 1, buf ^ 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) y[b][i & 1] = mfma32(f[i % AHEAD], q[b][i >> 1], i < 2 ? zero : y[b][i & 1]);
+                    y[i & 1] = mfma32(f[i % AHEAD], q[i >> 1], i < 2 ? zero : y[i & 1]);
                     const int r = i + AHEAD;
                     if (!F8 && r == NS) loads_barrier<L>();  // V is there
                     f[i % AHEAD] = r < NS ? k_frag(r & 1, r >> 1, buf ^ 1) : v_frag((r - NS) % (D / 32), (r - NS) / (D / 32), buf);
@@ -502,27 +481,24 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
                     const int n = i % (D / 32), k = i / (D / 32), r = i + AHEAD;
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) o[b][n] = mfma32(f[i % AHEAD], p[b][k], o[b][n]);
+                    o[n] = mfma32(f[i % AHEAD], p[k], o[n]);
                     if (const int j = F8 ? i - NS / 2 : i; j >= 0 && j < L) load.v.part(j);
                     if (r < NS) f[i % AHEAD] = v_frag(r % (D / 32), r / (D / 32), buf);
                     powers(NS + i);
                     if (i >= NS / 2) {
 #pragma unroll
                         for (int e = (i - NS / 2) * 64 / NS; e < (i - NS / 2 + 1) * 64 / NS; ++e)
-#pragma unroll
-                            for (int b = 0; b < RB; ++b) top[b] = fmaxf(top[b], y[b][e >> 4][e & 15]);
+                            top = fmaxf(top, y[e >> 4][e & 15]);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) top[b] = largest(top[b]);
+                top = largest(top);
             };
             int t0 = begin, buf = 0;
             // (pages of fewer than 16 rows take the plain loop below for all tiles)
             const int open = missing || a.page_shift < 4 ? begin : min(max(open_end, begin), end - 1);
             {
-                f32x16 y[RB][2];
+                f32x16 y[2];
                 for (; t0 + 2 * kKeys <= open; t0 += 2 * kKeys) {
                     turn(x, y, t0, std::integral_constant<int, 0>());
                     turn(y, x, t0 + kKeys, std::integral_constant<int, 1>());
@@ -530,9 +506,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
                 if (t0 + kKeys <= open) {
                     turn(x, y, t0, std::integral_constant<int, 0>());
 #pragma unroll
-                    for (int b = 0; b < RB; ++b)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) x[b][j] = y[b][j];
+                    for (int j = 0; j < 2; ++j) x[j] = y[j];
                     t0 += kKeys;
                     buf = 1;
                 }
@@ -543,7 +517,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             for (; t0 < end; t0 += kKeys, buf ^= 1) {
                 arrive(t0, buf, std::integral_constant<int, 0>());
                 if (t0 + kKeys < end) rest();
-                uint32_t see[RB][2];
+                uint32_t see[2];
                 bool odd = false;
                 const bool masked = missing || t0 + kKeys > min(open_end, end);
                 if (masked) {
@@ -555,58 +529,49 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t there = 0xffffffffu;
+                    uint32_t bits = 0xffffffffu;
                     if (missing) {
                         const int t = t0 + 32 * j + col;
                         const int page = t < end ? table[t >> a.page_shift] : -1;
-                        there = uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
+                        bits = uint32_t(__ballot(page >= 0 && page < a.cache.n_pages));
                     }
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        uint32_t bits = there;
-                        if (masked)
-                            bits &= visible<KIND>(a, s, token[b],
-                                                  KIND == kAttnVerify
-                                                      ? a.anc + (int64_t(at.b) * s.n + token[b]) * ((a.d.T + 31) >> 5)
-                                                      : nullptr,
-                                                  t0 + 32 * j, end);
-                        see[b][j] = bits >> (4 * half);
-                    }
+                    if (masked)
+                        bits &= visible<KIND>(a, s, token,
+                                              KIND == kAttnVerify
+                                                  ? a.anc + (int64_t(at.b) * s.n + token) * ((a.d.T + 31) >> 5)
+                                                  : nullptr,
+                                              t0 + 32 * j, end);
+                    see[j] = bits >> (4 * half);
                 }
-                bf16x8 p[RB][4];
+                bf16x8 p[4];
+                float most = -inf;
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    float most = -inf;
+                for (int i = 0; i < 32; ++i) {
+                    if (!(see[i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) x[i >> 4][i & 15] = -inf;
+                    most = fmaxf(most, x[i >> 4][i & 15]);
+                }
+                raise(largest(most));
+                const float base = finite_max(m);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (!(see[b][i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) x[b][i >> 4][i & 15] = -inf;
-                        most = fmaxf(most, x[b][i >> 4][i & 15]);
-                    }
-                    raise(b, largest(most));
-                    const float base = finite_max(m[b]);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float e = exp2_fast(fmaf(x[b][i >> 4][i & 15], scale, -base));
-                        // a scale of zero turns -inf into NaN
-                        if (!(see[b][i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) e = 0.0f;
-                        p[b][i >> 3][i & 7] = static_cast<__bf16>(e);
-                        l[b] += static_cast<float>(p[b][i >> 3][i & 7]);
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    float e = exp2_fast(fmaf(x[i >> 4][i & 15], scale, -base));
+                    // a scale of zero turns -inf into NaN
+                    if (!(see[i >> 4] >> (8 * (i >> 2 & 3) + (i & 3)) & 1)) e = 0.0f;
+                    p[i >> 3][i & 7] = static_cast<__bf16>(e);
+                    l += static_cast<float>(p[i >> 3][i & 7]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int n = 0; n < D / 32; ++n) {
                         const bf16x8 f = v_frag(n, k, buf);
-#pragma unroll
-                        for (int b = 0; b < RB; ++b) o[b][n] = mfma32(f, p[b][k], o[b][n]);
+                        o[n] = mfma32(f, p[k], o[n]);
                     }
                 if (t0 + kKeys < end) {
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
                         const bf16x8 f = k_frag(i & 1, i >> 1, buf ^ 1);
-#pragma unroll
-                        for (int b = 0; b < RB; ++b) x[b][i & 1] = mfma32(f, q[b][i >> 1], i < 2 ? zero : x[b][i & 1]);
+                        x[i & 1] = mfma32(f, q[i >> 1], i < 2 ? zero : x[i & 1]);
                     }
                 }
                 if (!odd) continue;
@@ -629,61 +594,57 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
                     rewrite<D>(to, kind, tid);
                     __syncthreads();
 #pragma unroll
-                    for (int b = 0; b < RB; ++b)
+                    for (int n = 0; n < D / 32; ++n) {
+                        f32x16 count = zero;
 #pragma unroll
-                        for (int n = 0; n < D / 32; ++n) {
-                            f32x16 count = zero;
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t bits = see[k >> 1];
+                            asm volatile("" : "+v"(bits));  // formed anew each time, to hold no registers for it
+                            bf16x8 one;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t bits = see[b][k >> 1];
-                                asm volatile("" : "+v"(bits));  // formed anew each time, to hold no registers for it
-                                bf16x8 one;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int r = 8 * (k & 1) + i;
-                                    one[i] = static_cast<__bf16>((bits >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
-                                }
-                                count = mfma32(v_frag(n, k, buf), one, count);
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = 8 * (k & 1) + i;
+                                one[i] = static_cast<__bf16>((bits >> (8 * (r >> 2) + (r & 3)) & 1) ? 1.0f : 0.0f);
                             }
-                            float g[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
-                            if constexpr (D == 256) {
-                                update_acc(o[b][n], 1.0f, g);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[b][n][i] += g[i];
-                            }
+                            count = mfma32(v_frag(n, k, buf), one, count);
                         }
+                        float g[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) g[i] = count[i] > 0.0f ? what : 0.0f;
+                        if constexpr (D == 256) {
+                            update_acc(o[n], 1.0f, g);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[n][i] += g[i];
+                        }
+                    }
                 }
             }
         }
 
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            l[b] += __shfl_xor(l[b], 32);
-            const int r = (wave * RB + b) * 32 + col;
-            if (r >= rows) continue;
+        l += __shfl_xor(l, 32);
+        const int r = wave * 32 + col;
+        if (r < rows) {
             if (it.units < it.all) {
                 // 4 elements of each lane at a time, as they lie in the registers
-                float* part = part_out(a, 2 * int64_t(range.w) + (first ? 0 : 1), kRows, D);
-                f32x4* out = reinterpret_cast<f32x4*>(part) + (wave * RB + b) * (D / 4 * 32) + lane;
+                float* part = part_out(a, 2 * int64_t(range.w) + (first ? 0 : 1), kTileRows, D);
+                f32x4* out = reinterpret_cast<f32x4*>(part) + wave * (D / 4 * 32) + lane;
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        out[(4 * n + i) * 64] = f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]};
+                        out[(4 * n + i) * 64] = f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
                 if (half == 0) {
-                    part[kRows * D + r] = m[b];
-                    part[kRows * (D + 1) + r] = l[b];
+                    part[kTileRows * D + r] = m;
+                    part[kTileRows * (D + 1) + r] = l;
                 }
             } else {
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        attn_store<D>(a, s.row0 + token[b], h, head[b], 32 * n + 8 * i + 4 * half,
-                                      f32x4{o[b][n][4 * i], o[b][n][4 * i + 1], o[b][n][4 * i + 2], o[b][n][4 * i + 3]}, l[b]);
+                        attn_store<D>(a, s.row0 + token, h, head, 32 * n + 8 * i + 4 * half,
+                                      f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]}, l);
             }
         }
         if (u < range.end) __syncthreads();  // the next piece overwrites LDS
