@@ -62,9 +62,7 @@ __device__ __forceinline__ void update_acc(f32x16& x, float f, const float (&g)[
         float t, y = x[i];
         asm volatile(
             "v_accvgpr_read_b32 %1, %0\n\t"
-            "s_nop 1\n\t"
             "v_fma_f32 %1, %1, %2, %3\n\t"
-            "s_nop 1\n\t"
             "v_accvgpr_write_b32 %0, %1"
             : "+a"(y), "=&v"(t)
             : "v"(f), "v"(g[i]));
@@ -183,23 +181,25 @@ struct Loader {
         v.init(a, h, lane);
         window.open(end, a.page_shift);
     }
+    template <bool LARGE = false>
     __device__ __forceinline__ void find(const AttnArgs& a, const int32_t* table, int t0, int end, int wave, int lane) {
         t0 += 16 * wave;
         const int from = min(t0, end - 1) >> a.page_shift, to = min(t0 + 15, end - 1) >> a.page_shift;
         window.cover(table, from, to, lane);
-        if (a.page_shift >= 4) {
+        if (LARGE || a.page_shift >= 4) {
             page = __builtin_amdgcn_readlane(window.ids, from - window.first);
             if (page < 0 || page >= a.cache.n_pages) page = 0;
             row = t0 & (a.cache.page_size - 1);
         }
     }
     // V's tile at t0 and K's at t0 + kKeys: all of it where pages are small,
-    // otherwise the loads follow with k.part() and v.part().
+    // otherwise (and only those with LARGE) the loads follow with k.part() and v.part().
+    template <bool LARGE>
     __device__ __forceinline__ void begin(const AttnArgs& a, const int32_t* table, uint32_t k_lds, uint32_t v_lds, int t0,
                                           int end, int wave, int lane) {
-        if (a.page_shift >= 4) {
+        if (LARGE || a.page_shift >= 4) {
             v.at(v_lds, page, row, wave);
-            find(a, table, t0 + kKeys, end, wave, lane);
+            find<LARGE>(a, table, t0 + kKeys, end, wave, lane);
             k.at(k_lds, page, row, wave);
         } else {
             find(a, table, t0, end, wave, lane);
@@ -375,7 +375,9 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
         auto raise = [&](float top) {
             if (__ballot(top > m + 8.0f)) {
                 const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
+                const bool some = __ballot(m != -inf) != 0;  // that is not zero
                 m = m_new;
+                if (!some) return;
                 l *= keep;
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n) {
@@ -415,16 +417,16 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             wait_count<0>();
             missing = __builtin_amdgcn_readfirstlane(__syncthreads_or(missing));
             // K of the tile behind the last is not used: it repeats what there is
-            load.begin(a, table, lds_k + KL::kTile, lds_v, begin, end, wave, lane);
+            load.template begin<false>(a, table, lds_k + KL::kTile, lds_v, begin, end, wave, lane);
             rest();
             // K of the tile after t0 and, but for the last PENDING loads, V of that
             // at t0 are in LDS; those after them may come.
-            auto arrive = [&](int t0, int buf, auto pending) {
+            auto arrive = [&](int t0, int buf, auto pending, auto large) {
                 load.k.store(lds_k + (buf ^ 1) * KL::kTile, wave, lane);
                 load.v.store(lds_v + buf * VL::kTile, wave, lane);
                 loads_barrier<pending>();
                 if (t0 + kKeys < end)
-                    load.begin(a, table, lds_k + buf * KL::kTile, lds_v + (buf ^ 1) * VL::kTile, t0 + kKeys, end, wave, lane);
+                    load.template begin<large>(a, table, lds_k + buf * KL::kTile, lds_v + (buf ^ 1) * VL::kTile, t0 + kKeys, end, wave, lane);
             };
             // products of a tile with K, and with V; operands read ahead
             constexpr int NS = D / 8, AHEAD = D == 256 ? 8 : 4;
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             // registers, has V's beside the products with V as well, where x no
             // longer needs them, and stores both at once).
             auto turn = [&](f32x16 (&x)[2], f32x16 (&y)[2], int t0, auto buf) {
-                arrive(t0, buf, std::integral_constant<int, F8 ? 0 : L>());
+                arrive(t0, buf, std::integral_constant<int, F8 ? 0 : L>(), std::true_type());
                 bf16x8 f[AHEAD], p[4];
                 raise(top);
                 const float base = finite_max(m);
@@ -499,23 +501,24 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             const int open = missing || a.page_shift < 4 ? begin : min(max(open_end, begin), end - 1);
             {
                 f32x16 y[2];
-                for (; t0 + 2 * kKeys <= open; t0 += 2 * kKeys) {
+                while (t0 + kKeys <= open) {
                     turn(x, y, t0, std::integral_constant<int, 0>());
-                    turn(y, x, t0 + kKeys, std::integral_constant<int, 1>());
-                }
-                if (t0 + kKeys <= open) {
-                    turn(x, y, t0, std::integral_constant<int, 0>());
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) x[j] = y[j];
                     t0 += kKeys;
-                    buf = 1;
+                    if (t0 + kKeys > open) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) x[j] = y[j];
+                        buf = 1;
+                        break;
+                    }
+                    turn(y, x, t0, std::integral_constant<int, 1>());
+                    t0 += kKeys;
                 }
             }
 
             // Other tiles, step by step.
 #pragma unroll 1
             for (; t0 < end; t0 += kKeys, buf ^= 1) {
-                arrive(t0, buf, std::integral_constant<int, 0>());
+                arrive(t0, buf, std::integral_constant<int, 0>(), std::false_type());
                 if (t0 + kKeys < end) rest();
                 uint32_t see[2];
                 bool odd = false;
