@@ -14,12 +14,11 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJoinPieces = 2;  // of 4 elements, of a thread that joins tiles
 
-// Workgroups that join a tile (or team).
-__host__ __device__ inline int join_blocks(const AttnArgs& a) {
+// Workgroups that join a tile (or team), whose threads take `pieces` times 4 elements.
+__host__ __device__ inline int join_blocks(const AttnArgs& a, int pieces) {
     const int rows = a.group < kDecodeRows ? a.group : kDecodeRows;
-    return a.kind == kAttnDecode ? rows : kTileRows * (a.cache.d / 4) / (kThreads * kJoinPieces) * a.team;
+    return a.kind == kAttnDecode ? rows : kTileRows * (a.cache.d / 4) / (kThreads * pieces) * a.team;
 }
 
 struct Joined {
@@ -39,10 +38,10 @@ struct Joined {
 // not), otherwise for every end of a range within a tile, of which the first
 // joins it: whichever are fewer, since each of them has to find its place.  Single tokens: a workgroup for every row, since
 // there are few and their parts may be hundreds; the workgroup's threads take
-// the parts in turn.  Tiles: every thread has kJoinPieces pieces of 4 elements,
-// in the order in which the parts hold them.
+// the parts in turn.  Tiles: every thread has `pieces` pieces of 4 elements, in
+// the order in which the parts hold them.
 template <AttnKind KIND, int D, bool BY_TILE>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int64_t workgroups) {
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int64_t workgroups, int pieces) {
     constexpr int C = D / 4, K = kThreads / C;  // threads of a row, shares of the parts (single tokens)
     constexpr bool one = KIND == kAttnDecode;
     constexpr int rows_of_part = one ? kDecodeRows : kTileRows;
@@ -50,7 +49,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int64_t work
     __shared__ float share_m[4], share_l[one ? K : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int heads = a.cache.H_kv * a.head_tiles;
-    const int blocks = join_blocks(a);
+    const int blocks = join_blocks(a, pieces);
     const int64_t wg = block_id();
     if (wg >= workgroups) return;
     const int block = int(wg % blocks) / a.team, mate = int(wg % blocks) % a.team;
@@ -119,9 +118,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int64_t work
         }
     } else {
         const int row0 = (KIND == kAttnVerify ? mate : t) * kTileRows, rows = min(kTileRows, s.n * a.group - row0);
-#pragma unroll
-        for (int j = 0; j < kJoinPieces; ++j) {
-            const int e = (block * kJoinPieces + j) * kThreads + tid;  // 32 rows have 32 C pieces
+        for (int j = 0; j < pieces; ++j) {
+            const int e = (block * pieces + j) * kThreads + tid;  // 32 rows have 32 C pieces
             const int r = e / (32 * C) * 32 + (e & 31), d = e / 64 % (C / 2) * 8 + (e >> 5 & 1) * 4;
             if (r >= rows) continue;
             Joined y;
@@ -161,12 +159,18 @@ __global__ __launch_bounds__(kThreads) void status_kernel(AttnArgs a) {
 }
 
 template <AttnKind KIND, bool BY_TILE>
-hipError_t launch_join(const AttnArgs& a, int64_t workgroups, hipStream_t stream) {
+hipError_t launch_join(const AttnArgs& a, int64_t tiles, hipStream_t stream) {
+    // half as many workgroups as the GPU has room for, or more: a thread with one piece waits for memory only once, but every
+    // workgroup has to find its place (one piece against two: 38 us and 40 us for a tree of 48 nodes behind
+    // 2855 tokens, but 448 us and 436 us for prompts of 6007 tokens behind 20011)
+    int pieces = 1;
+    while (KIND != kAttnDecode && pieces < 8 && tiles * join_blocks(a, 2 * pieces) >= 1024) pieces *= 2;
+    const int64_t workgroups = tiles * join_blocks(a, pieces);
     const dim3 grid = grid_of(workgroups);
     switch (a.cache.d) {
-        case 64: join_kernel<KIND, 64, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
-        case 128: join_kernel<KIND, 128, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
-        default: join_kernel<KIND, 256, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups); break;
+        case 64: join_kernel<KIND, 64, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups, pieces); break;
+        case 128: join_kernel<KIND, 128, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups, pieces); break;
+        default: join_kernel<KIND, 256, BY_TILE><<<grid, kThreads, 0, stream>>>(a, workgroups, pieces); break;
     }
     return hipGetLastError();
 }
@@ -174,8 +178,8 @@ template <AttnKind KIND>
 hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
     const int64_t tiles = int64_t(a.d.B) * a.cache.H_kv * a.head_tiles, ends = a.teams - 1;
     if constexpr (KIND != kAttnPrefill)  // how many tiles prompts have is not known here
-        if (tiles <= ends) return launch_join<KIND, true>(a, tiles * join_blocks(a), stream);
-    return launch_join<KIND, false>(a, ends * join_blocks(a), stream);
+        if (tiles <= ends) return launch_join<KIND, true>(a, tiles, stream);
+    return launch_join<KIND, false>(a, ends, stream);
 }
 
 }  // namespace
@@ -189,7 +193,7 @@ void attn_shape(AttnArgs& a) {
     a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
     const int unit = one ? kDecodeUnit : kTilesUnit;
     a.unit_shift = __builtin_ctz(unit);
-    a.min_units = one ? 1 : 4;
+    a.min_units = one ? 1 : 2;
     const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
     // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
     // overlap, where cu_seqlens decreases, and each may then have all rows)

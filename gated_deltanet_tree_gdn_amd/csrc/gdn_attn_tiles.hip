@@ -333,10 +333,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
         float m = -inf, l = 0.0f;  // m: what the powers are taken against
         const uint16_t* qp = a.q + (s.row0 + token) * a.d.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            q[n] = load_frag(qp + 16 * n);
-            if constexpr (D == 256) asm volatile("" : "+a"(q[n]));  // beside the accumulators
-        }
+        for (int n = 0; n < D / 16; ++n) q[n] = load_frag(qp + 16 * n);
 #pragma unroll
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -412,6 +409,10 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
             for (int p = (begin >> a.page_shift) + tid; p <= (end - 1) >> a.page_shift; p += kThreads) {
                 const int page = table[p];
                 missing |= page < 0 || page >= a.cache.n_pages;
+            }
+            if constexpr (D == 256) {
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) asm volatile("" : "+a"(q[n]));  // beside the accumulators
             }
             load.k.store(lds_k, wave, lane);
             wait_count<0>();
