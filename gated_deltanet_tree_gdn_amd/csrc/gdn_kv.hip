@@ -61,7 +61,9 @@ struct Raw {
 // there to a fraction of a turn, and from then on fp32 is enough for outputs
 // of 8 bits.  A workgroup takes `passes` times 256 / (d / 8) heads of one token;
 // the elements of a pass are on their way while the one before (the first:
-// while the angles) is worked on.
+// while the angles) is worked on.  Memory bounds it: 12289 tokens of 32 + 2 x 8
+// heads of 128 into an e4m3 cache take 71 us, 3.9 TB/s; a single token 4 us, a
+// launch and loads that wait for each other.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int passes, int groups, int page_shift) {
@@ -181,7 +183,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a, int pa
 // ranked by counting bits, then every thread carries its 16-byte pieces of all
 // rows down in the path's order.  A row's new place is never behind its old
 // one (the j-th node of a path has index j or more), so what a thread
-// overwrites it has read before, also with 8 rows in flight.
+// overwrites it has read before, also with 8 rows in flight.  Latency bounds it:
+// 12 caches take 5 us for one sequence and 6 for 32 (path of 8, 13 MB).
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void commit_kernel(KvCommitArgs a, int page_shift) {
     __shared__ int32_t from[GDN_ATTN_MAX_N], to[GDN_ATTN_MAX_N];
