@@ -296,11 +296,11 @@ __device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 // in order, so the main loop stands in the order in which it is to run: beside
 // every product what the vector unit can do meanwhile.
 // Measured, causal prompts and trees of 64 nodes over 4096 tokens with 16 query
-// and 2 key heads: 406 and 438 TFLOP/s (d = 64, bound by the powers: 32 x 64 of
-// them per 16 matrix instructions), 621 and 702 (128), 787 and 852 (256); a
+// and 2 key heads: 382 and 457 TFLOP/s (d = 64, bound by the powers: 32 x 64 of
+// them per 16 matrix instructions), 626 and 702 (128), 833 and 881 (256); a
 // prompt of 16384 with d = 256: 1.04 PFLOP/s, two thirds of what the largest
 // library product reaches, the rest being instructions that no product covers.
-// e4m3 is 3 to 12 % slower, pages of fewer than 16 tokens (whose rows are
+// e4m3 is 0 to 17 % slower, pages of fewer than 16 tokens (whose rows are
 // addressed one by one, and which take the plain loop) half as fast.
 // ---------------------------------------------------------------------------
 template <AttnKind KIND, int D, bool F8>

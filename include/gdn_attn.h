@@ -26,6 +26,10 @@
  *  - Keys and values that a query may not see (behind its sequence's end, on
  *    other branches of a tree, later in a prompt) have no influence on its
  *    output, whatever they hold, infinities and NaN included.
+ *    Those that it sees and that are not finite make what they reach infinite
+ *    or NaN.
+ *  - A workspace is one call's until that call has run: calls that may overlap
+ *    (on two streams, or graphs replayed at once) need one each.
  *  - Scores, maxima and sums of the softmax and all accumulations are fp32.
  */
 #ifndef GDN_ATTN_H
