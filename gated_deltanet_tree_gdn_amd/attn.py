@@ -103,8 +103,9 @@ class GdnKvCache:
         scales = [_dense(s, name, (H,), index, _torch.float32) for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
         self.k, self.v, self.k_scale, self.v_scale, self.index = k, v, k_scale, v_scale, index
         self.heads, self.d = H, d
+        strides = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in range(3)]  # one page, row or head has none
         self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), *scales, n, page, H, d,
-                                    GDN_BF16 if k.dtype == _bf16 else GDN_E4M3, 0, *k.stride()[:3], *v.stride()[:3])
+                                    GDN_BF16 if k.dtype == _bf16 else GDN_E4M3, 0, *strides)
         self.raw = bytes(self.struct)  # an array of these is joined, 6 us sooner than built of 12 structs
 
 

@@ -118,3 +118,18 @@ def test_two_streams_at_once():
     got = [[gdn.gdn_attn_decode(cache, x, p.table, length, stream=s) for _ in range(8)] for x, s in zip(q, streams)]
     torch.cuda.synchronize()
     assert all(torch.equal(y, w) for x, w in zip(got, want) for y in x)
+
+
+def test_one_page_row_or_head_has_no_stride():
+    """what a view has there is any number"""
+    gen = generator(2)
+    page = randn(gen, 16, 64).to(BF16)
+    q, table = randn(gen, 1, 2, 64).to(BF16), i32(0).view(1, 1)
+    plain = gdn.GdnKvCache(page.view(1, 16, 1, 64), page.view(1, 16, 1, 64))
+    odd = page.as_strided((1, 16, 1, 64), (7, 64, 3, 1))
+    cache = gdn.GdnKvCache(odd, odd)
+    want = gdn.gdn_attn_decode(plain, q, table, i32(11))
+    assert torch.equal(gdn.gdn_attn_decode(cache, q, table, i32(11)), want)
+    row = page[:5, :].as_strided((5, 1, 1, 64), (64, 1, 5, 1))  # pages of one token
+    got = gdn.gdn_attn_decode(gdn.GdnKvCache(row, row), q, i32(0, 1, 2, 3, 4).view(1, 5), i32(5))
+    assert torch.equal(got, gdn.gdn_attn_decode(plain, q, table, i32(5)))
