@@ -94,7 +94,9 @@ gdn_status check_attn(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::AttnKi
     if (kind == gdn::kAttnVerify && d->T > GDN_ATTN_MAX_N) return fail(GDN_ERR_SHAPE, "N must be at most 256");
     if (d->H_q < 1 || d->H_q % c->H_kv) return fail(GDN_ERR_SHAPE, "H_q must be a multiple of H_kv, at least 1");
     const int64_t rows = kind == gdn::kAttnDecode ? d->B : kind == gdn::kAttnVerify ? int64_t(d->B) * d->T : d->T;
-    if (rows * d->H_q > INT32_MAX || d->H_q > (1 << 24)) return fail(GDN_ERR_SHAPE, "rows of q times H_q must be at most 2^31 - 1");
+    // (the last tile's rows are numbered in 32 bits as if it were whole)
+    if (rows * d->H_q > INT32_MAX - 255 || d->H_q > (1 << 24))
+        return fail(GDN_ERR_SHAPE, "rows of q times H_q must be at most 2^31 - 256");
     if (!(d->scale >= 0.0f) || !std::isfinite(d->scale)) return fail(GDN_ERR_SHAPE, "scale must be >= 0 and finite");
     if (d->reserved != 0) return fail(GDN_ERR_SHAPE, "reserved must be 0");
     GDN_TRY(check_stride(d->q_stride, 8, "q_stride"));

@@ -106,7 +106,7 @@ gdn_status gdn_kv_append(const gdn_kv_append_dims* dims, const gdn_kv_cache* cac
 typedef struct {
     int32_t B;            /* sequences, at most 65535                                 */
     int32_t T;            /* prefill: rows of q; verify: tree nodes N of a sequence;
-                             decode: ignored.  Rows of q times H_q at most 2^31 - 1   */
+                             decode: ignored.  Rows of q times H_q at most 2^31 - 256 */
     int32_t H_q;          /* query heads, a multiple of H_kv: head h reads key head
                              h / (H_q / H_kv)                                         */
     int32_t max_pages;    /* entries of a row of table; max_pages page_size at most
@@ -177,6 +177,7 @@ typedef struct {
  * (the set bits of anc[b][accepted[b]], in order) move from tokens
  * length[b] + node to tokens length[b], length[b] + 1, ..., in each of
  * `n_caches` caches that differ in k and v only.
+ * No two sequences of a call may share a page that rows move to.
  *   caches     host array
  *   accepted   [B] int32, in [-1, N - 1]; -1 (or outside) moves nothing
  *   new_length [B] int32, written: length[b] + tokens of the path; not length

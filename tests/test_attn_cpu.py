@@ -107,6 +107,15 @@ def test_attention_rejects_sizes(lib, kind):
     assert status(fn(dims(), None, *rest, 1 << 40, None)) == "GDN_ERR_NULL"
 
 
+def test_rows_are_numbered_in_32_bits(lib):
+    """the last tile's 128 rows too"""
+    most = (1 << 31) - 256
+    for T in (most // 8 + 1, (1 << 28) - 1):
+        assert call(lib, "prefill", dims(T=T, H_q=8), cache(), nbytes=1 << 40) == "GDN_ERR_SHAPE"
+        assert need(lib, "prefill", dims(T=T, H_q=8), cache()) == 0
+    assert need(lib, "prefill", dims(T=most // 8, H_q=8), cache()) > 0
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_attention_rejects_pointers(lib, kind):
     odd = dict(q=8, cu_seqlens=2, anc=2, table=2, length=1, gate=1, o=8, seq_status=2)
