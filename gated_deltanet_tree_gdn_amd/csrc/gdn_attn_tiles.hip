@@ -75,9 +75,15 @@ __device__ __forceinline__ void update_acc(f32x16& x, float f, const float (&g)[
 // forms of these make it wait for all of them before any read of LDS; here what
 // has to have arrived is what loads_barrier() waits for.  Nothing else in these
 // kernels uses m0.
+// A vector memory instruction may read a scalar register no sooner than five wait
+// states after a vector instruction wrote it, as one does that brings back a
+// spilled register (v_readlane).  The compiler does not look into a statement, so
+// the statement itself has them: the move and s_nop 3, of which the load's use of
+// m0 needs one.  Two and four loads to a statement, which then share them, are no
+// faster (a prompt of 16384, 16 and 2 heads of 256: 2135 us, 2137 and 2155).
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_to_lds(const i32x4& rsrc, int off, int more, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(rsrc), "s"(more),
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(rsrc), "s"(more),
                  "s"(lds)
                  : "memory");
 }
