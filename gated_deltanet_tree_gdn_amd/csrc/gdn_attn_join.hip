@@ -205,7 +205,7 @@ void attn_shape(AttnArgs& a) {
     const int64_t tiles = (rows + a.tile_rows - 1) / a.tile_rows;
     const int64_t units = (a.kind == kAttnPrefill ? tiles : 1) * a.d.B * a.cache.H_kv * a.head_tiles *
                           ((cap + unit - 1) / unit + 2);
-    a.team = a.kind == kAttnVerify ? int(tiles) : 1;
+    a.team = a.kind == kAttnVerify ? int(std::max<int64_t>(tiles, 1)) : 1;  // no tiles: seq_status only
     a.teams = int(std::max<int64_t>(
         1, std::min<int64_t>(kCu * (one ? decode_per_cu(a.cache.d, a.cache.dtype == GDN_E4M3) : tiles_per_cu(a.cache.d)) / a.team,
                              (units + a.min_units - 1) / a.min_units)));

@@ -1,0 +1,36 @@
+"""The division of the attention calls of gdn_attn.h over workgroups at its ends: sizes of nothing and the largest."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import gated_deltanet_tree_gdn_amd as gdn
+from gated_deltanet_tree_gdn_amd import attn
+from test_attn_cpu import cache, call, dims, need
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(gdn.LIB_PATH):
+        pytest.fail("libgdn_tree.so is not built: run __graft_entry__.build()")
+    return attn.attn_library()
+
+
+@pytest.mark.parametrize("kind", ["prefill", "verify"])
+def test_sequences_without_queries(kind):
+    """nothing is launched where no seq_status is asked for; in a process of its own, which a division by zero would end"""
+    code = f"""
+import sys
+sys.path.insert(0, {os.path.join(ROOT, 'tests')!r})
+from test_attn_cpu import *
+lib = attn.attn_library()
+for H_q in (2, 8, 600):
+    assert need(lib, {kind!r}, dims(T=0, H_q=H_q), cache()) == 0
+    assert call(lib, {kind!r}, dims(T=0, H_q=H_q), cache(), q=None, o=None, anc=None, seq_status=None, workspace=None) == "GDN_OK"
+"""
+    code = code.replace(", anc=None", "") if kind == "prefill" else code
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, f"{r.returncode}: {r.stderr[-600:]}"
