@@ -308,7 +308,9 @@ def gdn_attn_verify(cache, q, anc, table, length, scale=None, gate=None, o=None,
 
 def gdn_attn_workspace_bytes(kind, cache, B, T, H_q, max_pages):
     """Bytes of workspace of a call of ``kind`` "decode", "prefill" or "verify"
-    with B sequences, T rows of q (nodes of a tree) and a table of max_pages."""
+    with B sequences, T rows of q (nodes of a tree) and a table of max_pages.
+    A workspace of that many serves calls with fewer of them too (not one of 0
+    bytes for trees)."""
     _cache(cache)
     need = {"decode": _lib.gdn_attn_decode_workspace_bytes, "prefill": _lib.gdn_attn_prefill_workspace_bytes,
             "verify": _lib.gdn_attn_verify_workspace_bytes}.get(kind)

@@ -118,6 +118,26 @@ size_t workspace_bytes_of(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::At
     return gdn::attn_ws_bytes(a);
 }
 
+// Whether the parts have room in a workspace of `bytes`.  Teams are whole, so the
+// parts of a tree may be a little fewer than those of one with fewer nodes; what a
+// larger tree asks for, which is two thirds or more, serves a smaller one with
+// fewer teams.
+bool attn_fit(gdn::AttnArgs& a, size_t bytes) {
+    const size_t need = gdn::attn_ws_bytes(a);
+    if (bytes >= need) return true;
+    if (a.kind != gdn::kAttnVerify) return false;
+    size_t least = need;
+    gdn::AttnArgs larger = a;
+    while (++larger.d.T <= GDN_ATTN_MAX_N) {
+        gdn::attn_shape(larger);
+        if (const size_t n = gdn::attn_ws_bytes(larger)) least = std::min(least, n);
+    }
+    if (bytes < least) return false;
+    a.teams = int(bytes / (need / a.teams));
+    a.join = a.teams > 1;
+    return true;
+}
+
 gdn_status run(gdn::AttnArgs& a, size_t workspace_bytes, hipStream_t stream, const char* what) {
     const bool prefill = a.kind == gdn::kAttnPrefill;
     if (a.d.B == 0) return fail(GDN_OK, "");
@@ -135,9 +155,8 @@ gdn_status run(gdn::AttnArgs& a, size_t workspace_bytes, hipStream_t stream, con
     }
     gdn::attn_shape(a);
     if (!empty) {
-        const size_t need = gdn::attn_ws_bytes(a);
-        if (need > 0) {
-            if (!a.ws || workspace_bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace missing or smaller than required");
+        if (gdn::attn_ws_bytes(a) > 0) {
+            if (!a.ws || !attn_fit(a, workspace_bytes)) return fail(GDN_ERR_WORKSPACE, "workspace missing or smaller than required");
             GDN_TRY(check_ptr(a.ws, 256, "workspace"));
         }
         hipError_t e = a.kind == gdn::kAttnDecode ? gdn::launch_attn_decode(a, stream) : gdn::launch_attn_tiles(a, stream);

@@ -1,10 +1,8 @@
-// gdn_attn_join.hip -- what the attention kernels share: the sizes of a call's
-// division, the join of tiles whose keys were divided, and the verdict on a
-// call's sequences.
+// gdn_attn_join.hip -- what the attention kernels share: the join of tiles whose
+// keys were divided, and the verdict on a call's sequences.
 
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 
 #include "gdn_attn_internal.h"
@@ -186,35 +184,6 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
-
-void attn_shape(AttnArgs& a) {
-    constexpr int kCu = 256;
-    a.page_shift = __builtin_ctz(a.cache.page_size);
-    a.group = a.d.H_q / a.cache.H_kv;
-    const bool one = a.kind == kAttnDecode;
-    a.tile_rows = one ? kDecodeRows : kTileRows;
-    a.head_tiles = one ? (a.group + kDecodeRows - 1) / kDecodeRows : 1;
-    const int unit = one ? kDecodeUnit : kTilesUnit;
-    a.unit_shift = __builtin_ctz(unit);
-    // of tiles two or more: a part is as large as four tiles of keys, but with few keys longer ranges leave most of the
-    // GPU idle (a tree of 48 nodes behind 2855 tokens: at least 2, 37 us; 3 and 4, 40; 8, 52)
-    a.min_units = one ? 1 : 2;
-    const int64_t cap = int64_t(a.d.max_pages) << a.page_shift, rows = int64_t(a.d.T) * a.group;
-    // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
-    // overlap, where cu_seqlens decreases, and each may then have all rows)
-    const int64_t tiles = (rows + a.tile_rows - 1) / a.tile_rows;
-    const int64_t units = (a.kind == kAttnPrefill ? tiles : 1) * a.d.B * a.cache.H_kv * a.head_tiles *
-                          ((cap + unit - 1) / unit + 2);
-    a.team = a.kind == kAttnVerify ? int(std::max<int64_t>(tiles, 1)) : 1;  // no tiles: seq_status only
-    a.teams = int(std::max<int64_t>(
-        1, std::min<int64_t>(kCu * (one ? decode_per_cu(a.cache.d, a.cache.dtype == GDN_E4M3) : tiles_per_cu(a.cache.d)) / a.team,
-                             (units + a.min_units - 1) / a.min_units)));
-    a.join = a.teams > 1 && cap > unit;  // otherwise a tile is one unit
-}
-
-size_t attn_ws_bytes(const AttnArgs& a) {
-    return a.join ? size_t(2 * a.teams) * a.team * a.tile_rows * (a.cache.d + 2) * sizeof(float) : 0;
-}
 
 hipError_t launch_attn_join(const AttnArgs& a, hipStream_t stream) {
     return a.kind == kAttnDecode   ? launch_join<kAttnDecode>(a, stream)

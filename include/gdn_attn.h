@@ -121,7 +121,11 @@ typedef struct {
 
 /* Bytes of device workspace the calls below need (a multiple of 256; 0 where
  * none is needed or an argument is NULL or out of range).  The workspace
- * holds nothing between calls. */
+ * holds nothing between calls.  One of n > 0 bytes serves every call whose
+ * sizes are not greater (B, max_pages; T) and otherwise the same; for a tree of
+ * fewer nodes than it was asked for, the keys may then be divided into fewer
+ * parts.  Where no workspace is needed for a large tree, one may be for a
+ * smaller. */
 size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_cache* cache);
 size_t gdn_attn_decode_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_cache* cache);
 size_t gdn_attn_verify_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_cache* cache);

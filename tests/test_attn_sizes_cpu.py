@@ -1,5 +1,6 @@
 """The division of the attention calls of gdn_attn.h over workgroups at its ends: sizes of nothing and the largest."""
 import os
+import shutil
 import subprocess
 import sys
 
@@ -34,3 +35,32 @@ for H_q in (2, 8, 600):
     code = code.replace(", anc=None", "") if kind == "prefill" else code
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, f"{r.returncode}: {r.stderr[-600:]}"
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    """The host layer with its own sizing, under sanitizers."""
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not installed")
+    exe = str(tmp_path_factory.mktemp("sizes") / "attn_sizes_driver")
+    csrc = os.path.join(ROOT, "gated_deltanet_tree_gdn_amd", "csrc")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                        "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                        os.path.join(csrc, "gdn_attn_api.cpp"), os.path.join(csrc, "gdn_attn_shape.cpp"),
+                        os.path.join(ROOT, "tests", "sanitize", "attn_sizes_driver.cpp"), "-o", exe],
+                       capture_output=True, text=True)
+    if r.returncode != 0 and "cannot find" in r.stderr and "asan" in r.stderr.lower():
+        pytest.skip("sanitizer runtime not installed")
+    assert r.returncode == 0, r.stderr
+    return exe
+
+
+def run(exe, *args):
+    r = subprocess.run([exe, *args], capture_output=True, text=True, timeout=120,
+                       env=dict(os.environ, UBSAN_OPTIONS="print_stacktrace=1"))
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "runtime error" not in r.stderr and "AddressSanitizer" not in r.stderr, r.stderr
+
+
+def test_the_workspace_of_a_tree_serves_smaller_ones(driver):
+    run(driver)
