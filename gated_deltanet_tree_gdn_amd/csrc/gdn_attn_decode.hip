@@ -257,7 +257,7 @@ hipError_t launch(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((a.teams + 7) / 8 * 8);
+    const dim3 grid(attn_grid(a));
     switch (a.cache.d) {
         case 64: return launch<64>(a, grid, stream);
         case 128: return launch<128>(a, grid, stream);

@@ -77,6 +77,20 @@ constexpr int kDecodeUnit = 128, kTilesUnit = 64;  // keys of a unit
 // Fills the derived members.
 void attn_shape(AttnArgs& a);
 size_t attn_ws_bytes(const AttnArgs& a);
+int attn_grid(const AttnArgs& a);  // workgroups of the attention kernels
+
+// Which of `all` pieces of work, range times team plus place in the team,
+// workgroup `wg` of the grid takes; -1 if none.  Workgroups go to the 8 XCDs in
+// turn; each XCD has neighbouring numbers, which share keys, and as many as the
+// others, so that what fits the GPU fits every XCD.  With whole teams on an XCD
+// some had more than they have room for, or all of a team that is alone: 16 trees
+// of 48 nodes behind 6000 tokens, 16 and 2 heads of 256, 175 us, as here 120; one
+// of 256 behind 20000, 260 heads of 64 to a key head, 3030 us and 660; 8 of 128
+// nodes behind 3000, 50 heads of 128, 220 us and 131.
+__host__ __device__ inline int attn_number(int all, int wg) {
+    const int each = all >> 3, more = all & 7, xcd = wg & 7, at = wg >> 3;
+    return at < each + (xcd < more) ? xcd * each + (xcd < more ? xcd : more) + at : -1;
+}
 
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
 hipError_t launch_kv_commit(const KvCommitArgs& a, int n_caches, hipStream_t stream);

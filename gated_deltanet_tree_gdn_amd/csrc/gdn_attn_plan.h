@@ -201,13 +201,6 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int lane, AttnL
     return p;
 }
 
-// The number of workgroup `wg` of the grid, range times team plus place in the
-// team; -1 if it has no range.  Workgroups go to the 8 XCDs in turn; teams stay
-// on one, and so do neighbouring ranges, which share keys.
-__device__ __forceinline__ int attn_range(const AttnArgs& a, const AttnPlan& plan, int wg) {
-    const int per_xcd = ((plan.ranges + 7) >> 3) * a.team, w = (wg & 7) * per_xcd + (wg >> 3);
-    return wg >> 3 < per_xcd && w < plan.ranges * a.team ? w : -1;
-}
 // A workgroup's range, and the place of its first unit.
 struct AttnRange {
     int w, team, mate;  // its number, its team and its place there
@@ -217,7 +210,7 @@ template <AttnKind KIND>
 __device__ __forceinline__ bool attn_begin(const AttnArgs& a, int wg, int lane, AttnRange& r, AttnPlace& at) {
     AttnLane<KIND> x;
     const AttnPlan plan = attn_plan<KIND>(a, lane, x);
-    r.w = attn_range(a, plan, wg);
+    r.w = attn_number(plan.ranges * a.team, wg);
     if (r.w < 0) return false;
     r.team = a.team == 1 ? r.w : __builtin_amdgcn_readfirstlane(r.w / a.team);
     r.mate = r.w - r.team * a.team;

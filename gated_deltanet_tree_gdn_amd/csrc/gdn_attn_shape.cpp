@@ -37,4 +37,8 @@ size_t attn_ws_bytes(const AttnArgs& a) {
     return a.join ? size_t(2 * a.teams) * a.team * a.tile_rows * (a.cache.d + 2) * sizeof(float) : 0;
 }
 
+// At most 2^24 - 1: several teams are 512 workgroups or fewer, and one has a place for every 128 rows of a sequence, which
+// are fewer than 2^31.
+int attn_grid(const AttnArgs& a) { return a.teams * a.team; }
+
 }  // namespace gdn

@@ -685,7 +685,7 @@ hipError_t launch_one(const AttnArgs& a, const dim3& grid, hipStream_t stream) {
 
 template <AttnKind KIND>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((a.teams + 7) / 8 * 8 * a.team);
+    const dim3 grid(attn_grid(a));
     const bool f8 = a.cache.dtype == GDN_E4M3;
     switch (a.cache.d) {
         case 64: return f8 ? launch_one<KIND, 64, true>(a, grid, stream) : launch_one<KIND, 64, false>(a, grid, stream);

@@ -63,4 +63,12 @@ def run(exe, *args):
 
 
 def test_the_workspace_of_a_tree_serves_smaller_ones(driver):
-    run(driver)
+    run(driver, "trees")
+
+
+def test_the_largest_sizes_that_pass_the_checks(driver):
+    run(driver, "largest")
+
+
+def test_workgroups_are_spread_evenly(driver):
+    run(driver, "numbers")
