@@ -292,7 +292,8 @@ __device__ __forceinline__ void rewrite(uint32_t v, int kind, int tid) {
 //   O^T += V^T P   V read transposed; the lanes hold P where the product wants it
 // The running maximum is raised only where a row's scores pass it by more than
 // 2^8: P then stays below 2^8, which costs no precision in floating point, and
-// O is rarely rescaled.  P is rounded to bf16 for the product, at most 2^-8 of a
+// O is rarely rescaled (by rows: what a wavefront's other rows see has no part in
+// a row's rounding).  P is rounded to bf16 for the product, at most 2^-8 of a
 // weight, as much as the output's own rounding; the sum is that of the rounded
 // weights.
 // A masked key has P = 0, but 0 times an infinity or NaN of its value would not
@@ -385,7 +386,7 @@ __global__ __launch_bounds__(kThreads, tiles_per_cu(D)) void tiles_kernel(AttnAr
         };
         auto raise = [&](float top) {
             if (__ballot(top > m + 8.0f)) {
-                const float m_new = fmaxf(m, top), keep = exp2_fast(m - finite_max(m_new));
+                const float m_new = top > m + 8.0f ? top : m, keep = exp2_fast(m - finite_max(m_new));
                 const bool some = __ballot(m != -inf) != 0;  // that is not zero
                 m = m_new;
                 if (!some) return;

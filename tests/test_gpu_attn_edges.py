@@ -4,8 +4,9 @@ import pytest
 torch = pytest.importorskip("torch")
 gdn = pytest.importorskip("gated_deltanet_tree_gdn_amd")
 
-from attn_cases import BF16, Paged, ancestors, i32, random_tree  # noqa: E402
-from test_gpu_attn import check_verify  # noqa: E402
+from attn_cases import (BF16, E4M3, HALF, Paged, ancestors, attend, bits_of, close, generator, i32, randn,  # noqa: E402
+                        random_tree, tolerance)
+from test_gpu_attn import TWO, causal, check_verify  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,45 @@ def test_a_workspace_for_the_largest_tree_serves_smaller_ones(d, group):
         masks = [ancestors(random_tree(N, N + b))[1] for b in range(len(prefix))]
         check_verify(p, prefix, masks, H * group, N, workspace=ws[:nbytes])
         assert (ws[nbytes:] == 93).all()
+
+
+def one_sequence(kind, p, H_q, seed=1):
+    """A call of `kind` on p's only sequence: (queries, the mask of what they see, what makes the call, its weights)"""
+    d, keys = p.k.shape[3], p.counts[0]
+    n = {"decode": 1, "prefill": 100, "verify": 45}[kind]
+    q = randn(generator(seed), n, H_q, d).to(BF16)
+    if kind == "decode":
+        return q, torch.ones(1, keys, dtype=torch.bool), lambda st=None: gdn.gdn_attn_decode(
+            p.cache(), q, p.table, i32(keys), seq_status=st), TWO
+    if kind == "prefill":
+        return q, causal(n, keys), lambda st=None: gdn.gdn_attn_prefill(
+            p.cache(), q, i32(0, n), p.table, i32(keys), seq_status=st), HALF
+    tree = ancestors(random_tree(n, seed))[1]
+    mask = torch.cat([torch.ones(n, keys - n, dtype=torch.bool), tree], 1)
+    bits = bits_of(tree).cuda()[None]
+    return q, mask, lambda st=None: gdn.gdn_attn_verify(p.cache(), q[None], bits, p.table, i32(keys - n), seq_status=st)[0], HALF
+
+
+def spoil(p, pool, token, head, element, bad):
+    x = p.get(pool, 0, torch.tensor([token]))
+    x[:, head, element] = bad
+    p.put(pool, 0, torch.tensor([token]), x)
+
+
+@pytest.mark.parametrize("kind", ["prefill", "verify"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("size", [30.0, float("inf")])
+def test_large_scores_of_other_rows_leave_no_trace(kind, d, page, size):
+    """rows of a tile that do not see a key are the same to the last bit, however large its scores are for their neighbours"""
+    H, group = 2, 3
+    p = Paged([300], H, d, page)
+    q, mask, run, _ = one_sequence(kind, p, H * group)
+    clean = run()
+    for token in (262, 285):
+        spoil(p, p.k, token, slice(None), slice(None), size)
+        sees = mask[:, token].cuda()
+        got = run()
+        assert sees.any() and (~sees).any()
+        mine = ~(mask[:, 262].cuda() | sees)
+        assert torch.equal(got[mine], clean[mine]) and not torch.equal(got, clean)
