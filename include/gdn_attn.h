@@ -26,11 +26,17 @@
  *  - Keys and values that a query may not see (behind its sequence's end, on
  *    other branches of a tree, later in a prompt) have no influence on its
  *    output, whatever they hold, infinities and NaN included.
- *    Those that it sees and that are not finite make what they reach infinite
- *    or NaN.
+ *    Of those that it sees, a score of NaN or +infinity makes the query's
+ *    output NaN, one of -infinity is a weight of zero (a query that sees no
+ *    other gets zero, too), and a value that is not finite makes its element
+ *    of the output infinite or NaN.
  *  - A workspace is one call's until that call has run: calls that may overlap
  *    (on two streams, or graphs replayed at once) need one each.
  *  - Scores, maxima and sums of the softmax and all accumulations are fp32.
+ *    For the product with the values a weight is rounded: to two bf16 (16 bits
+ *    together) by gdn_attn_decode, to one (off by 2^-8 of the weight at most)
+ *    by gdn_attn_prefill and gdn_attn_verify, where the sum is that of the
+ *    rounded weights.
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H

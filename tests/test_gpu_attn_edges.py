@@ -85,3 +85,87 @@ def test_large_scores_of_other_rows_leave_no_trace(kind, d, page, size):
         assert sees.any() and (~sees).any()
         mine = ~(mask[:, 262].cuda() | sees)
         assert torch.equal(got[mine], clean[mine]) and not torch.equal(got, clean)
+
+
+NOT_FINITE = [(BF16, float("nan")), (BF16, float("inf")), (BF16, float("-inf")), (E4M3, float("nan"))]
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill", "verify"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("dtype,bad", NOT_FINITE)
+@pytest.mark.parametrize("token", [20, 285])  # among what all queries see, and among what some see
+def test_a_key_that_is_not_finite(kind, d, page, dtype, bad, token):
+    """scores of NaN and +inf make a row NaN, one of -inf is a weight of zero, whoever does not see the key has no trace of it"""
+    H, group, element = 2, 3, 5
+    p = Paged([300], H, d, page, dtype)
+    q, mask, run, weights = one_sequence(kind, p, H * group)
+    clean = run()
+    spoil(p, p.k, token, 1, element, bad)
+    got = run()
+    assert torch.equal(got[:, :group], clean[:, :group])
+    sees = mask[:, token].cuda()
+    assert torch.equal(got[~sees], clean[~sees]) and sees.any()
+    score = q[:, group:, element].float() * bad
+    gone = sees[:, None] & (score == -float("inf"))
+    lost = sees[:, None] & ~gone
+    assert got[:, group:][lost].isnan().all() and lost.any() and (gone.any() or bad != bad)
+    if gone.any():
+        without = mask.clone()
+        without[:, token] = False
+        ref = attend(q, p.real["k"][0], p.real["v"][0], without.cuda(), d ** -0.5)
+        tol = tolerance(*ref, d, weights)
+        close(got[:, group:][gone], ref[0][:, group:][gone], tol[:, group:][gone])
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill", "verify"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("dtype,bad", NOT_FINITE)
+@pytest.mark.parametrize("token", [20, 285])
+def test_a_value_that_is_not_finite(kind, d, page, dtype, bad, token):
+    """makes that element of who sees it infinite or NaN, and nothing else"""
+    H, group, element = 2, 3, 5
+    p = Paged([300], H, d, page, dtype)
+    q, mask, run, _ = one_sequence(kind, p, H * group)
+    clean = run()
+    spoil(p, p.v, token, 1, element, bad)
+    got = run()
+    sees = mask[:, token].cuda()
+    hit = got[sees][:, group:, element]
+    assert not hit.isfinite().any() and hit.numel()
+    if bad != bad:
+        assert hit.isnan().all()
+    got[sees.nonzero(), torch.arange(group, 2 * group, device="cuda"), element] = clean[
+        sees.nonzero(), torch.arange(group, 2 * group, device="cuda"), element]
+    assert torch.equal(got, clean)
+
+
+def test_only_keys_with_scores_of_minus_infinity():
+    """weights of zero: as if nothing were visible"""
+    p = Paged([3], 1, 64)
+    q = torch.ones(1, 2, 64, dtype=BF16, device="cuda")
+    for t in range(3):
+        spoil(p, p.k, t, 0, 7, -float("inf"))
+    assert (gdn.gdn_attn_decode(p.cache(), q, p.table, i32(3)) == 0).all()
+    assert (gdn.gdn_attn_prefill(p.cache(), q, i32(0, 1), p.table, i32(3)) == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill", "verify"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page", [1, 8, 16, 64])
+def test_pages_outside_the_pool(kind, d, dtype, page):
+    """keys there are left out: among those before a tree, in it, and the last"""
+    H, group, keys = 2, 3, 330
+    p = Paged([keys], H, d, page, dtype)
+    q, mask, run, weights = one_sequence(kind, p, H * group)
+    gone = sorted({t // page for t in (3, 140, 141, 290, 300, keys - 1)})
+    for i, g in enumerate(gone):
+        p.table[0, g] = (-1, p.k.shape[0], 2 ** 31 - 1, -2 ** 31)[i % 4]
+    mask[:, [t for t in range(keys) if t // page in gone]] = False
+    st = i32(9)
+    got = run(st)
+    ref = attend(q, p.real["k"][0], p.real["v"][0], mask.cuda(), d ** -0.5)
+    close(got, ref[0], tolerance(*ref, d, weights))
+    assert st.tolist() == [2]
