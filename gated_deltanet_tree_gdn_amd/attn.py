@@ -321,7 +321,7 @@ def gdn_attn_workspace_bytes(kind, cache, B, T, H_q, max_pages):
 
 def gdn_kv_commit(caches, anc, accepted, table, length, new_length=None, seq_status=None, stream=None):
     """After a tree's verify: in all of ``caches`` (a GdnKvCache, or a list of
-    equal ones) the keys and values of the path to node accepted[b] move to
+    equal ones; layers may share one) the keys and values of the path to node accepted[b] move to
     tokens length[b], length[b] + 1, ...; -1 moves nothing.  Returns
     new_length [B] int32: length[b] + tokens of the path."""
     caches = [caches] if isinstance(caches, GdnKvCache) else list(caches)

@@ -300,10 +300,14 @@ gdn_status gdn_kv_commit(const gdn_kv_commit_dims* dims, const gdn_kv_cache* cac
     if (new_length == length) return fail(GDN_ERR_SHAPE, "new_length may not be length");
     for (int first = 0; first < n_caches; first += gdn::kCommitCaches) {
         const int n = std::min(n_caches - first, gdn::kCommitCaches);
-        gdn::KvCommitArgs a{d, *caches, {}, {}, anc, accepted, table, length, first ? nullptr : new_length, seq_status};
+        gdn::KvCommitArgs a{d, *caches, {}, {}, 0, 0, anc, accepted, table, length, first ? nullptr : new_length, seq_status};
         for (int i = 0; i < n; ++i) {
             a.k[i] = caches[first + i].k;
             a.v[i] = caches[first + i].v;
+            for (int j = 0; j < first + i; ++j) {
+                if (caches[j].k == a.k[i]) a.k_moved |= 1u << i;
+                if (caches[j].v == a.v[i]) a.v_moved |= 1u << i;
+            }
         }
         const hipError_t e = gdn::launch_kv_commit(a, n, stream);
         if (e != hipSuccess) return done(e, "kv_commit");

@@ -32,6 +32,7 @@ struct KvCommitArgs {
     gdn_kv_cache cache;  // k and v as in the arrays
     void* k[kCommitCaches];
     void* v[kCommitCaches];
+    uint32_t k_moved, v_moved;  // bits of caches whose k or v an earlier one has, too
     const uint32_t* anc;
     const int32_t* accepted;
     const int32_t* table;

@@ -243,7 +243,9 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(KvCommitArgs a, int pa
 
     const int size = a.cache.dtype == GDN_BF16 ? 2 : 1;
     const int pieces = a.cache.d * size / 16, per_side = a.cache.H_kv * pieces;
-    for (int i = tid; i < 2 * per_side; i += kThreads) {
+    // what is listed twice moves once: a path's rows that have moved are not where they were
+    const int begin = a.k_moved >> c & 1 ? per_side : 0, end = a.v_moved >> c & 1 ? per_side : 2 * per_side;
+    for (int i = begin + tid; i < end; i += kThreads) {
         const bool is_v = i >= per_side;
         const int at = is_v ? i - per_side : i;
         const int64_t page_stride = (is_v ? a.cache.v_page_stride : a.cache.k_page_stride) * size;

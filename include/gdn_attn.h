@@ -188,7 +188,7 @@ typedef struct {
  * length[b] + node to tokens length[b], length[b] + 1, ..., in each of
  * `n_caches` caches that differ in k and v only.
  * No two sequences of a call may share a page that rows move to.
- *   caches     host array
+ *   caches     host array; k or v of an earlier one in it moves once
  *   accepted   [B] int32, in [-1, N - 1]; -1 (or outside) moves nothing
  *   new_length [B] int32, written: length[b] + tokens of the path; not length
  *   seq_status [B] int32, written, or NULL: 0, GDN_ERR_ACCEPT for an accepted

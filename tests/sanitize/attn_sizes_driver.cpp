@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdio>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "gdn_attn_internal.h"
@@ -26,7 +27,11 @@ static void check(bool fine, const char* what, long long a = 0, long long b = 0,
 namespace gdn {
 void set_last_error(const std::string& msg) { last_error = msg; }
 hipError_t launch_kv_append(const KvAppendArgs&, hipStream_t) { return hipSuccess; }
-hipError_t launch_kv_commit(const KvCommitArgs&, int, hipStream_t) { return hipSuccess; }
+static std::vector<std::pair<void*, void*>> moved;  // what the launches move, null where they do not
+hipError_t launch_kv_commit(const KvCommitArgs& a, int n, hipStream_t) {
+    for (int i = 0; i < n; ++i) moved.push_back({a.k_moved >> i & 1 ? nullptr : a.k[i], a.v_moved >> i & 1 ? nullptr : a.v[i]});
+    return ++launches, hipSuccess;
+}
 static hipError_t look(const AttnArgs& a) {
     ++launches;
     check(a.teams >= 1 && a.team >= 1 && a.min_units >= 1, "empty division", a.teams, a.team);
@@ -123,10 +128,27 @@ static void numbers() {
     launches = 1;
 }
 
+// Of caches that are listed more than once the first moves, in all launches of a call.
+static void shared() {
+    unsigned char* at = mem;
+    int32_t* i = reinterpret_cast<int32_t*>(mem);
+    const gdn_kv_cache c{at, at + 16, nullptr, nullptr, 10, 16, 2, 64, GDN_BF16, 0, 2048, 128, 64, 2048, 128, 64};
+    std::vector<gdn_kv_cache> all(100, c);
+    for (int n = 0; n < 100; ++n) all[n].k = at + 16 * (n % 37), all[n].v = at + 4096 + 16 * (n % 41);
+    const gdn_kv_commit_dims m{3, 20, 40, 0, 40};
+    check(gdn_kv_commit(&m, all.data(), 100, reinterpret_cast<uint32_t*>(mem), i, i, i, i + 1, nullptr, nullptr) == GDN_OK, "commit");
+    check(gdn::moved.size() == 100, "caches", gdn::moved.size());
+    for (int n = 0; n < 100; ++n) {
+        check(gdn::moved[n].first == (n < 37 ? all[n].k : nullptr), "k", n);
+        check(gdn::moved[n].second == (n < 41 ? all[n].v : nullptr), "v", n);
+    }
+}
+
 int main(int argc, char** argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "trees") smaller_trees();
     if (what == "largest") largest();
+    if (what == "shared") shared();
     if (what == "numbers") numbers();
     if (bad) std::printf("%d failures\n", bad);
     std::printf("%d launches, %d joins\n", launches, joins);

@@ -72,3 +72,7 @@ def test_the_largest_sizes_that_pass_the_checks(driver):
 
 def test_workgroups_are_spread_evenly(driver):
     run(driver, "numbers")
+
+
+def test_a_cache_that_is_listed_twice_moves_once(driver):
+    run(driver, "shared")

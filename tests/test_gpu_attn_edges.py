@@ -169,3 +169,29 @@ def test_pages_outside_the_pool(kind, d, dtype, page):
     ref = attend(q, p.real["k"][0], p.real["v"][0], mask.cuda(), d ** -0.5)
     close(got, ref[0], tolerance(*ref, d, weights))
     assert st.tolist() == [2]
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_commit_of_layers_that_share_a_cache(dtype):
+    """the path moves once, also where the cache is in two launches of the call, or keys alone are shared"""
+    N, lengths = 60, [30, 7]
+    anc = torch.zeros(2, N, 2, dtype=torch.int32)
+    anc[:, N - 1] = bits_of(torch.arange(N).expand(N, N) % 3 == 2)[0]  # nodes 2, 5, 8, ... 59
+    anc = anc.cuda()
+    accepted, length = i32(N - 1, N - 1), i32(*lengths)
+    ps = [Paged([n + N for n in lengths], 2, 64, dtype=dtype, seed=s) for s in (1, 1, 2, 2)]
+    single, shared = ps[0::2], ps[1::2]
+    for p in ps[1:]:
+        p.table.copy_(ps[0].table)
+    for a, b in zip(single, shared):
+        for x in "kv":
+            getattr(b, x).view(torch.uint8).copy_(getattr(a, x).view(torch.uint8))
+    gdn.gdn_kv_commit([p.cache() for p in single], anc, accepted, single[0].table, length)
+    first, second = (p.cache() for p in shared)
+    keys_only = gdn.GdnKvCache(shared[0].k, shared[1].v, shared[0].k_scale, shared[0].v_scale)
+    many = [first] * 3 + [keys_only] + [second] * 40 + [first, keys_only]
+    new = gdn.gdn_kv_commit(many, anc, accepted, shared[0].table, length)
+    assert new.tolist() == [n + N // 3 for n in lengths]
+    for a, b in zip(single, shared):
+        for x in "kv":
+            assert torch.equal(getattr(a, x).view(torch.uint8), getattr(b, x).view(torch.uint8))
