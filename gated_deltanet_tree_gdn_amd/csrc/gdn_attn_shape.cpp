@@ -24,7 +24,8 @@ void attn_shape(AttnArgs& a) {
     // what the kernels' registers leave room for at once, and not more than there is work for (prompts may
     // overlap, where cu_seqlens decreases, and each may then have all rows)
     const int64_t tiles = (rows + a.tile_rows - 1) / a.tile_rows;
-    const int64_t units = (a.kind == kAttnPrefill ? tiles : 1) * a.d.B * a.cache.H_kv * a.head_tiles *
+    auto few = [](int64_t n) { return std::min<int64_t>(n, 1 << 20); };  // enough for all workgroups; the products stay below 2^63
+    const int64_t units = few(few((a.kind == kAttnPrefill ? tiles : 1) * a.d.B) * a.cache.H_kv * a.head_tiles) *
                           ((cap + unit - 1) / unit + 2);
     a.team = a.kind == kAttnVerify ? int(std::max<int64_t>(tiles, 1)) : 1;  // no tiles: seq_status only
     a.teams = int(std::max<int64_t>(

@@ -105,6 +105,25 @@ static void largest() {
                 const size_t need = gdn_attn_verify_workspace_bytes(&v, &c);
                 check(verify(v, c, need) == GDN_OK, "largest tree", B, T, heads);
             }
+    // work for every workgroup that there is room for: two parts each
+    void *p = mem, *o = mem + 4096;
+    int32_t* i = reinterpret_cast<int32_t*>(mem);
+    for (int d : {64, 128, 256})
+        for (int heads : {1, 8, 65535})
+            for (int group : {1, 16, 100}) {
+                if (int64_t(heads) * group > 1 << 24) continue;
+                const gdn_kv_cache c{mem, mem, nullptr, nullptr, 10, 16, heads, d, GDN_BF16, 0, 16 * d, d, d, 16 * d, d, d};
+                gdn_attn_dims a{65535, most / (heads * group), heads * group, 1 << 26, 0.1f, 0, 0, 0, 0, 0};
+                const int wide = d == 256 ? 256 : 512, one = d == 64 ? 768 : wide;
+                given = gdn_attn_prefill_workspace_bytes(&a, &c);
+                check(given == size_t(2) * wide * 128 * (d + 2) * 4, "workspace of prompts", d, heads, group);
+                check(gdn_attn_prefill(&a, &c, p, i, i, i, nullptr, o, nullptr, p, given, nullptr) == GDN_OK, "prompts", d, heads, group);
+                a.B = std::min(65535, most / (heads * group));
+                given = gdn_attn_decode_workspace_bytes(&a, &c);
+                check(given == size_t(2) * one * 16 * (d + 2) * 4, "workspace of tokens", d, heads, group);
+                a.T = -1;
+                check(gdn_attn_decode(&a, &c, p, i, i, nullptr, o, nullptr, p, given, nullptr) == GDN_OK, "tokens", d, heads, group);
+            }
 }
 
 // Every number has one workgroup, in grids of that many and more, and no XCD more than an eighth, rounded up.
