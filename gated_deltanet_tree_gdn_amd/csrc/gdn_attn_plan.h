@@ -11,7 +11,8 @@
 // parts 2 w and 2 w + 1 of the workspace and are joined by another launch.
 //
 // In a prompt the last tile sees most keys and the first fewest, so tiles are
-// taken in pairs from both ends, and every pair counts the same.  The tiles of a
+// taken in pairs from both ends, and every pair counts the same (the middle one of
+// an odd number, too, whose second half is empty).  The tiles of a
 // tree all see the same keys: a team of as many workgroups takes them side by
 // side, as one unit, so that the keys come from memory once.
 #pragma once
