@@ -126,6 +126,29 @@ static void largest() {
             }
 }
 
+// What a call of some sizes asks for serves calls of fewer sequences, pages and rows.
+static void smaller_calls() {
+    void *p = mem, *o = mem + 4096;
+    int32_t* i = reinterpret_cast<int32_t*>(mem);
+    const int sizes[][3] = {{1, 1, 1}, {1, 9, 7}, {2, 40, 33}, {3, 40, 128}, {17, 300, 160}, {200, 300, 200}, {200, 5000, 256}};  // B, pages, T
+    for (int d : {64, 128, 256})
+        for (int group : {1, 5, 64})
+            for (int dtype : {int(GDN_BF16), int(GDN_E4M3)})
+                for (const auto& large : sizes)
+                    for (const auto& small : sizes) {
+                        if (small[0] > large[0] || small[1] > large[1] || small[2] > large[2]) continue;
+                        const gdn_kv_cache c{mem, mem, nullptr, nullptr, 10, 16, 2, d, dtype, 0, 32 * d, 2 * d, d, 32 * d, 2 * d, d};
+                        const gdn_attn_dims a{large[0], large[2], 2 * group, large[1], 0.1f, 0, 2 * group * d, 0, 0, large[1]};
+                        const gdn_attn_dims b{small[0], small[2], 2 * group, small[1], 0.1f, 0, 2 * group * d, 0, 0, small[1]};
+                        given = gdn_attn_decode_workspace_bytes(&a, &c);
+                        check(gdn_attn_decode(&b, &c, p, i, i, nullptr, o, nullptr, p, given, nullptr) == GDN_OK, "decode", large[0], small[0]);
+                        given = gdn_attn_prefill_workspace_bytes(&a, &c);
+                        check(gdn_attn_prefill(&b, &c, p, i, i, i, nullptr, o, nullptr, p, given, nullptr) == GDN_OK, "prefill", large[0], small[0]);
+                        given = gdn_attn_verify_workspace_bytes(&a, &c);
+                        check(given == 0 || verify(b, c, given) == GDN_OK, "verify", large[0], small[0], group);
+                    }
+}
+
 // Every number has one workgroup, in grids of that many and more, and no XCD more than an eighth, rounded up.
 static void numbers() {
     for (int all = 0; all < 1100; ++all)
@@ -166,6 +189,7 @@ static void shared() {
 int main(int argc, char** argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "trees") smaller_trees();
+    if (what == "calls") smaller_calls();
     if (what == "largest") largest();
     if (what == "shared") shared();
     if (what == "numbers") numbers();

@@ -66,6 +66,10 @@ def test_the_workspace_of_a_tree_serves_smaller_ones(driver):
     run(driver, "trees")
 
 
+def test_the_workspace_of_a_call_serves_smaller_ones(driver):
+    run(driver, "calls")
+
+
 def test_the_largest_sizes_that_pass_the_checks(driver):
     run(driver, "largest")
 
